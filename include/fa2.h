@@ -343,12 +343,172 @@ int fa2_step_from_host(const void* q, const void* k, const void* v, const void* 
                        const int* group_heads, int num_groups, int compute_streams, void* workspace,
                        size_t workspace_bytes, void* stream);
 
+/*
+ * Norm of queries and keys for each head, with the position rotation in the
+ * same pass: what a layer does to q and k before fa2_fwd and its kin.  For a
+ * row x of d values (one head of one token), gain w and r = 1 / sqrt(mean
+ * x^2 + eps): y_i = x_i r w_i; then the first rot_dim columns are rotated in
+ * pairs (a, b) = (i, i + rot_dim/2), or (2i, 2i + 1) if `interleaved`,
+ * i < rot_dim/2, by the token's angle for i:
+ *   out_a = y_a cos - y_b sin,  out_b = y_b cos + y_a sin;
+ * the other columns are y.
+ *   q, q_out  [B, H, N, d], k, k_out [B, H_kv, N, d], bf16
+ *   strides   host array of 4 x 3 element strides {batch, head, token} for q,
+ *             k, q_out, k_out (the last dimension is contiguous; multiples of
+ *             8; the stride of a dimension of size 1 is not looked at), or
+ *             NULL: all contiguous.  A packed batch [total, heads, d] is
+ *             B = 1, N = total.  Views of one fused projection are fine.
+ *   q_weight, k_weight   gains [d], fp32 if weight_fp32 != 0, else bf16;
+ *             NULL: ones
+ *   rope      fp32 [max_positions, rot_dim], 16-byte aligned: each row the
+ *             rot_dim/2 cosines, then the sines.  rot_dim: a multiple of 16,
+ *             0 (no rotation; rope may be NULL) to d
+ *   positions DEVICE int32 [B, N], or NULL: token n is at position n.  A row
+ *             whose position is outside [0, max_positions) is not written and
+ *             the device status word becomes 5.
+ *   eps       finite and > 0 (FA2_ERR_SCALE)
+ * q_out may be q, and k_out k, with the same strides (in place); outputs may
+ * be heads of one token-major buffer; any other overlap is FA2_ERR_ALIAS.
+ * H must be a multiple of H_kv.  N = 0 is allowed and does nothing.  One
+ * launch.
+ */
+int fa2_qk_norm_rope(const void* q, const void* k, const void* q_weight, const void* k_weight, int weight_fp32,
+                     const float* rope, const int* positions, void* q_out, void* k_out, int B, int H, int H_kv, int N,
+                     int d, int rot_dim, int interleaved, int max_positions, float eps, const long long* strides,
+                     void* stream);
+
+/*
+ * Its gradient: dq_out, dk_out are the gradients of q_out, k_out (fa2_bwd's
+ * dq and dk); q, k the inputs of the forward call.  Writes dq, dk (bf16) and,
+ * where not NULL, dq_weight, dk_weight (fp32 [d], sums over every row, added
+ * in a fixed order: run-to-run the same bits).  strides: 6 x 3 for dq_out,
+ * dk_out, q, k, dq, dk; dq may be dq_out or q with the same strides, dk
+ * likewise.  Rows at a position out of range are not written and add nothing.
+ * workspace: 256-byte aligned, fa2_qk_norm_rope_bwd_workspace_bytes(d) bytes
+ * (0 for an invalid d); needed only where a gain's gradient is wanted.  Two
+ * launches then, one otherwise.  N = 0 zeroes the gains' gradients.
+ */
+size_t fa2_qk_norm_rope_bwd_workspace_bytes(int d);
+int fa2_qk_norm_rope_bwd(const void* dq_out, const void* dk_out, const void* q, const void* k, const void* q_weight,
+                         const void* k_weight, int weight_fp32, const float* rope, const int* positions, void* dq,
+                         void* dk, float* dq_weight, float* dk_weight, int B, int H, int H_kv, int N, int d,
+                         int rot_dim, int interleaved, int max_positions, float eps, const long long* strides,
+                         void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Block tables and slot maps of a paged key-value cache, built on the GPU
+ * from request lengths (all arrays are DEVICE arrays).  Request b has
+ * cached_lens[b] tokens in the cache and new_lens[b] new ones; pages hold
+ * page_size (16, 32, 64 or 128) tokens.  The pages its new tokens need are
+ * taken from free_pages in request order and written behind the ones its row
+ * of block_table [B, table_width] (row stride table_stride) has.  Writes
+ *   lens [B]            cached + new tokens
+ *   cu_new [B + 1]      offsets of the packed new tokens (cu_seqlens_q)
+ *   cu_total [B + 1]    offsets of all tokens (cu_seqlens_k, fa2_kv4_gather)
+ *   slots, positions    [max_tokens] of each packed new token: its cache slot
+ *                       page * page_size + offset and its position in the
+ *                       request; behind the last token -1 and 0
+ *   pages_needed [1]    free pages taken
+ * Where the free list is too short (pages_needed > num_free) the entries
+ * without a page, and the slots in them, are -1: the caller compares before
+ * it uses the step.  A request with a negative length, or with more tokens
+ * than its table row has room for, counts as empty (its row is left as it
+ * is) and the device status word becomes 3, as it does where there are more
+ * new tokens than max_tokens (those behind are left out) or more than 2^31 -
+ * 1 tokens (every request then counts as empty).  1 <= B <= 16384.  One
+ * launch; nothing is read on the host, so a captured step may be replayed
+ * with other lengths.
+ */
+int fa2_page_plan(const int* cached_lens, const int* new_lens, const int* free_pages, int* block_table, int* lens,
+                  int* cu_new, int* cu_total, long long* slots, int* positions, int* pages_needed, int B, int num_free,
+                  int table_width, long long table_stride, int page_size, int max_tokens, void* stream);
+
+/*
+ * A paged key-value cache held in 4 bits: keys and values as e2m1 codes (0,
+ * 0.5, 1, 1.5, 2, 3, 4, 6 with a sign) with one e4m3 scale per 16 columns of
+ * a token's head, times k_scale or v_scale, a power of two from 2^-64 to 2^64
+ * (FA2_ERR_SCALE otherwise) that moves the range and must be the same for
+ * every call on one cache: 4.5 bits a value.  Every value that can be stored
+ * is exact in bf16.  The cache is one device buffer [num_pages, H_kv,
+ * page_size / 16, 18 d] bytes, 16-byte aligned, pages page_stride bytes apart
+ * (a multiple of 16, at least fa2_kv4_page_bytes; more where the pages of
+ * several layers alternate).  18 d bytes hold 16 tokens of one head:
+ *   bytes 0 .. 8d     K codes [key 16][d / 2], the even column in the low half
+ *   bytes 8d .. 16d   V codes [t 2][g 8][c 4][p 2][d / 16]: columns g d/8 .. of
+ *                     key 8 t + 2 c + p
+ *   bytes 16d .. 17d  K scales [key mod 8][column / 16][key / 8]
+ *   bytes 17d .. 18d  V scales [column / 16][c 4][t 2][p 2]
+ * page_size is 16, 32, 64 or 128; d as everywhere 16, 32, 64 or 128.
+ * fa2_kv4_page_bytes: bytes of a page (0 for invalid sizes).
+ */
+size_t fa2_kv4_page_bytes(int H_kv, int page_size, int d);
+
+/*
+ * Write num_tokens keys and values, k, v [num_tokens, H_kv, d] bf16, to their
+ * slots (DEVICE int64, as fa2_page_plan makes them).  strides: host array of 2
+ * x 2 element strides {token, head} for k and v (multiples of 8), or NULL:
+ * contiguous.  A group's scale is e4m3(max |x| / (6 k_scale)), a code the
+ * nearest of x / (k_scale scale), ties to even; both saturate (infinities
+ * become the largest value), a group whose scale rounds to zero is stored as
+ * zeros and one that holds a NaN as NaN.  k_out, v_out (bf16 [num_tokens,
+ * H_kv, d], or NULL) receive the values as stored: attention over them sees
+ * what attention over the cache will.  A slot < 0 is a padding token (not
+ * stored), one past the last page is not stored either and the device status
+ * word becomes 5.  Slots must differ from one another: a slot that is named
+ * twice holds a mixture of its tokens (nothing else is touched).  One launch.
+ */
+int fa2_kv4_append(const void* k, const void* v, const long long* strides, void* cache, long long page_stride,
+                   const long long* slots, void* k_out, void* v_out, int num_tokens, int H_kv, int num_pages,
+                   int page_size, int d, float k_scale, float v_scale, void* stream);
+
+/*
+ * Read the cache back: k, v [total, H_kv, d] bf16, packed by cu_seqlens
+ * (DEVICE int32 [B + 1]; fa2_page_plan's cu_total), the form fa2_fwd_varlen
+ * takes.  For prompts and prompt chunks: many queries against a history are
+ * faster through fa2_fwd_varlen on the gathered cache than through
+ * fa2_kv4_attn, which is made for few.  Rows outside every sequence are not
+ * written; rows of a sequence that its table row has no room for (status word
+ * 3) or whose page id is outside [0, num_pages) (status word 5) neither.  One
+ * launch.
+ */
+int fa2_kv4_gather(const void* cache, long long page_stride, const int* block_table, long long table_stride,
+                   const int* cu_seqlens, void* k, void* v, int B, int H_kv, int total, int num_pages, int page_size,
+                   int table_width, int d, float k_scale, float v_scale, void* stream);
+
+/*
+ * Attention of new query tokens over the 4-bit cache.  q, o: packed
+ * [total_q, H, d] bf16, lse: fp32 [H, total_q], as in fa2_fwd_varlen; request
+ * b owns the query rows cu_seqlens_q[b] .. cu_seqlens_q[b+1] - 1 (DEVICE
+ * int32 [B + 1], at most max_seqlen_q each; or NULL: every request has
+ * max_seqlen_q rows, total_q = B * max_seqlen_q) and the first lens[b] tokens
+ * of its pages, block_table [B, table_width] (DEVICE int32, row stride
+ * table_stride).  Query head h reads key/value head h / (H / H_kv).  With
+ * causal != 0 a request's Lq queries are its last positions: query i sees key
+ * j iff j <= i + Lk - Lq; a query that sees no key gets o = 0 and lse = -inf.
+ * Rows outside every request are not written.  What the pages hold past a
+ * request's length has no influence, not even a NaN.
+ * A request whose lengths are out of range (negative, more tokens than its
+ * table row has room for, query rows outside [0, total_q] or more than
+ * max_seqlen_q) is skipped and the device status word becomes 3; a page id
+ * outside [0, num_pages) leaves its keys out and sets 5.
+ * workspace: 256-byte aligned, fa2_kv4_attn_workspace_bytes(...) bytes (0 for
+ * invalid sizes), whatever it holds.  Two launches.  Results do not vary
+ * from run to run.  total_q = 0 is allowed and does nothing.
+ */
+size_t fa2_kv4_attn_workspace_bytes(int B, int H, int H_kv, int max_seqlen_q, int d);
+int fa2_kv4_attn(const void* q, const void* cache, long long page_stride, const int* block_table, long long table_stride,
+                 const int* lens, const int* cu_seqlens_q, void* o, float* lse, int B, int H, int H_kv, int total_q,
+                 int max_seqlen_q, int num_pages, int page_size, int table_width, int d, float scale, float k_scale,
+                 float v_scale, int causal, void* workspace, size_t workspace_bytes, void* stream);
+
 /* Static description of a status code (never NULL). */
 const char* fa2_status_string(int status);
 
 /* Read (and if `reset` != 0, clear) the kernels' device status word on the
  * current device: 0 = every wait completed, 1 = some wait timed out,
- * 2 = shared memory base misaligned, 3 = invalid cu_seqlens (varlen calls).
+ * 2 = shared memory base misaligned, 3 = invalid cu_seqlens or request
+ * lengths (varlen and paged-cache calls), 5 = a page id, cache slot or
+ * rotation position out of range (paged-cache calls, fa2_qk_norm_rope).
  * Synchronous with respect to the device. Returns an fa2_status. */
 int fa2_device_status(int* value, int reset);
 

@@ -13,7 +13,7 @@ from __future__ import annotations
 import ctypes
 import math
 import os
-from typing import Optional, Tuple
+from typing import NamedTuple, Optional, Tuple
 
 import torch
 
@@ -25,6 +25,8 @@ __all__ = [
     "fa2_step_from_host_workspace_bytes",
     "fa2_bwd_stages", "fa2_bwd_noalloc", "fa2_fwd_gqa", "fa2_bwd_gqa", "fa2_fwd_splitkv",
     "fa2_fwd_varlen", "fa2_bwd_varlen", "prepared_step", "FA2_OK",
+    "fa2_qk_norm_rope", "fa2_qk_norm_rope_bwd", "fa2_page_plan", "PagePlan", "fa2_kv4_cache", "fa2_kv4_page_bytes",
+    "fa2_kv4_append", "fa2_kv4_gather", "fa2_kv4_attn", "fa2_kv4_attn_workspace_bytes",
 ]
 
 FA2_OK = 0
@@ -34,6 +36,8 @@ _vp = ctypes.c_void_p
 _i = ctypes.c_int
 _f = ctypes.c_float
 _sz = ctypes.c_size_t
+_ll = ctypes.c_longlong
+_llp = ctypes.POINTER(_ll)
 
 _SIGNATURES = {
     "fa2_fwd": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _f, _i, _vp]),
@@ -73,6 +77,17 @@ _SIGNATURES = {
     "fa2_bwd_varlen_workspace_bytes": (_sz, [_i, _i, _i]),
     "fa2_bwd_varlen": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _i,
                             _f, _i, _vp, _sz, _vp]),
+    "fa2_qk_norm_rope": (_i, [_vp, _vp, _vp, _vp, _i, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _i, _f, _llp, _vp]),
+    "fa2_qk_norm_rope_bwd_workspace_bytes": (_sz, [_i]),
+    "fa2_qk_norm_rope_bwd": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _i, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i,
+                                  _i, _i, _f, _llp, _vp, _sz, _vp]),
+    "fa2_page_plan": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _ll, _i, _i, _vp]),
+    "fa2_kv4_page_bytes": (_sz, [_i, _i, _i]),
+    "fa2_kv4_append": (_i, [_vp, _vp, _llp, _vp, _ll, _vp, _vp, _vp, _i, _i, _i, _i, _i, _f, _f, _vp]),
+    "fa2_kv4_gather": (_i, [_vp, _ll, _vp, _ll, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _f, _f, _vp]),
+    "fa2_kv4_attn_workspace_bytes": (_sz, [_i, _i, _i, _i, _i]),
+    "fa2_kv4_attn": (_i, [_vp, _vp, _ll, _vp, _ll, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _i, _i, _f, _f, _f, _i,
+                          _vp, _sz, _vp]),
 }
 
 
@@ -570,3 +585,323 @@ def fa2_step_from_host(host: dict, causal: bool = True, scale: Optional[float] =
     if rc != FA2_OK:
         raise FA2Error("fa2_step_from_host", rc)
     return host
+
+
+# --------------------------------------------------------------- around the attention: norm + rotation, paged 4-bit cache
+def _rows4(t, name: str):
+    """q / k as [B, heads, N, d] with any strides: a 4-D tensor as it is, a packed [total, heads, d] one as B = 1."""
+    if t.dtype != torch.bfloat16 or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA bfloat16 tensor")
+    if t.dim() == 3:
+        t = t.transpose(0, 1).unsqueeze(0)
+    elif t.dim() != 4:
+        raise ValueError(f"{name} must be [B, heads, N, d] or packed [total, heads, d], got {tuple(t.shape)}")
+    if t.shape[3] > 1 and t.stride(3) != 1:
+        raise ValueError(f"{name}'s last dimension must be contiguous")
+    return t
+
+
+def _strides(*tensors):
+    vals = [s for t in tensors for s in t.stride()[:3]]
+    return (_ll * len(vals))(*vals)
+
+
+def _ints(t, name: str, device, dtype=torch.int32, dim: int = 1):
+    if t.dtype != dtype or t.device != device or t.dim() != dim or (t.shape[-1] > 1 and t.stride(-1) != 1):
+        raise ValueError(f"{name} must be a contiguous {dim}-D {dtype} tensor on {device}")
+    return t
+
+
+class _on:
+    """For one call: `device` current, and the call's stream torch's current one, so that what the call allocates
+    belongs to the stream that uses it.  Gives the stream's handle."""
+
+    def __init__(self, device, stream):
+        self.device, self.stream, self.guards = device, stream, ()
+
+    def __enter__(self):
+        if self.device.index != torch.cuda.current_device():
+            self.guards += (torch.cuda.device(self.device),)
+        if self.stream is not None:
+            s = self.stream
+            if not isinstance(s, torch.cuda.Stream):
+                s = torch.cuda.ExternalStream(int(s), device=self.device)
+            self.guards += (torch.cuda.stream(s),)
+        for g in self.guards:
+            g.__enter__()
+        return _stream(self.stream, self.device)
+
+    def __exit__(self, *exc):
+        for g in reversed(self.guards):
+            g.__exit__(*exc)
+
+
+def _norm_args(q, k, q_weight, k_weight, rope, positions, interleaved):
+    """The checks and C arguments that the norm's two directions share; q and k as 4-D."""
+    packed = q.dim() == 3
+    q4, k4 = _rows4(q, "q"), _rows4(k, "k")
+    B, H, N, d = q4.shape
+    if k.dim() != q.dim() or (k4.shape[0], k4.shape[2], k4.shape[3]) != (B, N, d):
+        raise ValueError("k must have q's B, N and d")
+    dev = q.device
+    wts = [w for w in (q_weight, k_weight) if w is not None]
+    if any(w.dtype != wts[0].dtype for w in wts):
+        raise ValueError("q_weight and k_weight must have the same type")
+    for w in wts:
+        if w.dtype not in (torch.bfloat16, torch.float32) or tuple(w.shape) != (d,) or not w.is_contiguous():
+            raise ValueError("a weight must be a contiguous bfloat16 or float32 tensor of d values")
+    rot = max_pos = 0
+    if rope is not None:
+        if rope.dtype != torch.float32 or rope.dim() != 2 or not rope.is_contiguous():
+            raise ValueError("rope must be a contiguous float32 [max_positions, rot_dim] tensor")
+        max_pos, rot = rope.shape
+    if positions is not None:
+        if positions.dtype != torch.int32 or not positions.is_contiguous() or tuple(positions.shape) != (
+                (N,) if packed else (B, N)):
+            raise ValueError("positions must be a contiguous int32 tensor, one per token")
+    for t in (k, rope, positions, *wts):
+        if t is not None and t.device != dev:
+            raise ValueError("all tensors must be on q's device")
+    return (packed, q4, k4, (B, H, k4.shape[1], N, d, rot, 1 if interleaved else 0, max_pos),
+            1 if wts and wts[0].dtype == torch.float32 else 0)
+
+
+def _norm_out(like, out, name: str):
+    """`out` checked against `like` (an input as given), or a new contiguous tensor; and its 4-D form."""
+    if out is None:
+        out = torch.empty(like.shape, dtype=torch.bfloat16, device=like.device)
+    elif out.shape != like.shape or out.device != like.device:
+        raise ValueError(f"{name} must have its input's shape and device")
+    return out, _rows4(out, name)
+
+
+def _dp(t):
+    return None if t is None else t.data_ptr()
+
+
+def fa2_qk_norm_rope(q, k, q_weight=None, k_weight=None, rope=None, positions=None, eps: float = 1e-6,
+                     interleaved: bool = False, q_out=None, k_out=None, stream=None):
+    """Per-head RMS norm of q and k and the position rotation, in one pass (see include/fa2.h).
+
+    q [B, H, N, d], k [B, H_kv, N, d] with any strides but a contiguous last
+    dimension (views of a fused projection), or packed [total, heads, d].
+    ``rope`` is fp32 [max_positions, rot_dim]: cosines, then sines;
+    ``positions`` int32 [B, N] (packed: [total]), default 0, 1, ...  Returns
+    (q_out, k_out), new contiguous tensors unless given; q_out may be q.
+    """
+    packed, q4, k4, dims, w32 = _norm_args(q, k, q_weight, k_weight, rope, positions, interleaved)
+    lib = load_library()
+    with _on(q.device, stream) as st:
+        q_out, qo4 = _norm_out(q, q_out, "q_out")
+        k_out, ko4 = _norm_out(k, k_out, "k_out")
+        rc = lib.fa2_qk_norm_rope(q.data_ptr(), k.data_ptr(), _dp(q_weight), _dp(k_weight), w32, _dp(rope),
+                                  _dp(positions), q_out.data_ptr(), k_out.data_ptr(), *dims, eps,
+                                  _strides(q4, k4, qo4, ko4), st)
+    if rc != FA2_OK:
+        raise FA2Error("fa2_qk_norm_rope", rc)
+    return q_out, k_out
+
+
+def fa2_qk_norm_rope_bwd(dq_out, dk_out, q, k, q_weight=None, k_weight=None, rope=None, positions=None,
+                         eps: float = 1e-6, interleaved: bool = False, dq=None, dk=None, workspace=None, stream=None):
+    """Gradient of fa2_qk_norm_rope: (dq, dk, dq_weight, dk_weight) from the gradients of its outputs.
+
+    q and k are the forward call's inputs.  dq, dk are new contiguous tensors
+    unless given (dq may be dq_out or q).  The weights' gradients are fp32, None where
+    there is no weight.
+    """
+    packed, q4, k4, dims, w32 = _norm_args(q, k, q_weight, k_weight, rope, positions, interleaved)
+    if dq_out.shape != q.shape or dk_out.shape != k.shape or dq_out.device != q.device or dk_out.device != q.device:
+        raise ValueError("dq_out and dk_out must have q's and k's shapes and device")
+    g4, h4 = _rows4(dq_out, "dq_out"), _rows4(dk_out, "dk_out")
+    d = dims[4]
+    lib = load_library()
+    with _on(q.device, stream) as st:
+        dq, dq4 = _norm_out(q, dq, "dq")
+        dk, dk4 = _norm_out(k, dk, "dk")
+        dwq = None if q_weight is None else torch.empty(d, dtype=torch.float32, device=q.device)
+        dwk = None if k_weight is None else torch.empty(d, dtype=torch.float32, device=q.device)
+        if workspace is None and (dwq is not None or dwk is not None):
+            workspace = torch.empty(max(1, lib.fa2_qk_norm_rope_bwd_workspace_bytes(d)), dtype=torch.uint8, device=q.device)
+        rc = lib.fa2_qk_norm_rope_bwd(dq_out.data_ptr(), dk_out.data_ptr(), q.data_ptr(), k.data_ptr(), _dp(q_weight),
+                                      _dp(k_weight), w32, _dp(rope), _dp(positions), dq.data_ptr(), dk.data_ptr(),
+                                      _dp(dwq), _dp(dwk), *dims, eps, _strides(g4, h4, q4, k4, dq4, dk4),
+                                      _dp(workspace), 0 if workspace is None else workspace.numel() * workspace.element_size(),
+                                      st)
+    if rc != FA2_OK:
+        raise FA2Error("fa2_qk_norm_rope_bwd", rc)
+    return dq, dk, dwq, dwk
+
+
+class PagePlan(NamedTuple):
+    """What fa2_page_plan writes besides the block table (all on the GPU; see include/fa2.h)."""
+    lens: torch.Tensor          # int32 [B]
+    cu_new: torch.Tensor        # int32 [B + 1]
+    cu_total: torch.Tensor      # int32 [B + 1]
+    slots: torch.Tensor         # int64 [max_tokens]
+    positions: torch.Tensor     # int32 [max_tokens]
+    pages_needed: torch.Tensor  # int32 [1]
+
+
+def fa2_page_plan(cached_lens, new_lens, free_pages, block_table, page_size: int, max_tokens: int,
+                  plan: Optional[PagePlan] = None, stream=None) -> PagePlan:
+    """One step's page plan from request lengths, on the GPU: fills the new entries of ``block_table``
+    (int32 [B, width]) and returns the rest.  ``plan``: an earlier call's result to write into."""
+    dev = cached_lens.device
+    if not cached_lens.is_cuda:
+        raise ValueError("cached_lens must be a CUDA tensor")
+    for t, name in ((cached_lens, "cached_lens"), (new_lens, "new_lens"), (free_pages, "free_pages")):
+        _ints(t, name, dev)
+    _ints(block_table, "block_table", dev, dim=2)
+    B = cached_lens.numel()
+    if new_lens.numel() != B or block_table.shape[0] != B:
+        raise ValueError("cached_lens, new_lens and block_table must have one entry per request")
+    if max_tokens < 0:
+        raise ValueError("max_tokens must be at least 0")
+    if plan is not None:
+        sizes = (B, B + 1, B + 1, max_tokens, max_tokens, 1)
+        for t, name, n in zip(plan, PagePlan._fields, sizes):
+            _ints(t, name, dev, torch.int64 if name == "slots" else torch.int32)
+            if t.numel() != n:
+                raise ValueError(f"plan.{name} must have {n} entries")
+    lib = load_library()
+    with _on(dev, stream) as st:
+        if plan is None:
+            new = lambda n, dt=torch.int32: torch.empty(n, dtype=dt, device=dev)  # noqa: E731
+            plan = PagePlan(new(B), new(B + 1), new(B + 1), new(max_tokens, torch.int64), new(max_tokens), new(1))
+        rc = lib.fa2_page_plan(cached_lens.data_ptr(), new_lens.data_ptr(), _ptr(free_pages), block_table.data_ptr(),
+                               plan.lens.data_ptr(), plan.cu_new.data_ptr(), plan.cu_total.data_ptr(), _ptr(plan.slots),
+                               _ptr(plan.positions), plan.pages_needed.data_ptr(), B, free_pages.numel(),
+                               block_table.shape[1], block_table.stride(0), page_size, max_tokens, st)
+    if rc != FA2_OK:
+        raise FA2Error("fa2_page_plan", rc)
+    return plan
+
+
+def fa2_kv4_page_bytes(H_kv: int, page_size: int, d: int) -> int:
+    return load_library().fa2_kv4_page_bytes(H_kv, page_size, d)
+
+
+def fa2_kv4_cache(num_pages: int, H_kv: int, page_size: int, d: int, device="cuda") -> torch.Tensor:
+    """A cache of zeros: uint8 [num_pages, H_kv, page_size / 16, 18 d]."""
+    if fa2_kv4_page_bytes(H_kv, page_size, d) == 0 or num_pages < 1:
+        raise ValueError("page_size must be 16, 32, 64 or 128, d 16, 32, 64 or 128, and the counts at least 1")
+    return torch.zeros((num_pages, H_kv, page_size // 16, 18 * d), dtype=torch.uint8, device=device)
+
+
+def _cache_dims(cache):
+    if cache.dim() != 4 or cache.dtype != torch.uint8 or not cache.is_cuda or cache.shape[3] % 18 != 0:
+        raise ValueError("cache must be a CUDA uint8 tensor [num_pages, H_kv, page_size / 16, 18 d] (fa2_kv4_cache)")
+    pages, heads, tiles, row = cache.shape
+    if (cache.stride(3) != 1 or (tiles > 1 and cache.stride(2) != row) or (heads > 1 and cache.stride(1) != tiles * row)):
+        raise ValueError("a page of the cache must be contiguous")
+    # (one page: its stride says nothing)
+    stride = cache.stride(0) if pages > 1 else heads * tiles * row
+    return pages, heads, tiles * 16, row // 18, stride
+
+
+def fa2_kv4_append(k, v, cache, slots, k_scale: float = 1.0, v_scale: float = 1.0, k_out=None, v_out=None,
+                   stream=None) -> None:
+    """Write keys and values [T, H_kv, d] bf16 (any token and head strides) to their ``slots`` (int64 [T]) of the
+    4-bit cache.  ``k_out``, ``v_out``: contiguous tensors that receive the values as stored."""
+    pages, heads, page_size, d, stride = _cache_dims(cache)
+    T = slots.numel()
+    for t, name in ((k, "k"), (v, "v")):
+        if t.dtype != torch.bfloat16 or t.device != cache.device or tuple(t.shape) != (T, heads, d) or t.stride(2) != 1:
+            raise ValueError(f"{name} must be bfloat16 [tokens, H_kv, d] on the cache's device, its last dimension contiguous")
+    for t, name in ((k_out, "k_out"), (v_out, "v_out")):
+        if t is not None and (t.dtype != torch.bfloat16 or t.device != cache.device or t.shape != k.shape or not t.is_contiguous()):
+            raise ValueError(f"{name} must be a contiguous bfloat16 tensor of k's shape")
+    _ints(slots, "slots", cache.device, torch.int64)
+    lib = load_library()
+    strides = (_ll * 4)(k.stride(0), k.stride(1), v.stride(0), v.stride(1))
+    with _on(cache.device, stream) as st:
+        rc = lib.fa2_kv4_append(_ptr(k), _ptr(v), strides, cache.data_ptr(), stride, _ptr(slots),
+                                None if k_out is None else _ptr(k_out), None if v_out is None else _ptr(v_out), T, heads,
+                                pages, page_size, d, k_scale, v_scale, st)
+    if rc != FA2_OK:
+        raise FA2Error("fa2_kv4_append", rc)
+
+
+def fa2_kv4_gather(cache, block_table, cu_seqlens, total: int, k_scale: float = 1.0, v_scale: float = 1.0, k=None,
+                   v=None, stream=None):
+    """The cache's keys and values as packed bf16 [total, H_kv, d] (what fa2_fwd_varlen takes as k and v with
+    cu_seqlens_k = ``cu_seqlens``).  Rows outside every sequence of given k, v are left as they are."""
+    pages, heads, page_size, d, stride = _cache_dims(cache)
+    dev = cache.device
+    _ints(block_table, "block_table", dev, dim=2)
+    _ints(cu_seqlens, "cu_seqlens", dev)
+    B = block_table.shape[0]
+    if cu_seqlens.numel() != B + 1:
+        raise ValueError("cu_seqlens must have one entry more than block_table has rows")
+    for t, name in ((k, "k"), (v, "v")):
+        if t is not None and (t.device != dev or _packed(t, name) != (total, heads, d)):
+            raise ValueError(f"{name} must be [total, H_kv, d] on the cache's device")
+    lib = load_library()
+    with _on(dev, stream) as st:
+        k = torch.empty((total, heads, d), dtype=torch.bfloat16, device=dev) if k is None else k
+        v = torch.empty((total, heads, d), dtype=torch.bfloat16, device=dev) if v is None else v
+        rc = lib.fa2_kv4_gather(cache.data_ptr(), stride, block_table.data_ptr(), block_table.stride(0),
+                                cu_seqlens.data_ptr(), _ptr(k), _ptr(v), B, heads, total, pages, page_size,
+                                block_table.shape[1], d, k_scale, v_scale, st)
+    if rc != FA2_OK:
+        raise FA2Error("fa2_kv4_gather", rc)
+    return k, v
+
+
+def fa2_kv4_attn_workspace_bytes(B: int, H: int, H_kv: int, max_seqlen_q: int, d: int) -> int:
+    return load_library().fa2_kv4_attn_workspace_bytes(B, H, H_kv, max_seqlen_q, d)
+
+
+def fa2_kv4_attn(q, cache, block_table, lens, cu_seqlens_q=None, max_seqlen_q: Optional[int] = None, o=None, lse=None,
+                 workspace=None, scale: Optional[float] = None, k_scale: float = 1.0, v_scale: float = 1.0,
+                 causal: bool = True, stream=None):
+    """Attention of packed queries q [total_q, H, d] over the 4-bit paged cache: (o [total_q, H, d] bf16,
+    lse [H, total_q] fp32).
+
+    Request b's keys are the first lens[b] tokens of its pages block_table[b]
+    (int32 [B, width]); its queries are rows cu_seqlens_q[b] .. of q, its last
+    positions where ``causal``.  Without cu_seqlens_q every request has
+    ``max_seqlen_q`` queries (default: total_q / B).  With cu_seqlens_q and no
+    max_seqlen_q the maximum is read from the offsets (a device sync).
+    """
+    pages, heads, page_size, d, stride = _cache_dims(cache)
+    dev = cache.device
+    tq, H, dq = _packed(q, "q")
+    if dq != d or q.device != dev:
+        raise ValueError("q must have the cache's head dim and device")
+    _ints(block_table, "block_table", dev, dim=2)
+    _ints(lens, "lens", dev)
+    B = block_table.shape[0]
+    if lens.numel() != B:
+        raise ValueError("lens must have one entry per row of block_table")
+    if cu_seqlens_q is not None:
+        _ints(cu_seqlens_q, "cu_seqlens_q", dev)
+        if cu_seqlens_q.numel() != B + 1:
+            raise ValueError("cu_seqlens_q must have one entry more than block_table has rows")
+        mq = _max_len(cu_seqlens_q, max_seqlen_q)
+    else:
+        mq = tq // B if max_seqlen_q is None else int(max_seqlen_q)
+        if mq * B != tq:
+            raise ValueError("without cu_seqlens_q every request has the same number of queries")
+    if o is not None and (o.device != dev or _packed(o, "o") != (tq, H, d)):
+        raise ValueError("o must have q's shape and device")
+    if lse is not None and (lse.dtype != torch.float32 or lse.device != dev or not lse.is_contiguous()
+                            or tuple(lse.shape) != (H, tq)):
+        raise ValueError("lse must be a contiguous fp32 [H, total_q] tensor")
+    if workspace is not None and workspace.device != dev:
+        raise ValueError("workspace must be on the cache's device")
+    lib = load_library()
+    with _on(dev, stream) as st:
+        o = torch.empty_like(q) if o is None else o
+        lse = torch.empty((H, tq), dtype=torch.float32, device=dev) if lse is None else lse
+        if workspace is None:
+            workspace = torch.empty(max(1, lib.fa2_kv4_attn_workspace_bytes(B, H, heads, mq, d)), dtype=torch.uint8,
+                                    device=dev)
+        rc = lib.fa2_kv4_attn(_ptr(q), cache.data_ptr(), stride, block_table.data_ptr(), block_table.stride(0),
+                              lens.data_ptr(), _dp(cu_seqlens_q), _ptr(o), _ptr(lse), B, H, heads, tq, mq, pages,
+                              page_size, block_table.shape[1], d, _scale(scale, d), k_scale, v_scale,
+                              1 if causal else 0, workspace.data_ptr(), workspace.numel() * workspace.element_size(), st)
+    if rc != FA2_OK:
+        raise FA2Error("fa2_kv4_attn", rc)
+    return o, lse

@@ -4,13 +4,14 @@
 #include <cuda_runtime.h>
 
 #include <atomic>
-#include <cmath>
 #include <cstdint>
 #include <cstdio>
+#include <initializer_list>
 #include <mutex>
 #include <set>
 #include <utility>
 
+#include "args.h"
 #include "fa2.h"
 #include "launch.h"
 
@@ -151,17 +152,6 @@ bool make_tmap_f32(CUtensorMap* out, const void* base, int BH, int N, int d) {
   return encode_rows(out, base, Elem::kF32, BH, N, d, d, static_cast<long long>(N) * d);
 }
 
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-
-struct Range {
-  uintptr_t lo, hi;
-};
-bool overlap(Range a, Range b) { return a.lo < b.hi && b.lo < a.hi; }
-Range range_of(const void* p, size_t bytes) {
-  const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
-  return {lo, lo + bytes};
-}
-
 int check_sizes(int B, int H, int N, int d) {
   if (B < 1 || H < 1 || N < 1) return FA2_ERR_SHAPE;
   if (d != 16 && d != 32 && d != 64 && d != 128) return FA2_ERR_HEADDIM;
@@ -171,11 +161,6 @@ int check_sizes(int B, int H, int N, int d) {
   if (BH > 0x7fffffffLL || tiles * BH > 0x7fffffffLL || N > (1 << 30)) return FA2_ERR_SHAPE;
   return FA2_OK;
 }
-
-int check_scale(float scale) { return (std::isfinite(scale) && scale > 0.f) ? FA2_OK : FA2_ERR_SCALE; }
-
-constexpr size_t kWsAlign = 256;
-size_t round_up(size_t x) { return (x + kWsAlign - 1) / kWsAlign * kWsAlign; }
 
 size_t workspace_bytes(int B, int H, int N, int d) {
   const size_t rows = static_cast<size_t>(B) * H * N;
@@ -216,9 +201,6 @@ int prepare_v16(TmapSet* tm, FwdProblem* p, const void* v, int heads, int rows, 
     return cuda_fail(e, "v to f16 launch");
   return FA2_OK;
 }
-
-// Query heads H, key/value heads Hkv (H a multiple of Hkv).
-int check_heads(int H, int Hkv) { return (Hkv >= 1 && Hkv <= H && H % Hkv == 0) ? FA2_OK : FA2_ERR_SHAPE; }
 
 int validate_bwd(const void* q, const void* k, const void* v, const void* o, const void* dO, const float* lse,
                  void* dq, void* dk, void* dv, int B, int H, int Hkv, int N, int d, float scale) {
@@ -903,10 +885,14 @@ const char* fa2_status_string(int status) {
 
 int fa2_device_status(int* value, int reset) {
   if (!value) return FA2_ERR_NULL;
-  int a = 0, b = 0;
-  if (int e = read_fwd_status(&a, reset != 0)) return cuda_fail(e, "read status");
-  if (int e = read_bwd_status(&b, reset != 0)) return cuda_fail(e, "read status");
-  *value = a > b ? a : b;
+  int worst = 0;
+  for (auto read : {read_fwd_status, read_bwd_status, read_norm_status, read_plan_status, read_cache_status,
+                    read_attn4_status}) {
+    int v = 0;
+    if (int e = read(&v, reset != 0)) return cuda_fail(e, "read status");
+    if (v > worst) worst = v;
+  }
+  *value = worst;
   return FA2_OK;
 }
 

@@ -1,0 +1,780 @@
+// Attention of new query tokens over a paged key-value cache held in 4 bits.
+//
+// O = softmax(scale Q K^T) V over each request's cached keys, the queries
+// being its last positions (causal: query i of Lq sees key j iff
+// j <= i + Lk - Lq).  Bound by reading the cache once: 9 d / 8 bytes a key
+// and K/V head against 4 d flops for each query head of its group, far below
+// the balance of even the warp-level matrix instructions (1024 fp16
+// multiply-adds a clock and SM, measured), so the products are
+// mma.sync.m16n8k16 on operands decoded in registers: a tcgen05 operand would
+// have to be written to shared memory in 16 bits first, 3.6 times the bytes
+// that come in, for 128-row tiles of which a decoding step fills 1 to 16.
+//
+// Work.  A unit is (request, K/V head, 8 NT query rows), its keys 16-key
+// tiles; row r of a unit is query r / G, head r % G of the group.  All
+// units' tiles form one line, which is cut into equal spans, one for each
+// warp: every warp reads as many bytes as any other, whatever the lengths.
+// A unit inside one span is finished by its warp; one that spans share leaves
+// a partial result per span (unnormalised O, running maximum and sum), which
+// the combine kernel joins in span order.  Warps share nothing, so there are
+// no barriers, and the result does not depend on the order they run in.
+//
+// Operands (lane (g, c) = (lane / 4, lane % 4)).  The first product is
+// S^T = K Q^T: a tile's 16 keys are the rows of the instruction and the 8
+// query rows its columns, which wastes none of it on a group of 8 heads.  The
+// columns of K are a contraction index, so their order is free as long as Q
+// has the same: lane c holds columns c d/4 .. of keys g and g + 8, contiguous
+// in the cache.  The second is O^T = V^T P^T, columns of V as rows: lane g
+// holds columns g d/8 .. of keys 2c, 2c+1, 2c+8, 2c+9, and one
+// byte-interleave of two keys' codes makes the pairs along the contraction
+// that the instruction wants before they are decoded.  P^T comes from S^T's
+// registers by two 8x8 transposes (movmatrix).
+//
+// Precision.  Cache values are exact in fp16 (6 significant bits), Q (8 bits)
+// is divided by a power of two per row so that its largest value is in
+// [1, 2), which is exact in fp16 down to 2^-14 of it (2^-25 absolute below),
+// so S is exact up to its fp32 sums.  P is rounded to fp16 (11 bits against
+// bf16's 8), held 2^11 up so that weights down to 2^-25 of the largest keep
+// all 11.  The running maximum is raised only when a score passes it by 2^4
+// (weights then reach 2^15, inside fp16), which saves the tile's maximum
+// (three shuffles per column) and the rescaling of O for nearly every tile;
+// maximum, sum, O are fp32 and the final quotient removes the common factor
+// exactly.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+
+#include "args.h"
+#include "fa2.h"
+#include "kv4.cuh"
+#include "launch.h"
+
+namespace fa2 {
+namespace {
+
+__device__ int g_attn4_status;
+
+constexpr int kWarps = 4;  // warps of a CTA
+constexpr float kNoMax = -1.7e38f;  // running maximum of a row that has seen no key (finite: no inf - inf)
+constexpr float kLift = 11.f;   // weights are held 2^11 up
+constexpr float kLag = 4.f;     // a score may pass the running maximum by 2^4
+constexpr int kMinTiles = 4;    // shortest span: below, a partial result costs more than its tiles
+
+struct Attn4Problem {
+  const __nv_bfloat16* q;
+  __nv_bfloat16* o;
+  float* lse;
+  PagedCache cache;
+  const int* table;
+  long long table_stride;
+  const int* lens;
+  const int* cu_q;    // or NULL: every request has uniform_q queries
+  float* part;        // [2 * spans][rows][d] unnormalised O
+  float2* part_ml;    // [2 * spans][rows] maximum (log2), sum
+  long long* start;   // [B + 1] first tile of each request on the line
+  int B, H, G, total_q, uniform_q, max_q, width;
+  int spans;
+  float scale_log2, v_scale;
+  int causal;
+};
+
+struct Request {
+  int q0, Lq, Lk;
+  bool ok;
+};
+
+// A request with impossible lengths is left out (its rows are not written).
+__device__ __forceinline__ Request request(const Attn4Problem& p, int b) {
+  Request r;
+  r.Lk = __ldg(p.lens + b);
+  if (p.cu_q) {
+    r.q0 = __ldg(p.cu_q + b);
+    r.Lq = __ldg(p.cu_q + b + 1) - r.q0;
+  } else {
+    r.q0 = b * p.uniform_q;
+    r.Lq = p.uniform_q;
+  }
+  r.ok = r.Lk >= 0 && (r.Lk + ((1LL << p.cache.shift) - 1)) >> p.cache.shift <= p.width && r.q0 >= 0 && r.Lq >= 0 &&
+         r.Lq <= p.max_q && r.q0 <= p.total_q - r.Lq;
+  return r;
+}
+
+template <int ROWS>
+__device__ __forceinline__ int row_tiles(const Attn4Problem& p, const Request& r) {
+  return static_cast<int>((static_cast<long long>(p.G) * r.Lq + ROWS - 1) / ROWS);
+}
+__device__ __forceinline__ int key_tiles(const Request& r) { return (r.Lk + kCacheTile - 1) / kCacheTile; }
+
+template <int ROWS>
+__device__ __forceinline__ long long tiles_of(const Attn4Problem& p, const Request& r) {
+  return r.ok ? static_cast<long long>(p.cache.heads) * row_tiles<ROWS>(p, r) * key_tiles(r) : 0;
+}
+
+__device__ __forceinline__ long long span_length(long long total, int spans) {
+  const long long s = (total + spans - 1) / spans;
+  return s < kMinTiles ? kMinTiles : s;
+}
+
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
+
+// One tile's codes and scales of this lane.
+template <int D>
+struct TileRegs {
+  static constexpr int kW = D >= 32 ? D / 32 : 1;  // words of one load
+  uint32_t k[2][kW], v[2][kW], ks, vs;
+};
+
+template <int N>
+__device__ __forceinline__ void load_words(uint32_t (&w)[N], const char* p) {
+  if constexpr (N == 4) {
+    asm volatile("ld.global.nc.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                 : "l"(p));
+  } else if constexpr (N == 2) {
+    asm volatile("ld.global.nc.L1::no_allocate.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "l"(p));
+  } else {
+    asm volatile("ld.global.nc.L1::no_allocate.b32 %0, [%1];" : "=r"(w[0]) : "l"(p));
+  }
+}
+__device__ __forceinline__ uint32_t load_half(const char* p) {
+  uint16_t h;
+  asm volatile("ld.global.nc.L1::no_allocate.b16 %0, [%1];" : "=h"(h) : "l"(p));
+  return h;
+}
+
+template <int D>
+__device__ __forceinline__ void load_tile(TileRegs<D>& t, const char* tile, int lane) {
+  using L = Kv4<D>;
+  constexpr int kB = D / 8;  // bytes of a lane's piece
+  const int g = lane >> 2, c = lane & 3;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    if constexpr (kB == 2) {
+      t.k[i][0] = load_half(tile + i * 32 * kB + lane * kB);
+      t.v[i][0] = load_half(tile + L::kV + i * 32 * kB + lane * kB);
+    } else {
+      load_words(t.k[i], tile + i * 32 * kB + lane * kB);
+      load_words(t.v[i], tile + L::kV + i * 32 * kB + lane * kB);
+    }
+  }
+  uint32_t w[1];
+  if constexpr (D == 128) {  // groups 2 c, 2 c + 1 of keys g, g + 8
+    load_words(w, tile + L::kKS + lane * 4);
+    t.ks = w[0];
+  } else {
+    t.ks = load_half(tile + L::kKS + (g * L::kGroups + c * L::kGroups / 4) * 2);
+  }
+  load_words(w, tile + L::kVS + ((g * L::kGroups / 8) * 4 + c) * 4);
+  t.vs = w[0];
+}
+
+// One warp's running state of a unit.
+template <int D, int NT>
+struct Rows {
+  uint32_t q[NT][D / 16][2];  // Q^T operand
+  float o[NT][D / 16][4];
+  float cs[NT][2], off[NT][2], l[NT][2];  // score factor, kLift - maximum, sum, of columns 2c, 2c + 1
+  int vis[NT][2];                         // keys they see
+  int min_vis;                            // least of all the unit's rows
+};
+
+template <int D, int NT>
+__device__ __forceinline__ void start_unit(Rows<D, NT>& s, const Attn4Problem& p, const Request& rq, int h, int row0,
+                                           int lane) {
+  constexpr int kPer = D / 4;  // columns of a lane
+  const int g = lane >> 2, c = lane & 3;
+  const int rows = p.G * rq.Lq;
+  s.min_vis = rq.Lk;
+#pragma unroll
+  for (int j = 0; j < NT; ++j) {
+    const int r = row0 + 8 * j + g;
+    uint32_t w[kPer / 2];
+#pragma unroll
+    for (int i = 0; i < kPer / 2; ++i) w[i] = 0;
+    if (r < rows) {
+      const int i = r / p.G;
+      const __nv_bfloat16* src =
+          p.q + (static_cast<long long>(rq.q0 + i) * p.H + h * p.G + (r - i * p.G)) * D + c * kPer;
+      if constexpr (kPer >= 8) {
+#pragma unroll
+        for (int v = 0; v < kPer / 8; ++v) {
+          const uint4 u = __ldg(reinterpret_cast<const uint4*>(src) + v);
+          w[4 * v] = u.x, w[4 * v + 1] = u.y, w[4 * v + 2] = u.z, w[4 * v + 3] = u.w;
+        }
+      } else {
+        const uint2 u = __ldg(reinterpret_cast<const uint2*>(src));
+        w[0] = u.x, w[1] = u.y;
+      }
+    }
+    // the power of two at or below the row's largest magnitude (1 for a row
+    // of zeros, infinities or NaN)
+    float mx = 0.f;
+#pragma unroll
+    for (int i = 0; i < kPer / 2; ++i) {
+      const float2 f = unpack_bf16x2(w[i]);
+      mx = fmaxf(mx, fmaxf(fabsf(f.x), fabsf(f.y)));
+    }
+    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+    const bool plain = mx == 0.f || isinf(mx);
+    const int e = plain ? 0 : min(max(static_cast<int>(__float_as_uint(mx) >> 23) - 127, -126), 126);
+    const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+    // (kept off zero and infinity: the score of a masked key is -inf times it)
+    const float up = fminf(fmaxf(__uint_as_float(static_cast<uint32_t>(127 + e) << 23) * p.scale_log2, 1e-37f), 3e38f);
+#pragma unroll
+    for (int t = 0; t < D / 16; ++t)
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const float2 f = unpack_bf16x2(w[2 * t + u]);
+        s.q[j][t][u] = pack_f16x2(f.x * down, f.y * down);
+      }
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      s.cs[j][u] = __shfl_sync(0xffffffffu, up, (2 * c + u) * 4);
+      s.off[j][u] = kLift - kNoMax;
+      s.l[j][u] = 0.f;
+      const int col = row0 + 8 * j + 2 * c + u;
+      int vis = rq.Lk;
+      if (p.causal && col < rows) vis = min(max(rq.Lk - rq.Lq + col / p.G + 1, 0), rq.Lk);
+      s.vis[j][u] = vis;
+      s.min_vis = min(s.min_vis, vis);
+    }
+#pragma unroll
+    for (int t = 0; t < D / 16; ++t)
+#pragma unroll
+      for (int u = 0; u < 4; ++u) s.o[j][t][u] = 0.f;
+  }
+  s.min_vis = __reduce_min_sync(0xffffffffu, s.min_vis);
+}
+
+// e4m3 NaN bytes of a word, one bit per byte.
+__device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) m |= static_cast<uint32_t>(((w >> (8 * i)) & 0x7fu) == 0x7fu) << i;
+  return m;
+}
+
+// One 16-key tile at key0 into the unit's state.  `keys`: keys of the tile
+// that exist (a page id out of range leaves none).
+template <int D, int NT>
+__device__ __forceinline__ void step(Rows<D, NT>& s, const TileRegs<D>& t, int key0, int keys, int lane) {
+  using L = Kv4<D>;
+  const int g = lane >> 2, c = lane & 3;
+  uint32_t vs = t.vs;
+  uint32_t nan_keys = 0;  // keys of the tile with a NaN in this lane's columns of V
+  const bool masked = key0 + kCacheTile > s.min_vis || keys < kCacheTile;  // the same in all lanes
+  if (masked) {
+    // V of keys past the end counts as zeros, whatever the page holds; a NaN
+    // that some rows see is taken out of the product (0 x NaN would reach the
+    // rows that do not) and put into those rows afterwards.
+    uint32_t drop = 0, nan = nan_bytes(vs);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int key = (i >> 1) * 8 + 2 * c + (i & 1);
+      if (key >= keys) drop |= 1u << i;
+      else if (nan >> i & 1) nan_keys |= 1u << key, drop |= 1u << i;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (drop >> i & 1) vs &= ~(0xffu << (8 * i));
+    nan_keys |= __shfl_xor_sync(0xffffffffu, nan_keys, 1);
+    nan_keys |= __shfl_xor_sync(0xffffffffu, nan_keys, 2);
+  }
+
+  float x[NT][4];
+#pragma unroll
+  for (int j = 0; j < NT; ++j)
+#pragma unroll
+    for (int u = 0; u < 4; ++u) x[j][u] = 0.f;
+  {
+    // scales of keys g (low half) and g + 8 for the lane's columns
+    const uint32_t s0 = e4m3x2_to_f16(t.ks), s1 = D == 128 ? e4m3x2_to_f16(t.ks >> 16) : s0;
+    const uint32_t a0 = __byte_perm(s0, 0, 0x1010), b0 = __byte_perm(s0, 0, 0x3232);
+    const uint32_t a1 = __byte_perm(s1, 0, 0x1010), b1 = __byte_perm(s1, 0, 0x3232);
+    constexpr int kSteps = D / 16;
+#pragma unroll
+    for (int w = 0; w < (kSteps + 1) / 2; ++w) {
+      uint32_t lo[4], hi[4];
+      e2m1x8_to_f16(t.k[0][w], lo);
+      e2m1x8_to_f16(t.k[1][w], hi);
+      const uint32_t sa = w >= 2 ? a1 : a0, sb = w >= 2 ? b1 : b0;
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        if (2 * w + u < kSteps) {
+          const uint32_t a[4] = {hmul2(lo[2 * u], sa), hmul2(hi[2 * u], sb), hmul2(lo[2 * u + 1], sa),
+                                 hmul2(hi[2 * u + 1], sb)};
+#pragma unroll
+          for (int j = 0; j < NT; ++j) mma_f16(x[j], a, s.q[j][2 * w + u][0], s.q[j][2 * w + u][1]);
+        }
+      }
+    }
+  }
+  // x[j][0], [1]: key g, columns 2c, 2c + 1; [2], [3]: key g + 8.
+  if (masked) {
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int key = g + (u >> 1) * 8;
+        if (key >= keys || key0 + key >= s.vis[j][u & 1]) x[j][u] = -INFINITY;
+      }
+  }
+  bool over = false;
+  float y[NT][4];
+#pragma unroll
+  for (int j = 0; j < NT; ++j)
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      y[j][u] = fmaf(x[j][u], s.cs[j][u & 1], s.off[j][u & 1]);
+      over |= y[j][u] > kLift + kLag;
+    }
+  if (__any_sync(0xffffffffu, over)) {
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        float mx = fmaxf(x[j][u], x[j][u + 2]) * s.cs[j][u];
+#pragma unroll
+        for (int sh = 4; sh < 32; sh <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, sh));
+        const float old = kLift - s.off[j][u], m = fmaxf(old, mx);
+        const float down = ex2_approx(old - m);
+        s.off[j][u] = kLift - m;
+        s.l[j][u] *= down;
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+          s.o[j][i][u] *= down;
+          s.o[j][i][u + 2] *= down;
+        }
+        y[j][u] = fmaf(x[j][u], s.cs[j][u], s.off[j][u]);
+        y[j][u + 2] = fmaf(x[j][u + 2], s.cs[j][u], s.off[j][u]);
+      }
+  }
+  uint32_t pb[NT][2];
+#pragma unroll
+  for (int j = 0; j < NT; ++j) {
+    float e[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) e[u] = ex2_approx(y[j][u]);
+    s.l[j][0] += e[0] + e[2];
+    s.l[j][1] += e[1] + e[3];
+    pb[j][0] = transpose8x8(pack_f16x2(e[0], e[1]));
+    pb[j][1] = transpose8x8(pack_f16x2(e[2], e[3]));
+  }
+  {
+    const uint32_t s0 = e4m3x2_to_f16(vs), s1 = e4m3x2_to_f16(vs >> 16);  // keys 2c, 2c + 1; 2c + 8, 2c + 9
+    constexpr int kSteps = D / 16;
+    constexpr int kWords = D >= 64 ? D / 64 : 1;  // of one key's piece
+#pragma unroll
+    for (int w = 0; w < kWords; ++w) {
+      // low / high codes of the two keys' bytes side by side
+      uint32_t even[2][4], odd[2][4];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        uint32_t a, b;
+        if constexpr (D >= 64) {
+          a = t.v[i][w], b = t.v[i][kWords + w];
+        } else {
+          a = t.v[i][0], b = t.v[i][0] >> (D / 2);
+        }
+        e2m1x8_to_f16((a & 0x0f0f0f0fu) | ((b << 4) & 0xf0f0f0f0u), even[i]);
+        e2m1x8_to_f16(((a >> 4) & 0x0f0f0f0fu) | (b & 0xf0f0f0f0u), odd[i]);
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        if (4 * w + u < kSteps) {
+          const uint32_t a[4] = {hmul2(even[0][u], s0), hmul2(odd[0][u], s0), hmul2(even[1][u], s1),
+                                 hmul2(odd[1][u], s1)};
+#pragma unroll
+          for (int j = 0; j < NT; ++j) mma_f16(s.o[j][4 * w + u], a, pb[j][0], pb[j][1]);
+        }
+      }
+    }
+  }
+  if (masked && __any_sync(0xffffffffu, nan_keys != 0)) {
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int n = min(max(s.vis[j][u] - key0, 0), kCacheTile);
+        if (nan_keys & ((1u << n) - 1u)) {
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i) s.o[j][i][u] = s.o[j][i][u + 2] = __uint_as_float(0x7fffffffu);
+        }
+      }
+  }
+}
+
+// o and lse of a row from its sums (a row that saw no key: zeros, -inf).
+__device__ __forceinline__ float row_lse(float m, float l) { return (m - kLift + log2f(l)) * 0.69314718055994531f; }
+
+template <int D, int NT>
+__device__ __forceinline__ void end_unit(Rows<D, NT>& s, const Attn4Problem& p, const Request& rq, int h, int row0,
+                                         int slot, int lane) {
+  constexpr int kPer = D / 8, kRows = 8 * NT;
+  const int g = lane >> 2, c = lane & 3;
+  const int rows = p.G * rq.Lq;
+#pragma unroll
+  for (int j = 0; j < NT; ++j)
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      float l = s.l[j][u];
+#pragma unroll
+      for (int sh = 4; sh < 32; sh <<= 1) l += __shfl_xor_sync(0xffffffffu, l, sh);
+      const int local = 8 * j + 2 * c + u, r = row0 + local;
+      if (r >= rows) continue;
+      const float m = kLift - s.off[j][u];
+      float v[kPer];
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) {
+        v[2 * i] = s.o[j][i][u];
+        v[2 * i + 1] = s.o[j][i][u + 2];
+      }
+      if (slot >= 0) {
+        float* dst = p.part + (static_cast<long long>(slot) * kRows + local) * D + g * kPer;
+#pragma unroll
+        for (int i = 0; i < kPer; i += (kPer >= 4 ? 4 : 2)) {
+          if constexpr (kPer >= 4)
+            *reinterpret_cast<float4*>(dst + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+          else
+            *reinterpret_cast<float2*>(dst + i) = make_float2(v[i], v[i + 1]);
+        }
+        if (g == 0) p.part_ml[static_cast<long long>(slot) * kRows + local] = make_float2(m, l);
+        continue;
+      }
+      const float k = l == 0.f ? 0.f : p.v_scale / l;
+      const int i0 = r / p.G;
+      const long long tok = rq.q0 + i0;
+      const int head = h * p.G + (r - i0 * p.G);
+      uint32_t w[kPer / 2];
+#pragma unroll
+      for (int i = 0; i < kPer / 2; ++i) w[i] = pack_bf16x2(v[2 * i] * k, v[2 * i + 1] * k);
+      char* dst = reinterpret_cast<char*>(p.o + (tok * p.H + head) * D + g * kPer);
+      if constexpr (kPer == 16) {
+        reinterpret_cast<uint4*>(dst)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        reinterpret_cast<uint4*>(dst)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+      } else if constexpr (kPer == 8) {
+        *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+      } else if constexpr (kPer == 4) {
+        *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
+      } else {
+        *reinterpret_cast<uint32_t*>(dst) = w[0];
+      }
+      if (g == 0) p.lse[static_cast<long long>(head) * p.total_q + tok] = l == 0.f ? -INFINITY : row_lse(m, l);
+    }
+}
+
+// The page ids of a unit's next 32 pages, one per lane.
+struct Pages {
+  int ids, first;
+};
+
+template <int D>
+__device__ __forceinline__ const char* tile_address(Pages& pg, const Attn4Problem& p, const int* row, int pages, int h,
+                                                    int tile, int lane, bool& bad) {
+  const int per = p.cache.shift - 4;
+  const int idx = tile >> per;
+  if (idx >= pg.first + 32 || idx < pg.first) {
+    pg.first = idx;
+    pg.ids = idx + lane < pages ? __ldg(row + idx + lane) : 0;
+  }
+  int id = __shfl_sync(0xffffffffu, pg.ids, idx - pg.first);
+  bad = id < 0 || id >= p.cache.num_pages;
+  if (bad) {
+    if (lane == 0) atomicCAS(&g_attn4_status, kDevOk, kDevBadIndex);
+    id = 0;
+  }
+  return p.cache.base + id * p.cache.page_stride +
+         ((static_cast<long long>(h) << per) + (tile & ((1 << per) - 1))) * Kv4<D>::kTileBytes;
+}
+
+template <int D, int NT, int CTAS>
+__global__ void __launch_bounds__(kWarps * 32, CTAS) fa2_kv4_attn_kernel(const Attn4Problem p) {
+  constexpr int kRows = 8 * NT;
+  griddep_wait();
+  griddep_launch_dependents();
+  const int lane = threadIdx.x & 31;
+  // consecutive spans on different SMs, so that a short line spreads out
+  const int span = (threadIdx.x >> 5) * gridDim.x + blockIdx.x;
+  // Each lane adds up the tiles of its share of the requests.
+  const int per = (p.B + 31) / 32;
+  const int b_lo = min(lane * per, p.B), b_hi = min(b_lo + per, p.B);
+  long long mine = 0;
+  bool fine = true;
+  for (int b = b_lo; b < b_hi; ++b) {
+    const Request r = request(p, b);
+    fine &= r.ok;
+    mine += tiles_of<kRows>(p, r);
+  }
+  long long upto = mine;
+#pragma unroll
+  for (int s = 1; s < 32; s <<= 1) {
+    const long long v = __shfl_up_sync(0xffffffffu, upto, s);
+    if (lane >= s) upto += v;
+  }
+  const long long total = __shfl_sync(0xffffffffu, upto, 31);
+  if (span == 0) {  // for the combine kernel
+    long long at = upto - mine;
+    for (int b = b_lo; b < b_hi; ++b) {
+      p.start[b] = at;
+      at += tiles_of<kRows>(p, request(p, b));
+    }
+    if (lane == 31) p.start[p.B] = total;
+    if (!fine) atomicCAS(&g_attn4_status, kDevOk, kDevBadSeqlens);
+  }
+  const long long len = span_length(total, p.spans);
+  long long at = span * len;
+  const long long end = min(at + len, total);
+  if (at >= end) return;
+  // the request that holds tile `at`
+  const uint32_t holds = __ballot_sync(0xffffffffu, upto > at);
+  const int owner = __ffs(holds) - 1;
+  int b = __shfl_sync(0xffffffffu, b_lo, owner);
+  long long base = __shfl_sync(0xffffffffu, upto - mine, owner);
+  Request rq = request(p, b);
+  long long size = tiles_of<kRows>(p, rq);
+
+  Rows<D, NT> s;
+  while (at < end) {
+    while (at >= base + size) {
+      base += size;
+      rq = request(p, ++b);
+      size = tiles_of<kRows>(p, rq);
+    }
+    const int nt = key_tiles(rq), rt = row_tiles<kRows>(p, rq);
+    const long long rel = at - base;
+    const long long unit = rel / nt;
+    const int tile0 = static_cast<int>(rel - unit * nt);
+    const int h = static_cast<int>(unit / rt), row0 = static_cast<int>(unit - static_cast<long long>(h) * rt) * kRows;
+    const int n = static_cast<int>(min(static_cast<long long>(nt - tile0), end - at));
+    const int* row = p.table + b * p.table_stride;
+    const int pages = static_cast<int>((rq.Lk + ((1LL << p.cache.shift) - 1)) >> p.cache.shift);
+    Pages pg{0, -64};
+    TileRegs<D> t0, t1;
+    bool bad0, bad1 = false;
+    load_tile<D>(t0, tile_address<D>(pg, p, row, pages, h, tile0, lane, bad0), lane);
+    if (n > 1) load_tile<D>(t1, tile_address<D>(pg, p, row, pages, h, tile0 + 1, lane, bad1), lane);
+    start_unit<D, NT>(s, p, rq, h, row0, lane);
+    for (int i = 0; i < n; i += 2) {
+      int key0 = (tile0 + i) * kCacheTile;
+      step<D, NT>(s, t0, key0, bad0 ? 0 : min(rq.Lk - key0, kCacheTile), lane);
+      if (i + 2 < n) load_tile<D>(t0, tile_address<D>(pg, p, row, pages, h, tile0 + i + 2, lane, bad0), lane);
+      if (i + 1 < n) {
+        key0 += kCacheTile;
+        step<D, NT>(s, t1, key0, bad1 ? 0 : min(rq.Lk - key0, kCacheTile), lane);
+        if (i + 3 < n) load_tile<D>(t1, tile_address<D>(pg, p, row, pages, h, tile0 + i + 3, lane, bad1), lane);
+      }
+    }
+    // A unit that is whole goes out; else slot 0 of the span if the part
+    // began at the span's start, slot 1 if within it.
+    const int slot = n == nt ? -1 : 2 * span + (at == span * len ? 0 : 1);
+    end_unit<D, NT>(s, p, rq, h, row0, slot, lane);
+    at += n;
+  }
+}
+
+// Join the partial results of the units that several spans share, in span
+// order, and write the rows that see no key.  One CTA per query row of a
+// unit; its warps take every fourth span, then warp 0 adds the four sums.
+template <int D, int ROWS>
+__global__ void __launch_bounds__(128) fa2_kv4_combine_kernel(const Attn4Problem p, int max_row_tiles) {
+  griddep_wait();
+  griddep_launch_dependents();
+  __shared__ float s_o[4][D];
+  __shared__ float s_m[4], s_l[4];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int id = blockIdx.x;
+  const int local = id % ROWS;
+  id /= ROWS;
+  const int rt = id % max_row_tiles;
+  id /= max_row_tiles;
+  const int h = id % p.cache.heads, b = id / p.cache.heads;
+  const Request rq = request(p, b);
+  const int r = rt * ROWS + local;
+  if (!rq.ok || r >= p.G * rq.Lq) return;
+  const int i0 = r / p.G;
+  const long long tok = rq.q0 + i0;
+  const int head = h * p.G + (r - i0 * p.G);
+  __nv_bfloat16* dst = p.o + (tok * p.H + head) * D;
+  float* lse = p.lse + static_cast<long long>(head) * p.total_q + tok;
+  if (rq.Lk == 0) {
+    for (int c = threadIdx.x; c < D; c += 128) dst[c] = __float2bfloat16_rn(0.f);
+    if (threadIdx.x == 0) *lse = -INFINITY;
+    return;
+  }
+  const int nt = key_tiles(rq);
+  const long long len = span_length(p.start[p.B], p.spans);
+  const long long first = p.start[b] + (static_cast<long long>(h) * row_tiles<ROWS>(p, rq) + rt) * nt;
+  const long long s0 = first / len, s1 = (first + nt - 1) / len;
+  if (s0 == s1) return;  // one warp had it whole
+  auto slot = [&](long long s) { return (2 * s + (s == s0 && first != s * len ? 1 : 0)) * ROWS + local; };
+  constexpr int kCols = D >= 32 ? D / 32 : 1;
+  float m = kNoMax, l = 0.f, o[kCols];
+#pragma unroll
+  for (int k = 0; k < kCols; ++k) o[k] = 0.f;
+  const bool active = lane * kCols < D;
+  for (long long s = s0 + warp; s <= s1; s += 4) {
+    const long long at = slot(s);
+    const float2 ml = p.part_ml[at];
+    float v[kCols];
+#pragma unroll
+    for (int k = 0; k < kCols; ++k) v[k] = active ? p.part[at * D + lane * kCols + k] : 0.f;
+    const float top = fmaxf(m, ml.x), a = ex2_approx(m - top), e = ex2_approx(ml.x - top);
+    m = top;
+    l = l * a + ml.y * e;
+#pragma unroll
+    for (int k = 0; k < kCols; ++k) o[k] = o[k] * a + v[k] * e;
+  }
+#pragma unroll
+  for (int k = 0; k < kCols; ++k)
+    if (active) s_o[warp][lane * kCols + k] = o[k];
+  if (lane == 0) s_m[warp] = m, s_l[warp] = l;
+  __syncthreads();
+  if (threadIdx.x >= D) return;
+  float top = fmaxf(fmaxf(s_m[0], s_m[1]), fmaxf(s_m[2], s_m[3])), sum = 0.f, v = 0.f;
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    const float e = ex2_approx(s_m[w] - top);
+    sum += s_l[w] * e;
+    v += s_o[w][threadIdx.x] * e;
+  }
+  dst[threadIdx.x] = __float2bfloat16_rn(sum == 0.f ? 0.f : v * (p.v_scale / sum));
+  if (threadIdx.x == 0) *lse = sum == 0.f ? -INFINITY : row_lse(top, sum);
+}
+
+// Warps of the whole GPU: as many as are resident at once, so that the spans
+// are one wave.
+constexpr int kCtas1 = 4, kCtas2 = 2;  // resident CTAs per SM, 8 and 16 rows
+constexpr int kSpans1 = 152 * kCtas1 * kWarps, kSpans2 = 152 * kCtas2 * kWarps;
+
+// 16 rows a unit when 8 would read the cache twice.
+inline bool wide_rows(long long rows) { return rows > 8; }
+
+template <int D, int NT>
+int launch_attn_d(Attn4Problem p, long long max_rows, cudaStream_t st) {
+  constexpr int kCtas = NT == 1 ? kCtas1 : kCtas2, kRows = 8 * NT;
+  p.spans = NT == 1 ? kSpans1 : kSpans2;
+  if (int e = launch_pdl(fa2_kv4_attn_kernel<D, NT, kCtas>, dim3(152 * kCtas), dim3(kWarps * 32), 0, st, p)) return e;
+  const int rt = static_cast<int>((max_rows + kRows - 1) / kRows);
+  return launch_pdl(fa2_kv4_combine_kernel<D, kRows>,
+                    dim3(static_cast<unsigned>(static_cast<long long>(p.B) * p.cache.heads * rt * kRows)), dim3(128), 0, st, p,
+                    rt);
+}
+
+template <int D>
+int launch_attn(const Attn4Problem& p, long long max_rows, cudaStream_t st) {
+  return wide_rows(max_rows) ? launch_attn_d<D, 2>(p, max_rows, st) : launch_attn_d<D, 1>(p, max_rows, st);
+}
+
+size_t attn_slots(bool wide) { return wide ? static_cast<size_t>(kSpans2) * 2 * 16 : static_cast<size_t>(kSpans1) * 2 * 8; }
+
+int check_attn_sizes(int B, int H, int H_kv, int total_q, int max_q, int d) {
+  if (B < 1 || H < 1 || total_q < 0 || max_q < 0 || total_q > (1 << 30) || max_q > total_q || (total_q > 0 && max_q < 1))
+    return FA2_ERR_SHAPE;
+  if (!head_dim_ok(d)) return FA2_ERR_HEADDIM;
+  if (int rc = check_heads(H, H_kv)) return rc;
+  // combine grid: a CTA per row, rounded up to whole units
+  const long long rows = (static_cast<long long>(H / H_kv) * max_q + 15) / 16 * 16;
+  if (rows > (1LL << 30) || static_cast<double>(B) * H_kv * rows > 2147483647.0) return FA2_ERR_SHAPE;
+  return FA2_OK;
+}
+
+}  // namespace
+
+int read_attn4_status(int* value, bool reset) {
+  if (cudaError_t e = cudaMemcpyFromSymbol(value, g_attn4_status, sizeof(int))) return static_cast<int>(e);
+  if (reset) {
+    const int zero = 0;
+    if (cudaError_t e = cudaMemcpyToSymbol(g_attn4_status, &zero, sizeof(int))) return static_cast<int>(e);
+  }
+  return 0;
+}
+
+}  // namespace fa2
+
+using namespace fa2;
+
+extern "C" {
+
+size_t fa2_kv4_attn_workspace_bytes(int B, int H, int H_kv, int max_seqlen_q, int d) {
+  if (max_seqlen_q < 1 || check_attn_sizes(B, H, H_kv, max_seqlen_q, max_seqlen_q, d) != FA2_OK) return 0;
+  const size_t rows = attn_slots(wide_rows(static_cast<long long>(H / H_kv) * max_seqlen_q));
+  return round_up(rows * d * sizeof(float)) + round_up(rows * sizeof(float2)) +
+         round_up((static_cast<size_t>(B) + 1) * sizeof(long long));
+}
+
+int fa2_kv4_attn(const void* q, const void* cache, long long page_stride, const int* block_table, long long table_stride,
+                 const int* lens, const int* cu_seqlens_q, void* o, float* lse, int B, int H, int H_kv, int total_q,
+                 int max_seqlen_q, int num_pages, int page_size, int table_width, int d, float scale, float k_scale,
+                 float v_scale, int causal, void* workspace, size_t workspace_bytes, void* stream) {
+  if (int rc = check_attn_sizes(B, H, H_kv, total_q, max_seqlen_q, d)) return rc;
+  if (int rc = check_cache(cache, page_stride, num_pages, page_size, H_kv, d)) return rc;
+  if (table_width < 1 || table_width > (1 << 26) || (B > 1 && table_stride < table_width)) return FA2_ERR_SHAPE;
+  if (!cu_seqlens_q && total_q != 0 && static_cast<long long>(B) * max_seqlen_q != total_q) return FA2_ERR_SHAPE;
+  if (check_scale(scale) || !power_of_two(k_scale) || !power_of_two(v_scale) || check_scale(scale * k_scale))
+    return FA2_ERR_SCALE;
+  if (total_q == 0) return FA2_OK;
+  if (!q || !block_table || !lens || !o || !lse) return FA2_ERR_NULL;
+  if (!aligned(q, 16) || !aligned(o, 16) || !aligned(block_table, 4) || !aligned(lens, 4) || !aligned(cu_seqlens_q, 4) ||
+      !aligned(lse, 4))
+    return FA2_ERR_ALIGN;
+  const size_t need = fa2_kv4_attn_workspace_bytes(B, H, H_kv, max_seqlen_q, d);
+  if (!workspace || !aligned(workspace, kWsAlign) || workspace_bytes < need) return FA2_ERR_WORKSPACE;
+  const size_t qb = static_cast<size_t>(total_q) * H * d * 2;
+  const size_t tb = (static_cast<size_t>(B - 1) * (B > 1 ? table_stride : 0) + table_width) * 4;
+  const Range outs[] = {range_of(o, qb), range_of(lse, static_cast<size_t>(total_q) * H * 4), range_of(workspace, need)};
+  const Range ins[] = {range_of(q, qb), range_of(cache, cache_span(page_stride, num_pages, page_size, H_kv, d)),
+                       range_of(block_table, tb), range_of(lens, static_cast<size_t>(B) * 4),
+                       range_of(cu_seqlens_q, cu_seqlens_q ? static_cast<size_t>(B + 1) * 4 : 0)};
+  for (int i = 0; i < 3; ++i) {
+    for (const Range& r : ins)
+      if (r.lo != r.hi && overlap(outs[i], r)) return FA2_ERR_ALIAS;
+    for (int j = i + 1; j < 3; ++j)
+      if (overlap(outs[i], outs[j])) return FA2_ERR_ALIAS;
+  }
+  const long long max_rows = static_cast<long long>(H / H_kv) * max_seqlen_q;
+  const size_t rows = attn_slots(wide_rows(max_rows));
+  Attn4Problem p{};
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.o = static_cast<__nv_bfloat16*>(o);
+  p.lse = lse;
+  p.cache = paged_cache(cache, page_stride, num_pages, page_size, H_kv);
+  p.table = block_table;
+  p.table_stride = table_stride;
+  p.lens = lens;
+  p.cu_q = cu_seqlens_q;
+  char* ws = static_cast<char*>(workspace);
+  p.part = reinterpret_cast<float*>(ws);
+  ws += round_up(rows * d * sizeof(float));
+  p.part_ml = reinterpret_cast<float2*>(ws);
+  ws += round_up(rows * sizeof(float2));
+  p.start = reinterpret_cast<long long*>(ws);
+  p.B = B;
+  p.H = H;
+  p.G = H / H_kv;
+  p.total_q = total_q;
+  p.uniform_q = max_seqlen_q;
+  p.max_q = max_seqlen_q;
+  p.width = table_width;
+  p.scale_log2 = scale * k_scale * 1.44269504088896341f;
+  p.v_scale = v_scale;
+  p.causal = causal != 0;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const int e = d == 16    ? launch_attn<16>(p, max_rows, st)
+                : d == 32  ? launch_attn<32>(p, max_rows, st)
+                : d == 64  ? launch_attn<64>(p, max_rows, st)
+                           : launch_attn<128>(p, max_rows, st);
+  return e ? record_cuda_failure(e, "kv4 attention launch") : FA2_OK;
+}
+
+}  // extern "C"

@@ -161,5 +161,9 @@ int record_cuda_failure(int cuda_code, const char* where);
 // unreadable (changes after cudaDeviceReset).
 unsigned long long current_context_id();
 int read_bwd_status(int* value, bool reset);
+int read_norm_status(int* value, bool reset);
+int read_plan_status(int* value, bool reset);
+int read_cache_status(int* value, bool reset);
+int read_attn4_status(int* value, bool reset);
 
 }  // namespace fa2

@@ -23,6 +23,7 @@ enum DeviceStatus : int {
   kDevSmemMisaligned = 2,
   kDevBadSeqlens = 3,  // cu_seqlens not non-decreasing within [0, total] or a length above the stated maximum
   kDevBadSchedule = 4,  // the hardware scheduler returned a block index outside the grid
+  kDevBadIndex = 5,  // a page id, cache slot or rotation position outside its range
 };
 
 // ---------------------------------------------------------------- generic
