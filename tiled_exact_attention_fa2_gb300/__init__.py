@@ -588,91 +588,112 @@ def fa2_step_from_host(host: dict, causal: bool = True, scale: Optional[float] =
 
 
 # --------------------------------------------------------------- around the attention: norm + rotation, paged 4-bit cache
-def _rows4(t, name: str):
-    """q / k as [B, heads, N, d] with any strides: a 4-D tensor as it is, a packed [total, heads, d] one as B = 1."""
-    if t.dtype != torch.bfloat16 or not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA bfloat16 tensor")
-    if t.dim() == 3:
-        t = t.transpose(0, 1).unsqueeze(0)
-    elif t.dim() != 4:
-        raise ValueError(f"{name} must be [B, heads, N, d] or packed [total, heads, d], got {tuple(t.shape)}")
-    if t.shape[3] > 1 and t.stride(3) != 1:
-        raise ValueError(f"{name}'s last dimension must be contiguous")
-    return t
-
-
-def _strides(*tensors):
-    vals = [s for t in tensors for s in t.stride()[:3]]
-    return (_ll * len(vals))(*vals)
-
-
-def _ints(t, name: str, device, dtype=torch.int32, dim: int = 1):
-    if t.dtype != dtype or t.device != device or t.dim() != dim or (t.shape[-1] > 1 and t.stride(-1) != 1):
-        raise ValueError(f"{name} must be a contiguous {dim}-D {dtype} tensor on {device}")
-    return t
+# These calls are made once per layer and decoding step, where the kernels take
+# a few microseconds: the checks read each tensor's metadata once, and the
+# stream handle comes from torch without a Stream object.
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
 class _on:
-    """For one call: `device` current, and the call's stream torch's current one, so that what the call allocates
-    belongs to the stream that uses it.  Gives the stream's handle."""
+    """`device` current, and the given stream torch's current one, so that what a call allocates belongs to the stream
+    that uses it."""
 
     def __init__(self, device, stream):
-        self.device, self.stream, self.guards = device, stream, ()
+        self.guards = [torch.cuda.device(device)]
+        if stream is not None:
+            if not isinstance(stream, torch.cuda.Stream):
+                stream = torch.cuda.ExternalStream(int(stream), device=device)
+            self.guards.append(torch.cuda.stream(stream))
 
     def __enter__(self):
-        if self.device.index != torch.cuda.current_device():
-            self.guards += (torch.cuda.device(self.device),)
-        if self.stream is not None:
-            s = self.stream
-            if not isinstance(s, torch.cuda.Stream):
-                s = torch.cuda.ExternalStream(int(s), device=self.device)
-            self.guards += (torch.cuda.stream(s),)
         for g in self.guards:
             g.__enter__()
-        return _stream(self.stream, self.device)
 
     def __exit__(self, *exc):
         for g in reversed(self.guards):
             g.__exit__(*exc)
 
 
-def _norm_args(q, k, q_weight, k_weight, rope, positions, interleaved):
-    """The checks and C arguments that the norm's two directions share; q and k as 4-D."""
-    packed = q.dim() == 3
-    q4, k4 = _rows4(q, "q"), _rows4(k, "k")
-    B, H, N, d = q4.shape
-    if k.dim() != q.dim() or (k4.shape[0], k4.shape[2], k4.shape[3]) != (B, N, d):
+def _away(device, stream) -> bool:
+    """Whether a call has to change the current device or stream first."""
+    return stream is not None or device.index != torch.cuda.current_device()
+
+
+def _rows(t, name: str, device):
+    """((B, heads, N, d), (batch, head, token) strides) of a bf16 [B, heads, N, d] tensor, or of a packed [total, heads,
+    d] one as B = 1."""
+    if t.dtype is not torch.bfloat16 or t.device != device:
+        raise ValueError(f"{name} must be bfloat16 on {device}")
+    shape, stride = t.shape, t.stride()
+    if len(shape) == 4:
+        B, h, N, d = shape
+        sb, sh, sn, sd = stride
+    elif len(shape) == 3:
+        (N, h, d), (sn, sh, sd), B, sb = shape, stride, 1, 0
+    else:
+        raise ValueError(f"{name} must be [B, heads, N, d] or packed [total, heads, d], got {tuple(shape)}")
+    if sd != 1 and d > 1:
+        raise ValueError(f"{name}'s last dimension must be contiguous")
+    return (B, h, N, d), (sb, sh, sn)
+
+
+def _ints(t, name: str, device, count: int, dtype=torch.int32):
+    if t.dtype is not dtype or t.device != device or t.dim() != 1 or t.shape[0] != count or (count > 1 and t.stride(0) != 1):
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of {count} entries on {device}")
+
+
+def _table(t, device):
+    """(rows, width, row stride) of an int32 block table."""
+    if t.dtype is not torch.int32 or t.device != device or t.dim() != 2:
+        raise ValueError(f"block_table must be an int32 [B, width] tensor on {device}")
+    (rows, width), (sr, sc) = t.shape, t.stride()
+    if width > 1 and sc != 1:
+        raise ValueError("block_table's rows must be contiguous")
+    return rows, width, sr
+
+
+def _gpu(t, name: str):
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return t.device
+
+
+def _norm_args(q, k, q_weight, k_weight, rope, positions, interleaved, dev):
+    """The checks and C arguments that the norm's two directions share: (dims, weights are fp32, strides of q and k)."""
+    (B, H, N, d), sq = _rows(q, "q", dev)
+    (Bk, Hkv, Nk, dk), sk = _rows(k, "k", dev)
+    if Bk != B or Nk != N or dk != d or k.dim() != q.dim():
         raise ValueError("k must have q's B, N and d")
-    dev = q.device
-    wts = [w for w in (q_weight, k_weight) if w is not None]
-    if any(w.dtype != wts[0].dtype for w in wts):
+    w32 = 0
+    for w in (q_weight, k_weight):
+        if w is not None:
+            if w.dtype is torch.float32:
+                w32 = 1
+            elif w.dtype is not torch.bfloat16:
+                raise ValueError("a weight must be bfloat16 or float32")
+            if w.shape != (d,) or w.device != dev or not w.is_contiguous():
+                raise ValueError("a weight must be a contiguous tensor of d values on q's device")
+    if q_weight is not None and k_weight is not None and q_weight.dtype is not k_weight.dtype:
         raise ValueError("q_weight and k_weight must have the same type")
-    for w in wts:
-        if w.dtype not in (torch.bfloat16, torch.float32) or tuple(w.shape) != (d,) or not w.is_contiguous():
-            raise ValueError("a weight must be a contiguous bfloat16 or float32 tensor of d values")
     rot = max_pos = 0
     if rope is not None:
-        if rope.dtype != torch.float32 or rope.dim() != 2 or not rope.is_contiguous():
-            raise ValueError("rope must be a contiguous float32 [max_positions, rot_dim] tensor")
+        if rope.dtype is not torch.float32 or rope.dim() != 2 or rope.device != dev or not rope.is_contiguous():
+            raise ValueError("rope must be a contiguous float32 [max_positions, rot_dim] tensor on q's device")
         max_pos, rot = rope.shape
     if positions is not None:
-        if positions.dtype != torch.int32 or not positions.is_contiguous() or tuple(positions.shape) != (
-                (N,) if packed else (B, N)):
-            raise ValueError("positions must be a contiguous int32 tensor, one per token")
-    for t in (k, rope, positions, *wts):
-        if t is not None and t.device != dev:
-            raise ValueError("all tensors must be on q's device")
-    return (packed, q4, k4, (B, H, k4.shape[1], N, d, rot, 1 if interleaved else 0, max_pos),
-            1 if wts and wts[0].dtype == torch.float32 else 0)
+        if (positions.dtype is not torch.int32 or positions.device != dev or not positions.is_contiguous()
+                or positions.shape != ((N,) if q.dim() == 3 else (B, N))):
+            raise ValueError("positions must be a contiguous int32 tensor, one per token, on q's device")
+    return (B, H, Hkv, N, d, rot, 1 if interleaved else 0, max_pos), w32, sq + sk
 
 
 def _norm_out(like, out, name: str):
-    """`out` checked against `like` (an input as given), or a new contiguous tensor; and its 4-D form."""
+    """(`out` checked against `like`, or a new contiguous tensor; its strides)."""
     if out is None:
         out = torch.empty(like.shape, dtype=torch.bfloat16, device=like.device)
-    elif out.shape != like.shape or out.device != like.device:
-        raise ValueError(f"{name} must have its input's shape and device")
-    return out, _rows4(out, name)
+    elif out.shape != like.shape:
+        raise ValueError(f"{name} must have its input's shape")
+    return out, _rows(out, name, like.device)[1]
 
 
 def _dp(t):
@@ -689,14 +710,16 @@ def fa2_qk_norm_rope(q, k, q_weight=None, k_weight=None, rope=None, positions=No
     ``positions`` int32 [B, N] (packed: [total]), default 0, 1, ...  Returns
     (q_out, k_out), new contiguous tensors unless given; q_out may be q.
     """
-    packed, q4, k4, dims, w32 = _norm_args(q, k, q_weight, k_weight, rope, positions, interleaved)
-    lib = load_library()
-    with _on(q.device, stream) as st:
-        q_out, qo4 = _norm_out(q, q_out, "q_out")
-        k_out, ko4 = _norm_out(k, k_out, "k_out")
-        rc = lib.fa2_qk_norm_rope(q.data_ptr(), k.data_ptr(), _dp(q_weight), _dp(k_weight), w32, _dp(rope),
-                                  _dp(positions), q_out.data_ptr(), k_out.data_ptr(), *dims, eps,
-                                  _strides(q4, k4, qo4, ko4), st)
+    dev = _gpu(q, "q")
+    if _away(dev, stream):
+        with _on(dev, stream):
+            return fa2_qk_norm_rope(q, k, q_weight, k_weight, rope, positions, eps, interleaved, q_out, k_out)
+    dims, w32, strides = _norm_args(q, k, q_weight, k_weight, rope, positions, interleaved, dev)
+    q_out, sq = _norm_out(q, q_out, "q_out")
+    k_out, sk = _norm_out(k, k_out, "k_out")
+    rc = load_library().fa2_qk_norm_rope(
+        q.data_ptr(), k.data_ptr(), _dp(q_weight), _dp(k_weight), w32, _dp(rope), _dp(positions), q_out.data_ptr(),
+        k_out.data_ptr(), *dims, eps, (_ll * 12)(*strides, *sq, *sk), _raw_stream(dev.index))
     if rc != FA2_OK:
         raise FA2Error("fa2_qk_norm_rope", rc)
     return q_out, k_out
@@ -707,27 +730,33 @@ def fa2_qk_norm_rope_bwd(dq_out, dk_out, q, k, q_weight=None, k_weight=None, rop
     """Gradient of fa2_qk_norm_rope: (dq, dk, dq_weight, dk_weight) from the gradients of its outputs.
 
     q and k are the forward call's inputs.  dq, dk are new contiguous tensors
-    unless given (dq may be dq_out or q).  The weights' gradients are fp32, None where
-    there is no weight.
+    unless given (dq may be dq_out or q).  The weights' gradients are fp32,
+    None where there is no weight.
     """
-    packed, q4, k4, dims, w32 = _norm_args(q, k, q_weight, k_weight, rope, positions, interleaved)
-    if dq_out.shape != q.shape or dk_out.shape != k.shape or dq_out.device != q.device or dk_out.device != q.device:
-        raise ValueError("dq_out and dk_out must have q's and k's shapes and device")
-    g4, h4 = _rows4(dq_out, "dq_out"), _rows4(dk_out, "dk_out")
+    dev = _gpu(q, "q")
+    if _away(dev, stream):
+        with _on(dev, stream):
+            return fa2_qk_norm_rope_bwd(dq_out, dk_out, q, k, q_weight, k_weight, rope, positions, eps, interleaved, dq, dk,
+                                        workspace)
+    dims, w32, strides = _norm_args(q, k, q_weight, k_weight, rope, positions, interleaved, dev)
+    if dq_out.shape != q.shape or dk_out.shape != k.shape:
+        raise ValueError("dq_out and dk_out must have q's and k's shapes")
+    grads = _rows(dq_out, "dq_out", dev)[1] + _rows(dk_out, "dk_out", dev)[1]
+    dq, sq = _norm_out(q, dq, "dq")
+    dk, sk = _norm_out(k, dk, "dk")
     d = dims[4]
     lib = load_library()
-    with _on(q.device, stream) as st:
-        dq, dq4 = _norm_out(q, dq, "dq")
-        dk, dk4 = _norm_out(k, dk, "dk")
-        dwq = None if q_weight is None else torch.empty(d, dtype=torch.float32, device=q.device)
-        dwk = None if k_weight is None else torch.empty(d, dtype=torch.float32, device=q.device)
-        if workspace is None and (dwq is not None or dwk is not None):
-            workspace = torch.empty(max(1, lib.fa2_qk_norm_rope_bwd_workspace_bytes(d)), dtype=torch.uint8, device=q.device)
-        rc = lib.fa2_qk_norm_rope_bwd(dq_out.data_ptr(), dk_out.data_ptr(), q.data_ptr(), k.data_ptr(), _dp(q_weight),
-                                      _dp(k_weight), w32, _dp(rope), _dp(positions), dq.data_ptr(), dk.data_ptr(),
-                                      _dp(dwq), _dp(dwk), *dims, eps, _strides(g4, h4, q4, k4, dq4, dk4),
-                                      _dp(workspace), 0 if workspace is None else workspace.numel() * workspace.element_size(),
-                                      st)
+    dwq = None if q_weight is None else torch.empty(d, dtype=torch.float32, device=dev)
+    dwk = None if k_weight is None else torch.empty(d, dtype=torch.float32, device=dev)
+    if workspace is not None:
+        if workspace.device != dev:
+            raise ValueError("workspace must be on q's device")
+    elif dwq is not None or dwk is not None:
+        workspace = torch.empty(max(1, lib.fa2_qk_norm_rope_bwd_workspace_bytes(d)), dtype=torch.uint8, device=dev)
+    rc = lib.fa2_qk_norm_rope_bwd(
+        dq_out.data_ptr(), dk_out.data_ptr(), q.data_ptr(), k.data_ptr(), _dp(q_weight), _dp(k_weight), w32, _dp(rope),
+        _dp(positions), dq.data_ptr(), dk.data_ptr(), _dp(dwq), _dp(dwk), *dims, eps, (_ll * 18)(*grads, *strides, *sq, *sk),
+        _dp(workspace), 0 if workspace is None else workspace.numel() * workspace.element_size(), _raw_stream(dev.index))
     if rc != FA2_OK:
         raise FA2Error("fa2_qk_norm_rope_bwd", rc)
     return dq, dk, dwq, dwk
@@ -747,32 +776,29 @@ def fa2_page_plan(cached_lens, new_lens, free_pages, block_table, page_size: int
                   plan: Optional[PagePlan] = None, stream=None) -> PagePlan:
     """One step's page plan from request lengths, on the GPU: fills the new entries of ``block_table``
     (int32 [B, width]) and returns the rest.  ``plan``: an earlier call's result to write into."""
-    dev = cached_lens.device
-    if not cached_lens.is_cuda:
-        raise ValueError("cached_lens must be a CUDA tensor")
-    for t, name in ((cached_lens, "cached_lens"), (new_lens, "new_lens"), (free_pages, "free_pages")):
-        _ints(t, name, dev)
-    _ints(block_table, "block_table", dev, dim=2)
-    B = cached_lens.numel()
-    if new_lens.numel() != B or block_table.shape[0] != B:
-        raise ValueError("cached_lens, new_lens and block_table must have one entry per request")
+    dev = _gpu(cached_lens, "cached_lens")
+    if _away(dev, stream):
+        with _on(dev, stream):
+            return fa2_page_plan(cached_lens, new_lens, free_pages, block_table, page_size, max_tokens, plan)
+    B, width, row_stride = _table(block_table, dev)
+    _ints(cached_lens, "cached_lens", dev, B)
+    _ints(new_lens, "new_lens", dev, B)
+    num_free = free_pages.numel()
+    _ints(free_pages, "free_pages", dev, num_free)
     if max_tokens < 0:
         raise ValueError("max_tokens must be at least 0")
-    if plan is not None:
-        sizes = (B, B + 1, B + 1, max_tokens, max_tokens, 1)
-        for t, name, n in zip(plan, PagePlan._fields, sizes):
-            _ints(t, name, dev, torch.int64 if name == "slots" else torch.int32)
-            if t.numel() != n:
-                raise ValueError(f"plan.{name} must have {n} entries")
-    lib = load_library()
-    with _on(dev, stream) as st:
-        if plan is None:
-            new = lambda n, dt=torch.int32: torch.empty(n, dtype=dt, device=dev)  # noqa: E731
-            plan = PagePlan(new(B), new(B + 1), new(B + 1), new(max_tokens, torch.int64), new(max_tokens), new(1))
-        rc = lib.fa2_page_plan(cached_lens.data_ptr(), new_lens.data_ptr(), _ptr(free_pages), block_table.data_ptr(),
-                               plan.lens.data_ptr(), plan.cu_new.data_ptr(), plan.cu_total.data_ptr(), _ptr(plan.slots),
-                               _ptr(plan.positions), plan.pages_needed.data_ptr(), B, free_pages.numel(),
-                               block_table.shape[1], block_table.stride(0), page_size, max_tokens, st)
+    if plan is None:
+        lens, cu_new, cu_total, positions, needed = torch.empty(
+            3 * B + 3 + max_tokens, dtype=torch.int32, device=dev).split_with_sizes((B, B + 1, B + 1, max_tokens, 1))
+        plan = PagePlan(lens, cu_new, cu_total, torch.empty(max_tokens, dtype=torch.int64, device=dev), positions, needed)
+    else:
+        for t, name, n in zip(plan, PagePlan._fields, (B, B + 1, B + 1, max_tokens, max_tokens, 1)):
+            _ints(t, "plan." + name, dev, n, torch.int64 if name == "slots" else torch.int32)
+    rc = load_library().fa2_page_plan(
+        cached_lens.data_ptr(), new_lens.data_ptr(), free_pages.data_ptr() if num_free else None, block_table.data_ptr(),
+        plan.lens.data_ptr(), plan.cu_new.data_ptr(), plan.cu_total.data_ptr(), plan.slots.data_ptr() if max_tokens else None,
+        plan.positions.data_ptr() if max_tokens else None, plan.pages_needed.data_ptr(), B, num_free, width, row_stride, page_size,
+        max_tokens, _raw_stream(dev.index))
     if rc != FA2_OK:
         raise FA2Error("fa2_page_plan", rc)
     return plan
@@ -790,35 +816,40 @@ def fa2_kv4_cache(num_pages: int, H_kv: int, page_size: int, d: int, device="cud
 
 
 def _cache_dims(cache):
-    if cache.dim() != 4 or cache.dtype != torch.uint8 or not cache.is_cuda or cache.shape[3] % 18 != 0:
+    """(pages, H_kv, page size, d, page stride in bytes) of a cache, whose pages may lie apart."""
+    if cache.dtype is not torch.uint8 or cache.dim() != 4:
         raise ValueError("cache must be a CUDA uint8 tensor [num_pages, H_kv, page_size / 16, 18 d] (fa2_kv4_cache)")
-    pages, heads, tiles, row = cache.shape
-    if (cache.stride(3) != 1 or (tiles > 1 and cache.stride(2) != row) or (heads > 1 and cache.stride(1) != tiles * row)):
-        raise ValueError("a page of the cache must be contiguous")
+    (pages, heads, tiles, row), (s0, s1, s2, s3) = cache.shape, cache.stride()
+    if row % 18 != 0 or s3 != 1 or (tiles > 1 and s2 != row) or (heads > 1 and s1 != tiles * row):
+        raise ValueError("a page of the cache must be contiguous, its last dimension 18 d")
     # (one page: its stride says nothing)
-    stride = cache.stride(0) if pages > 1 else heads * tiles * row
-    return pages, heads, tiles * 16, row // 18, stride
+    return pages, heads, tiles * 16, row // 18, s0 if pages > 1 else heads * tiles * row
 
 
 def fa2_kv4_append(k, v, cache, slots, k_scale: float = 1.0, v_scale: float = 1.0, k_out=None, v_out=None,
                    stream=None) -> None:
     """Write keys and values [T, H_kv, d] bf16 (any token and head strides) to their ``slots`` (int64 [T]) of the
     4-bit cache.  ``k_out``, ``v_out``: contiguous tensors that receive the values as stored."""
-    pages, heads, page_size, d, stride = _cache_dims(cache)
+    dev = _gpu(cache, "cache")
+    if _away(dev, stream):
+        with _on(dev, stream):
+            return fa2_kv4_append(k, v, cache, slots, k_scale, v_scale, k_out, v_out)
+    pages, heads, page_size, d, page_stride = _cache_dims(cache)
     T = slots.numel()
-    for t, name in ((k, "k"), (v, "v")):
-        if t.dtype != torch.bfloat16 or t.device != cache.device or tuple(t.shape) != (T, heads, d) or t.stride(2) != 1:
-            raise ValueError(f"{name} must be bfloat16 [tokens, H_kv, d] on the cache's device, its last dimension contiguous")
-    for t, name in ((k_out, "k_out"), (v_out, "v_out")):
-        if t is not None and (t.dtype != torch.bfloat16 or t.device != cache.device or t.shape != k.shape or not t.is_contiguous()):
-            raise ValueError(f"{name} must be a contiguous bfloat16 tensor of k's shape")
-    _ints(slots, "slots", cache.device, torch.int64)
-    lib = load_library()
-    strides = (_ll * 4)(k.stride(0), k.stride(1), v.stride(0), v.stride(1))
-    with _on(cache.device, stream) as st:
-        rc = lib.fa2_kv4_append(_ptr(k), _ptr(v), strides, cache.data_ptr(), stride, _ptr(slots),
-                                None if k_out is None else _ptr(k_out), None if v_out is None else _ptr(v_out), T, heads,
-                                pages, page_size, d, k_scale, v_scale, st)
+    _ints(slots, "slots", dev, T, torch.int64)
+    want = (T, heads, d)
+    (kt, kh, kd), (vt, vh, vd) = k.stride(), v.stride()
+    if (k.dtype is not torch.bfloat16 or v.dtype is not torch.bfloat16 or k.device != dev or v.device != dev
+            or k.shape != want or v.shape != want or kd != 1 or vd != 1):
+        raise ValueError("k and v must be bfloat16 [tokens, H_kv, d] on the cache's device, the last dimension contiguous")
+    for t in (k_out, v_out):
+        if t is not None and (t.dtype is not torch.bfloat16 or t.device != dev or t.shape != want or not t.is_contiguous()):
+            raise ValueError("k_out and v_out must be contiguous bfloat16 tensors of k's shape")
+    if T == 0:
+        return
+    rc = load_library().fa2_kv4_append(
+        k.data_ptr(), v.data_ptr(), (_ll * 4)(kt, kh, vt, vh), cache.data_ptr(), page_stride, slots.data_ptr(), _dp(k_out),
+        _dp(v_out), T, heads, pages, page_size, d, k_scale, v_scale, _raw_stream(dev.index))
     if rc != FA2_OK:
         raise FA2Error("fa2_kv4_append", rc)
 
@@ -827,23 +858,22 @@ def fa2_kv4_gather(cache, block_table, cu_seqlens, total: int, k_scale: float = 
                    v=None, stream=None):
     """The cache's keys and values as packed bf16 [total, H_kv, d] (what fa2_fwd_varlen takes as k and v with
     cu_seqlens_k = ``cu_seqlens``).  Rows outside every sequence of given k, v are left as they are."""
-    pages, heads, page_size, d, stride = _cache_dims(cache)
-    dev = cache.device
-    _ints(block_table, "block_table", dev, dim=2)
-    _ints(cu_seqlens, "cu_seqlens", dev)
-    B = block_table.shape[0]
-    if cu_seqlens.numel() != B + 1:
-        raise ValueError("cu_seqlens must have one entry more than block_table has rows")
-    for t, name in ((k, "k"), (v, "v")):
-        if t is not None and (t.device != dev or _packed(t, name) != (total, heads, d)):
-            raise ValueError(f"{name} must be [total, H_kv, d] on the cache's device")
-    lib = load_library()
-    with _on(dev, stream) as st:
-        k = torch.empty((total, heads, d), dtype=torch.bfloat16, device=dev) if k is None else k
-        v = torch.empty((total, heads, d), dtype=torch.bfloat16, device=dev) if v is None else v
-        rc = lib.fa2_kv4_gather(cache.data_ptr(), stride, block_table.data_ptr(), block_table.stride(0),
-                                cu_seqlens.data_ptr(), _ptr(k), _ptr(v), B, heads, total, pages, page_size,
-                                block_table.shape[1], d, k_scale, v_scale, st)
+    dev = _gpu(cache, "cache")
+    if _away(dev, stream):
+        with _on(dev, stream):
+            return fa2_kv4_gather(cache, block_table, cu_seqlens, total, k_scale, v_scale, k, v)
+    pages, heads, page_size, d, page_stride = _cache_dims(cache)
+    B, width, row_stride = _table(block_table, dev)
+    _ints(cu_seqlens, "cu_seqlens", dev, B + 1)
+    for t in (k, v):
+        if t is not None and (t.device != dev or t.dtype is not torch.bfloat16 or t.shape != (total, heads, d)
+                              or not t.is_contiguous()):
+            raise ValueError("k and v must be contiguous bfloat16 [total, H_kv, d] on the cache's device")
+    k = torch.empty((total, heads, d), dtype=torch.bfloat16, device=dev) if k is None else k
+    v = torch.empty((total, heads, d), dtype=torch.bfloat16, device=dev) if v is None else v
+    rc = load_library().fa2_kv4_gather(
+        cache.data_ptr(), page_stride, block_table.data_ptr(), row_stride, cu_seqlens.data_ptr(), _ptr(k), _ptr(v), B, heads,
+        total, pages, page_size, width, d, k_scale, v_scale, _raw_stream(dev.index))
     if rc != FA2_OK:
         raise FA2Error("fa2_kv4_gather", rc)
     return k, v
@@ -865,43 +895,41 @@ def fa2_kv4_attn(q, cache, block_table, lens, cu_seqlens_q=None, max_seqlen_q: O
     ``max_seqlen_q`` queries (default: total_q / B).  With cu_seqlens_q and no
     max_seqlen_q the maximum is read from the offsets (a device sync).
     """
-    pages, heads, page_size, d, stride = _cache_dims(cache)
-    dev = cache.device
-    tq, H, dq = _packed(q, "q")
-    if dq != d or q.device != dev:
-        raise ValueError("q must have the cache's head dim and device")
-    _ints(block_table, "block_table", dev, dim=2)
-    _ints(lens, "lens", dev)
-    B = block_table.shape[0]
-    if lens.numel() != B:
-        raise ValueError("lens must have one entry per row of block_table")
+    dev = _gpu(cache, "cache")
+    if _away(dev, stream):
+        with _on(dev, stream):
+            return fa2_kv4_attn(q, cache, block_table, lens, cu_seqlens_q, max_seqlen_q, o, lse, workspace, scale, k_scale,
+                                v_scale, causal)
+    pages, heads, page_size, d, page_stride = _cache_dims(cache)
+    if q.dim() != 3 or q.dtype is not torch.bfloat16 or q.device != dev or not q.is_contiguous() or q.shape[2] != d:
+        raise ValueError("q must be contiguous bfloat16 [total_q, H, d] on the cache's device, with its head dim")
+    tq, H, _ = q.shape
+    B, width, row_stride = _table(block_table, dev)
+    _ints(lens, "lens", dev, B)
     if cu_seqlens_q is not None:
-        _ints(cu_seqlens_q, "cu_seqlens_q", dev)
-        if cu_seqlens_q.numel() != B + 1:
-            raise ValueError("cu_seqlens_q must have one entry more than block_table has rows")
+        _ints(cu_seqlens_q, "cu_seqlens_q", dev, B + 1)
         mq = _max_len(cu_seqlens_q, max_seqlen_q)
     else:
         mq = tq // B if max_seqlen_q is None else int(max_seqlen_q)
         if mq * B != tq:
             raise ValueError("without cu_seqlens_q every request has the same number of queries")
-    if o is not None and (o.device != dev or _packed(o, "o") != (tq, H, d)):
-        raise ValueError("o must have q's shape and device")
-    if lse is not None and (lse.dtype != torch.float32 or lse.device != dev or not lse.is_contiguous()
-                            or tuple(lse.shape) != (H, tq)):
+    if o is None:
+        o = torch.empty((tq, H, d), dtype=torch.bfloat16, device=dev)
+    elif o.shape != q.shape or o.dtype is not torch.bfloat16 or o.device != dev or not o.is_contiguous():
+        raise ValueError("o must be contiguous bfloat16 with q's shape and device")
+    if lse is None:
+        lse = torch.empty((H, tq), dtype=torch.float32, device=dev)
+    elif lse.dtype is not torch.float32 or lse.device != dev or not lse.is_contiguous() or lse.shape != (H, tq):
         raise ValueError("lse must be a contiguous fp32 [H, total_q] tensor")
-    if workspace is not None and workspace.device != dev:
-        raise ValueError("workspace must be on the cache's device")
     lib = load_library()
-    with _on(dev, stream) as st:
-        o = torch.empty_like(q) if o is None else o
-        lse = torch.empty((H, tq), dtype=torch.float32, device=dev) if lse is None else lse
-        if workspace is None:
-            workspace = torch.empty(max(1, lib.fa2_kv4_attn_workspace_bytes(B, H, heads, mq, d)), dtype=torch.uint8,
-                                    device=dev)
-        rc = lib.fa2_kv4_attn(_ptr(q), cache.data_ptr(), stride, block_table.data_ptr(), block_table.stride(0),
-                              lens.data_ptr(), _dp(cu_seqlens_q), _ptr(o), _ptr(lse), B, H, heads, tq, mq, pages,
-                              page_size, block_table.shape[1], d, _scale(scale, d), k_scale, v_scale,
-                              1 if causal else 0, workspace.data_ptr(), workspace.numel() * workspace.element_size(), st)
+    if workspace is None:
+        workspace = torch.empty(max(1, lib.fa2_kv4_attn_workspace_bytes(B, H, heads, mq, d)), dtype=torch.uint8, device=dev)
+    elif workspace.device != dev:
+        raise ValueError("workspace must be on the cache's device")
+    rc = lib.fa2_kv4_attn(
+        _ptr(q), cache.data_ptr(), page_stride, block_table.data_ptr(), row_stride, lens.data_ptr(), _dp(cu_seqlens_q), _ptr(o),
+        _ptr(lse), B, H, heads, tq, mq, pages, page_size, width, d, _scale(scale, d), k_scale, v_scale, 1 if causal else 0,
+        workspace.data_ptr(), workspace.numel() * workspace.element_size(), _raw_stream(dev.index))
     if rc != FA2_OK:
         raise FA2Error("fa2_kv4_attn", rc)
     return o, lse
