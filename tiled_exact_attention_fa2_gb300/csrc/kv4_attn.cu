@@ -10,9 +10,9 @@
 // have to be written to shared memory in 16 bits first, 3.6 times the bytes
 // that come in, for 128-row tiles of which a decoding step fills 1 to 16.
 //
-// Work.  A unit is (request, K/V head, 8 NT query rows), its keys 16-key
-// tiles; row r of a unit is query r / G, head r % G of the group.  All
-// units' tiles form one line, which is cut into equal spans, one for each
+// Work.  A unit is (request, K/V head, 8 NT query rows), its keys pairs of
+// 16-key tiles; row r of a unit is query r / G, head r % G of the group.  All
+// units' pairs form one line, which is cut into equal spans, one for each
 // warp: every warp reads as many bytes as any other, whatever the lengths.
 // A unit inside one span is finished by its warp; one that spans share leaves
 // a partial result per span (unnormalised O, running maximum and sum), which
@@ -59,7 +59,8 @@ constexpr int kWarps = 4;  // warps of a CTA
 constexpr float kNoMax = -1.7e38f;  // running maximum of a row that has seen no key (finite: no inf - inf)
 constexpr float kLift = 11.f;   // weights are held 2^11 up
 constexpr float kLag = 4.f;     // a score may pass the running maximum by 2^4
-constexpr int kMinTiles = 4;    // shortest span: below, a partial result costs more than its tiles
+constexpr int kMinPairs = 2;    // shortest span: below, a partial result costs more than its keys
+constexpr int kPair = 2, kPairKeys = kPair * kCacheTile;  // tiles and keys of a step
 
 struct Attn4Problem {
   const __nv_bfloat16* q;
@@ -72,7 +73,7 @@ struct Attn4Problem {
   const int* cu_q;    // or NULL: every request has uniform_q queries
   float* part;        // [2 * spans][rows][d] unnormalised O
   float2* part_ml;    // [2 * spans][rows] maximum (log2), sum
-  long long* start;   // [B + 1] first tile of each request on the line
+  long long* start;   // [B + 1] first tile pair of each request on the line
   int B, H, G, total_q, uniform_q, max_q, width;
   int spans;
   float scale_log2, v_scale;
@@ -104,16 +105,16 @@ template <int ROWS>
 __device__ __forceinline__ int row_tiles(const Attn4Problem& p, const Request& r) {
   return static_cast<int>((static_cast<long long>(p.G) * r.Lq + ROWS - 1) / ROWS);
 }
-__device__ __forceinline__ int key_tiles(const Request& r) { return (r.Lk + kCacheTile - 1) / kCacheTile; }
+__device__ __forceinline__ int key_pairs(const Request& r) { return (r.Lk + kPairKeys - 1) / kPairKeys; }
 
 template <int ROWS>
-__device__ __forceinline__ long long tiles_of(const Attn4Problem& p, const Request& r) {
-  return r.ok ? static_cast<long long>(p.cache.heads) * row_tiles<ROWS>(p, r) * key_tiles(r) : 0;
+__device__ __forceinline__ long long pairs_of(const Attn4Problem& p, const Request& r) {
+  return r.ok ? static_cast<long long>(p.cache.heads) * row_tiles<ROWS>(p, r) * key_pairs(r) : 0;
 }
 
 __device__ __forceinline__ long long span_length(long long total, int spans) {
   const long long s = (total + spans - 1) / spans;
-  return s < kMinTiles ? kMinTiles : s;
+  return s < kMinPairs ? kMinPairs : s;
 }
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -121,67 +122,74 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], u
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+__device__ __forceinline__ void mma_f16_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
   uint32_t r;
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
   return r;
 }
 
-// One tile's codes and scales of this lane.
-template <int D>
-struct TileRegs {
-  static constexpr int kW = D >= 32 ? D / 32 : 1;  // words of one load
-  uint32_t k[2][kW], v[2][kW], ks, vs;
-};
-
 template <int N>
-__device__ __forceinline__ void load_words(uint32_t (&w)[N], const char* p) {
+__device__ __forceinline__ void load_words(uint32_t (&w)[N], uint32_t p) {
   if constexpr (N == 4) {
-    asm volatile("ld.global.nc.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                 : "l"(p));
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(p));
   } else if constexpr (N == 2) {
-    asm volatile("ld.global.nc.L1::no_allocate.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "l"(p));
+    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(p));
   } else {
-    asm volatile("ld.global.nc.L1::no_allocate.b32 %0, [%1];" : "=r"(w[0]) : "l"(p));
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[0]) : "r"(p));
   }
 }
-__device__ __forceinline__ uint32_t load_half(const char* p) {
+__device__ __forceinline__ uint32_t load_half(uint32_t p) {
   uint16_t h;
-  asm volatile("ld.global.nc.L1::no_allocate.b16 %0, [%1];" : "=h"(h) : "l"(p));
+  asm volatile("ld.shared.b16 %0, [%1];" : "=h"(h) : "r"(p));
   return h;
 }
 
+// A lane's codes (of K at 0, of V at kV) and scales of a tile in shared
+// memory, as the tile lies in the cache: every load takes consecutive lanes'
+// consecutive pieces, so none has a bank conflict.
 template <int D>
-__device__ __forceinline__ void load_tile(TileRegs<D>& t, const char* tile, int lane) {
-  using L = Kv4<D>;
+constexpr int kWords = D >= 32 ? D / 32 : 1;  // of one load
+
+template <int D>
+__device__ __forceinline__ void load_codes(uint32_t (&w)[2][kWords<D>], uint32_t at, int lane) {
   constexpr int kB = D / 8;  // bytes of a lane's piece
-  const int g = lane >> 2, c = lane & 3;
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    if constexpr (kB == 2) {
-      t.k[i][0] = load_half(tile + i * 32 * kB + lane * kB);
-      t.v[i][0] = load_half(tile + L::kV + i * 32 * kB + lane * kB);
-    } else {
-      load_words(t.k[i], tile + i * 32 * kB + lane * kB);
-      load_words(t.v[i], tile + L::kV + i * 32 * kB + lane * kB);
-    }
+    if constexpr (kB == 2)
+      w[i][0] = load_half(at + i * 32 * kB + lane * kB);
+    else
+      load_words(w[i], at + i * 32 * kB + lane * kB);
   }
-  uint32_t w[1];
+}
+template <int D>
+__device__ __forceinline__ uint32_t load_k_scales(uint32_t tile, int lane) {
+  using L = Kv4<D>;
+  const int g = lane >> 2, c = lane & 3;
   if constexpr (D == 128) {  // groups 2 c, 2 c + 1 of keys g, g + 8
+    uint32_t w[1];
     load_words(w, tile + L::kKS + lane * 4);
-    t.ks = w[0];
+    return w[0];
   } else {
-    t.ks = load_half(tile + L::kKS + (g * L::kGroups + c * L::kGroups / 4) * 2);
+    return load_half(tile + L::kKS + (g * L::kGroups + c * L::kGroups / 4) * 2);
   }
-  load_words(w, tile + L::kVS + ((g * L::kGroups / 8) * 4 + c) * 4);
-  t.vs = w[0];
+}
+template <int D>
+__device__ __forceinline__ uint32_t load_v_scales(uint32_t tile, int lane) {
+  using L = Kv4<D>;
+  uint32_t w[1];
+  load_words(w, tile + L::kVS + (((lane >> 2) * L::kGroups / 8) * 4 + (lane & 3)) * 4);
+  return w[0];
 }
 
 // One warp's running state of a unit.
 template <int D, int NT>
 struct Rows {
-  uint32_t q[NT][D / 16][2];  // Q^T operand
+  uint32_t q;  // shared address of the lane's Q^T operand: 8 bytes at (row tile, step) x 256
   float o[NT][D / 16][4];
   float cs[NT][2], off[NT][2], l[NT][2];  // score factor, kLift - maximum, sum, of columns 2c, 2c + 1
   int vis[NT][2];                         // keys they see
@@ -236,8 +244,12 @@ __device__ __forceinline__ void start_unit(Rows<D, NT>& s, const Attn4Problem& p
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         const float2 f = unpack_bf16x2(w[2 * t + u]);
-        s.q[j][t][u] = pack_f16x2(f.x * down, f.y * down);
+        w[2 * t + u] = pack_f16x2(f.x * down, f.y * down);
       }
+#pragma unroll
+    for (int t = 0; t < D / 16; ++t)
+      asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(s.q + (j * (D / 16) + t) * 256), "r"(w[2 * t]), "r"(w[2 * t + 1])
+                   : "memory");
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       s.cs[j][u] = __shfl_sync(0xffffffffu, up, (2 * c + u) * 4);
@@ -265,86 +277,87 @@ __device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {
   return m;
 }
 
-// One 16-key tile at key0 into the unit's state.  `keys`: keys of the tile
-// that exist (a page id out of range leaves none).
-template <int D, int NT>
-__device__ __forceinline__ void step(Rows<D, NT>& s, const TileRegs<D>& t, int key0, int keys, int lane) {
+// Two 16-key tiles, keys key0 .., at `tiles` in shared memory, into the
+// unit's state: two, because their products are independent chains and the
+// step's fixed costs (wait, vote, branches) are shared.  Where some row does
+// not see all 32 keys (MASKED), a tile's keys are those below `end`, and none
+// where its bit of `bad` is set (a page id out of range); what shared memory
+// holds past them has no influence.
+template <int D, int NT, bool MASKED>
+__device__ __forceinline__ void step(Rows<D, NT>& s, uint32_t tiles, int key0, int end, uint32_t bad, int lane) {
   using L = Kv4<D>;
+  constexpr int kSteps = D / 16;
   const int g = lane >> 2, c = lane & 3;
-  uint32_t vs = t.vs;
-  uint32_t nan_keys = 0;  // keys of the tile with a NaN in this lane's columns of V
-  const bool masked = key0 + kCacheTile > s.min_vis || keys < kCacheTile;  // the same in all lanes
-  if (masked) {
-    // V of keys past the end counts as zeros, whatever the page holds; a NaN
-    // that some rows see is taken out of the product (0 x NaN would reach the
-    // rows that do not) and put into those rows afterwards.
-    uint32_t drop = 0, nan = nan_bytes(vs);
+  auto keys = [&](int i) { return bad >> i & 1 ? 0 : min(max(end - key0 - i * kCacheTile, 0), kCacheTile); };
+
+  float x[kPair][NT][4];
+  {
+    uint32_t k[kPair][2][kWords<D>], sa[kPair][2], sb[kPair][2];  // codes; scales of keys g and g + 8 for the lane's columns
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int key = (i >> 1) * 8 + 2 * c + (i & 1);
-      if (key >= keys) drop |= 1u << i;
-      else if (nan >> i & 1) nan_keys |= 1u << key, drop |= 1u << i;
+    for (int i = 0; i < kPair; ++i) {
+      load_codes<D>(k[i], tiles + i * L::kTileBytes, lane);
+      const uint32_t ks = load_k_scales<D>(tiles + i * L::kTileBytes, lane);
+      const uint32_t s0 = e4m3x2_to_f16(ks), s1 = D == 128 ? e4m3x2_to_f16(ks >> 16) : s0;
+      sa[i][0] = __byte_perm(s0, 0, 0x1010), sb[i][0] = __byte_perm(s0, 0, 0x3232);
+      sa[i][1] = __byte_perm(s1, 0, 0x1010), sb[i][1] = __byte_perm(s1, 0, 0x3232);
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (drop >> i & 1) vs &= ~(0xffu << (8 * i));
-    nan_keys |= __shfl_xor_sync(0xffffffffu, nan_keys, 1);
-    nan_keys |= __shfl_xor_sync(0xffffffffu, nan_keys, 2);
-  }
-
-  float x[NT][4];
-#pragma unroll
-  for (int j = 0; j < NT; ++j)
-#pragma unroll
-    for (int u = 0; u < 4; ++u) x[j][u] = 0.f;
-  {
-    // scales of keys g (low half) and g + 8 for the lane's columns
-    const uint32_t s0 = e4m3x2_to_f16(t.ks), s1 = D == 128 ? e4m3x2_to_f16(t.ks >> 16) : s0;
-    const uint32_t a0 = __byte_perm(s0, 0, 0x1010), b0 = __byte_perm(s0, 0, 0x3232);
-    const uint32_t a1 = __byte_perm(s1, 0, 0x1010), b1 = __byte_perm(s1, 0, 0x3232);
-    constexpr int kSteps = D / 16;
-#pragma unroll
     for (int w = 0; w < (kSteps + 1) / 2; ++w) {
-      uint32_t lo[4], hi[4];
-      e2m1x8_to_f16(t.k[0][w], lo);
-      e2m1x8_to_f16(t.k[1][w], hi);
-      const uint32_t sa = w >= 2 ? a1 : a0, sb = w >= 2 ? b1 : b0;
+      uint32_t q[NT][2][2];
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        if (2 * w + u < kSteps) {
-          const uint32_t a[4] = {hmul2(lo[2 * u], sa), hmul2(hi[2 * u], sb), hmul2(lo[2 * u + 1], sa),
-                                 hmul2(hi[2 * u + 1], sb)};
+      for (int j = 0; j < NT; ++j)
 #pragma unroll
-          for (int j = 0; j < NT; ++j) mma_f16(x[j], a, s.q[j][2 * w + u][0], s.q[j][2 * w + u][1]);
+        for (int u = 0; u < 2 && 2 * w + u < kSteps; ++u) load_words(q[j][u], s.q + (j * kSteps + 2 * w + u) * 256);
+#pragma unroll
+      for (int i = 0; i < kPair; ++i) {
+        uint32_t lo[4], hi[4];
+        e2m1x8_to_f16(k[i][0][w], lo);
+        e2m1x8_to_f16(k[i][1][w], hi);
+        const uint32_t a_s = sa[i][w >= 2], b_s = sb[i][w >= 2];
+#pragma unroll
+        for (int u = 0; u < 2 && 2 * w + u < kSteps; ++u) {
+          const uint32_t a[4] = {hmul2(lo[2 * u], a_s), hmul2(hi[2 * u], b_s), hmul2(lo[2 * u + 1], a_s),
+                                 hmul2(hi[2 * u + 1], b_s)};
+#pragma unroll
+          for (int j = 0; j < NT; ++j) {
+            if (w == 0 && u == 0)
+              mma_f16_first(x[i][j], a, q[j][u][0], q[j][u][1]);
+            else
+              mma_f16(x[i][j], a, q[j][u][0], q[j][u][1]);
+          }
         }
       }
     }
   }
-  // x[j][0], [1]: key g, columns 2c, 2c + 1; [2], [3]: key g + 8.
-  if (masked) {
+  // x[i][j][0], [1]: key g, columns 2c, 2c + 1; [2], [3]: key g + 8.
+  if constexpr (MASKED) {
+#pragma unroll
+    for (int i = 0; i < kPair; ++i)
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int key = g + (u >> 1) * 8;
+          if (key >= keys(i) || key0 + i * kCacheTile + key >= s.vis[j][u & 1]) x[i][j][u] = -INFINITY;
+        }
+  }
+  float y[kPair][NT][4], top = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < kPair; ++i)
 #pragma unroll
     for (int j = 0; j < NT; ++j)
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
-        const int key = g + (u >> 1) * 8;
-        if (key >= keys || key0 + key >= s.vis[j][u & 1]) x[j][u] = -INFINITY;
+        y[i][j][u] = fmaf(x[i][j][u], s.cs[j][u & 1], s.off[j][u & 1]);
+        top = fmaxf(top, y[i][j][u]);
       }
-  }
-  bool over = false;
-  float y[NT][4];
-#pragma unroll
-  for (int j = 0; j < NT; ++j)
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      y[j][u] = fmaf(x[j][u], s.cs[j][u & 1], s.off[j][u & 1]);
-      over |= y[j][u] > kLift + kLag;
-    }
-  if (__any_sync(0xffffffffu, over)) {
+  if (__builtin_expect(__any_sync(0xffffffffu, top > kLift + kLag), 0)) {
 #pragma unroll
     for (int j = 0; j < NT; ++j)
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        float mx = fmaxf(x[j][u], x[j][u + 2]) * s.cs[j][u];
+        float mx = fmaxf(x[0][j][u], x[0][j][u + 2]);
+        mx = fmaxf(mx, fmaxf(x[1][j][u], x[1][j][u + 2])) * s.cs[j][u];
 #pragma unroll
         for (int sh = 4; sh < 32; sh <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, sh));
         const float old = kLift - s.off[j][u], m = fmaxf(old, mx);
@@ -352,43 +365,69 @@ __device__ __forceinline__ void step(Rows<D, NT>& s, const TileRegs<D>& t, int k
         s.off[j][u] = kLift - m;
         s.l[j][u] *= down;
 #pragma unroll
-        for (int i = 0; i < D / 16; ++i) {
+        for (int i = 0; i < kSteps; ++i) {
           s.o[j][i][u] *= down;
           s.o[j][i][u + 2] *= down;
         }
-        y[j][u] = fmaf(x[j][u], s.cs[j][u], s.off[j][u]);
-        y[j][u + 2] = fmaf(x[j][u + 2], s.cs[j][u], s.off[j][u]);
+#pragma unroll
+        for (int i = 0; i < kPair; ++i) {
+          y[i][j][u] = fmaf(x[i][j][u], s.cs[j][u], s.off[j][u]);
+          y[i][j][u + 2] = fmaf(x[i][j][u + 2], s.cs[j][u], s.off[j][u]);
+        }
       }
   }
-  uint32_t pb[NT][2];
+  uint32_t pb[kPair][NT][2];
 #pragma unroll
-  for (int j = 0; j < NT; ++j) {
-    float e[4];
+  for (int i = 0; i < kPair; ++i)
 #pragma unroll
-    for (int u = 0; u < 4; ++u) e[u] = ex2_approx(y[j][u]);
-    s.l[j][0] += e[0] + e[2];
-    s.l[j][1] += e[1] + e[3];
-    pb[j][0] = transpose8x8(pack_f16x2(e[0], e[1]));
-    pb[j][1] = transpose8x8(pack_f16x2(e[2], e[3]));
-  }
-  {
+    for (int j = 0; j < NT; ++j) {
+      float e[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) e[u] = ex2_approx(y[i][j][u]);
+      s.l[j][0] += e[0] + e[2];
+      s.l[j][1] += e[1] + e[3];
+      pb[i][j][0] = transpose8x8(pack_f16x2(e[0], e[1]));
+      pb[i][j][1] = transpose8x8(pack_f16x2(e[2], e[3]));
+    }
+#pragma unroll
+  for (int i = 0; i < kPair; ++i) {
+    uint32_t v[2][kWords<D>];
+    load_codes<D>(v, tiles + i * L::kTileBytes + L::kV, lane);
+    uint32_t vs = load_v_scales<D>(tiles + i * L::kTileBytes, lane);
+    uint32_t nan_keys = 0;  // keys of the tile with a NaN in this lane's columns of V
+    if constexpr (MASKED) {
+      // V of keys past the end counts as zeros, whatever the page holds; a NaN
+      // that some rows see is taken out of the product (0 x NaN would reach the
+      // rows that do not) and put into those rows afterwards.
+      uint32_t drop = 0, nan = nan_bytes(vs);
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int key = (u >> 1) * 8 + 2 * c + (u & 1);
+        if (key >= keys(i)) drop |= 1u << u;
+        else if (nan >> u & 1) nan_keys |= 1u << key, drop |= 1u << u;
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (drop >> u & 1) vs &= ~(0xffu << (8 * u));
+      nan_keys |= __shfl_xor_sync(0xffffffffu, nan_keys, 1);
+      nan_keys |= __shfl_xor_sync(0xffffffffu, nan_keys, 2);
+    }
     const uint32_t s0 = e4m3x2_to_f16(vs), s1 = e4m3x2_to_f16(vs >> 16);  // keys 2c, 2c + 1; 2c + 8, 2c + 9
-    constexpr int kSteps = D / 16;
-    constexpr int kWords = D >= 64 ? D / 64 : 1;  // of one key's piece
+    constexpr int kPiece = D >= 64 ? D / 64 : 1;  // words of one key's piece
 #pragma unroll
-    for (int w = 0; w < kWords; ++w) {
+    for (int w = 0; w < kPiece; ++w) {
       // low / high codes of the two keys' bytes side by side
       uint32_t even[2][4], odd[2][4];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
+      for (int u = 0; u < 2; ++u) {
         uint32_t a, b;
         if constexpr (D >= 64) {
-          a = t.v[i][w], b = t.v[i][kWords + w];
+          a = v[u][w], b = v[u][kPiece + w];
         } else {
-          a = t.v[i][0], b = t.v[i][0] >> (D / 2);
+          a = v[u][0], b = v[u][0] >> (D / 2);
         }
-        e2m1x8_to_f16((a & 0x0f0f0f0fu) | ((b << 4) & 0xf0f0f0f0u), even[i]);
-        e2m1x8_to_f16(((a >> 4) & 0x0f0f0f0fu) | (b & 0xf0f0f0f0u), odd[i]);
+        e2m1x8_to_f16((a & 0x0f0f0f0fu) | ((b << 4) & 0xf0f0f0f0u), even[u]);
+        e2m1x8_to_f16(((a >> 4) & 0x0f0f0f0fu) | (b & 0xf0f0f0f0u), odd[u]);
       }
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
@@ -396,22 +435,22 @@ __device__ __forceinline__ void step(Rows<D, NT>& s, const TileRegs<D>& t, int k
           const uint32_t a[4] = {hmul2(even[0][u], s0), hmul2(odd[0][u], s0), hmul2(even[1][u], s1),
                                  hmul2(odd[1][u], s1)};
 #pragma unroll
-          for (int j = 0; j < NT; ++j) mma_f16(s.o[j][4 * w + u], a, pb[j][0], pb[j][1]);
+          for (int j = 0; j < NT; ++j) mma_f16(s.o[j][4 * w + u], a, pb[i][j][0], pb[i][j][1]);
         }
       }
     }
-  }
-  if (masked && __any_sync(0xffffffffu, nan_keys != 0)) {
+    if (MASKED && __any_sync(0xffffffffu, nan_keys != 0)) {
 #pragma unroll
-    for (int j = 0; j < NT; ++j)
+      for (int j = 0; j < NT; ++j)
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const int n = min(max(s.vis[j][u] - key0, 0), kCacheTile);
-        if (nan_keys & ((1u << n) - 1u)) {
+        for (int u = 0; u < 2; ++u) {
+          const int n = min(max(s.vis[j][u] - key0 - i * kCacheTile, 0), kCacheTile);
+          if (nan_keys & ((1u << n) - 1u)) {
 #pragma unroll
-          for (int i = 0; i < D / 16; ++i) s.o[j][i][u] = s.o[j][i][u + 2] = __uint_as_float(0x7fffffffu);
+            for (int t = 0; t < kSteps; ++t) s.o[j][t][u] = s.o[j][t][u + 2] = __uint_as_float(0x7fffffffu);
+          }
         }
-      }
+    }
   }
 }
 
@@ -474,39 +513,81 @@ __device__ __forceinline__ void end_unit(Rows<D, NT>& s, const Attn4Problem& p, 
     }
 }
 
-// The page ids of a unit's next 32 pages, one per lane.
-struct Pages {
-  int ids, first;
+// A warp's ring of two tile pairs in shared memory, filled by bulk copies, a
+// pair completing on its slot's mbarrier.  Every 32 pairs each lane looks one
+// of the next 32 up in the block table and keeps where it lies, so that a
+// pair's copy is one instruction of its lane (two where pages hold 16 tokens;
+// a larger page holds whole pairs, the last of a request perhaps with a tile
+// that has no key).
+struct Ring {
+  uint32_t tiles;        // shared address of slot 0
+  uint64_t* full;        // the two mbarriers
+  uint32_t slot, phase;  // next to be read, parity of its phase
+  // the request's pages and the lanes' pairs
+  const int* row;
+  const char* head;      // this head's part of page 0
+  int pages, first;      // first: the pair of lane 0
+  const char *a, *b;     // the lane's pair: its first (or only) copy, its second or NULL
+  uint32_t bad_a, bad_b; // lanes whose first / second tile has a page id out of range (copied from page 0, its keys left out)
+  uint32_t bad;          // the slots' bits: first and second tile of slot 0, of slot 1
 };
 
 template <int D>
-__device__ __forceinline__ const char* tile_address(Pages& pg, const Attn4Problem& p, const int* row, int pages, int h,
-                                                    int tile, int lane, bool& bad) {
-  const int per = p.cache.shift - 4;
-  const int idx = tile >> per;
-  if (idx >= pg.first + 32 || idx < pg.first) {
-    pg.first = idx;
-    pg.ids = idx + lane < pages ? __ldg(row + idx + lane) : 0;
+__device__ __forceinline__ void look_up(Ring& r, const Attn4Problem& p, int pair, int lane) {
+  constexpr int kBytes = Kv4<D>::kTileBytes;
+  const int per = p.cache.shift - 4, tile = (pair + lane) * kPair, idx = tile >> per;
+  const bool there = idx < r.pages, more = per == 0 && idx + 1 < r.pages;
+  int id = there ? __ldg(r.row + idx) : 0, id2 = more ? __ldg(r.row + idx + 1) : 0;
+  const bool bad = static_cast<uint32_t>(id) >= static_cast<uint32_t>(p.cache.num_pages);
+  const bool bad2 = static_cast<uint32_t>(id2) >= static_cast<uint32_t>(p.cache.num_pages);
+  if (bad) id = 0;
+  if (bad2) id2 = 0;
+  r.first = pair;
+  r.a = r.head + id * p.cache.page_stride + (tile & ((1 << per) - 1)) * kBytes;
+  r.b = more ? r.head + id2 * p.cache.page_stride : nullptr;
+  r.bad_a = __ballot_sync(0xffffffffu, bad);
+  r.bad_b = per == 0 ? __ballot_sync(0xffffffffu, bad2) : r.bad_a;
+  if (lane == 0 && (r.bad_a | r.bad_b)) atomicCAS(&g_attn4_status, kDevOk, kDevBadIndex);
+}
+
+// Start the copy of a pair into a slot.
+template <int D>
+__device__ __forceinline__ void fetch(Ring& r, const Attn4Problem& p, int pair, uint32_t slot, int lane) {
+  constexpr int kBytes = Kv4<D>::kTileBytes;
+  int at = pair - r.first;
+  if (at >= 32) {
+    look_up<D>(r, p, pair, lane);
+    at = 0;
   }
-  int id = __shfl_sync(0xffffffffu, pg.ids, idx - pg.first);
-  bad = id < 0 || id >= p.cache.num_pages;
-  if (bad) {
-    if (lane == 0) atomicCAS(&g_attn4_status, kDevOk, kDevBadIndex);
-    id = 0;
+  if (r.bad | r.bad_a | r.bad_b)
+    r.bad = (r.bad & ~(3u << 2 * slot)) | ((r.bad_a >> at & 1u) | (r.bad_b >> at & 1u) << 1) << 2 * slot;
+  if (lane == at) {
+    const uint32_t dst = r.tiles + slot * (kPair * kBytes);
+    const bool split = p.cache.shift == 4;
+    mbar_arrive_expect_tx(&r.full[slot], split && !r.b ? kBytes : kPair * kBytes);
+    bulk_load(dst, r.a, split ? kBytes : kPair * kBytes, &r.full[slot]);
+    if (r.b) bulk_load(dst + kBytes, r.b, kBytes, &r.full[slot]);
   }
-  return p.cache.base + id * p.cache.page_stride +
-         ((static_cast<long long>(h) << per) + (tile & ((1 << per) - 1))) * Kv4<D>::kTileBytes;
 }
 
 template <int D, int NT, int CTAS>
 __global__ void __launch_bounds__(kWarps * 32, CTAS) fa2_kv4_attn_kernel(const Attn4Problem p) {
   constexpr int kRows = 8 * NT;
+  __shared__ __align__(128) char s_tiles[kWarps][2 * kPair * Kv4<D>::kTileBytes];
+  __shared__ __align__(8) uint64_t s_q[kWarps][NT * (D / 16) * 32];
+  __shared__ __align__(8) uint64_t s_full[kWarps][2];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  // (a warp's barriers are its own: no other warp waits for this)
+  if (lane == 0) {
+    for (int i = 0; i < 2; ++i) mbar_init(&s_full[warp][i], 1);
+    fence_mbar_init();
+  }
+  __syncwarp();
   griddep_wait();
   griddep_launch_dependents();
-  const int lane = threadIdx.x & 31;
   // consecutive spans on different SMs, so that a short line spreads out
-  const int span = (threadIdx.x >> 5) * gridDim.x + blockIdx.x;
-  // Each lane adds up the tiles of its share of the requests.
+  const int span = warp * gridDim.x + blockIdx.x;
+  // Each lane adds up the pairs of its share of the requests.
   const int per = (p.B + 31) / 32;
   const int b_lo = min(lane * per, p.B), b_hi = min(b_lo + per, p.B);
   long long mine = 0;
@@ -514,7 +595,7 @@ __global__ void __launch_bounds__(kWarps * 32, CTAS) fa2_kv4_attn_kernel(const A
   for (int b = b_lo; b < b_hi; ++b) {
     const Request r = request(p, b);
     fine &= r.ok;
-    mine += tiles_of<kRows>(p, r);
+    mine += pairs_of<kRows>(p, r);
   }
   long long upto = mine;
 #pragma unroll
@@ -527,7 +608,7 @@ __global__ void __launch_bounds__(kWarps * 32, CTAS) fa2_kv4_attn_kernel(const A
     long long at = upto - mine;
     for (int b = b_lo; b < b_hi; ++b) {
       p.start[b] = at;
-      at += tiles_of<kRows>(p, request(p, b));
+      at += pairs_of<kRows>(p, request(p, b));
     }
     if (lane == 31) p.start[p.B] = total;
     if (!fine) atomicCAS(&g_attn4_status, kDevOk, kDevBadSeqlens);
@@ -536,125 +617,184 @@ __global__ void __launch_bounds__(kWarps * 32, CTAS) fa2_kv4_attn_kernel(const A
   long long at = span * len;
   const long long end = min(at + len, total);
   if (at >= end) return;
-  // the request that holds tile `at`
+  // the request that holds pair `at`
   const uint32_t holds = __ballot_sync(0xffffffffu, upto > at);
   const int owner = __ffs(holds) - 1;
   int b = __shfl_sync(0xffffffffu, b_lo, owner);
   long long base = __shfl_sync(0xffffffffu, upto - mine, owner);
   Request rq = request(p, b);
-  long long size = tiles_of<kRows>(p, rq);
+  long long size = pairs_of<kRows>(p, rq);
 
   Rows<D, NT> s;
+  s.q = smem_u32(s_q[warp]) + lane * 8;
+  Ring ring;
+  ring.tiles = smem_u32(s_tiles[warp]);
+  ring.full = s_full[warp];
+  ring.slot = ring.phase = ring.bad = 0;
   while (at < end) {
     while (at >= base + size) {
       base += size;
       rq = request(p, ++b);
-      size = tiles_of<kRows>(p, rq);
+      size = pairs_of<kRows>(p, rq);
     }
-    const int nt = key_tiles(rq), rt = row_tiles<kRows>(p, rq);
+    const int np = key_pairs(rq), rt = row_tiles<kRows>(p, rq);
+    // (a request's units are at most H_kv times its row tiles: 32 bits, as its
+    // pairs are; their product may not be)
     const long long rel = at - base;
-    const long long unit = rel / nt;
-    const int tile0 = static_cast<int>(rel - unit * nt);
-    const int h = static_cast<int>(unit / rt), row0 = static_cast<int>(unit - static_cast<long long>(h) * rt) * kRows;
-    const int n = static_cast<int>(min(static_cast<long long>(nt - tile0), end - at));
-    const int* row = p.table + b * p.table_stride;
-    const int pages = static_cast<int>((rq.Lk + ((1LL << p.cache.shift) - 1)) >> p.cache.shift);
-    Pages pg{0, -64};
-    TileRegs<D> t0, t1;
-    bool bad0, bad1 = false;
-    load_tile<D>(t0, tile_address<D>(pg, p, row, pages, h, tile0, lane, bad0), lane);
-    if (n > 1) load_tile<D>(t1, tile_address<D>(pg, p, row, pages, h, tile0 + 1, lane, bad1), lane);
+    const int unit = rel >> 32 ? static_cast<int>(rel / np) : static_cast<int>(static_cast<uint32_t>(rel) / static_cast<uint32_t>(np));
+    const int first = static_cast<int>(rel - static_cast<long long>(unit) * np);
+    const int h = unit / rt, row0 = (unit - h * rt) * kRows;
+    const int n = static_cast<int>(min(static_cast<long long>(np - first), end - at));
+    ring.row = p.table + b * p.table_stride;
+    ring.pages = static_cast<int>((rq.Lk + ((1LL << p.cache.shift) - 1)) >> p.cache.shift);
+    ring.head = p.cache.base + (static_cast<long long>(h) << (p.cache.shift - 4)) * Kv4<D>::kTileBytes;
+    // (both slots are free here: the part before has been read to its end)
+    look_up<D>(ring, p, first, lane);
+    fetch<D>(ring, p, first, ring.slot, lane);
+    if (n > 1) fetch<D>(ring, p, first + 1, ring.slot ^ 1, lane);
     start_unit<D, NT>(s, p, rq, h, row0, lane);
-    for (int i = 0; i < n; i += 2) {
-      int key0 = (tile0 + i) * kCacheTile;
-      step<D, NT>(s, t0, key0, bad0 ? 0 : min(rq.Lk - key0, kCacheTile), lane);
-      if (i + 2 < n) load_tile<D>(t0, tile_address<D>(pg, p, row, pages, h, tile0 + i + 2, lane, bad0), lane);
-      if (i + 1 < n) {
-        key0 += kCacheTile;
-        step<D, NT>(s, t1, key0, bad1 ? 0 : min(rq.Lk - key0, kCacheTile), lane);
-        if (i + 3 < n) load_tile<D>(t1, tile_address<D>(pg, p, row, pages, h, tile0 + i + 3, lane, bad1), lane);
+    const int whole = s.min_vis / kPairKeys;  // every row sees all keys of the pairs below
+    for (int pair = first; pair < first + n; ++pair) {
+      if (!mbar_wait(&ring.full[ring.slot], ring.phase, &g_attn4_status)) {
+        // a copy that never came: wait (as long again) for the other, then give up
+        if (pair + 1 < first + n) mbar_wait(&ring.full[ring.slot ^ 1], ring.phase ^ ring.slot, &g_attn4_status);
+        return;
       }
+      const uint32_t tiles = ring.tiles + ring.slot * (kPair * Kv4<D>::kTileBytes);
+      if (__builtin_expect(pair < whole && !ring.bad, 1))
+        step<D, NT, false>(s, tiles, 0, 0, 0, lane);
+      else
+        step<D, NT, true>(s, tiles, pair * kPairKeys, rq.Lk, ring.bad >> 2 * ring.slot & 3u, lane);
+      __syncwarp();  // every lane has read the slot
+      if (pair + 2 < first + n) fetch<D>(ring, p, pair + 2, ring.slot, lane);
+      ring.phase ^= ring.slot;  // (the parity changes when the ring has gone round)
+      ring.slot ^= 1;
     }
     // A unit that is whole goes out; else slot 0 of the span if the part
     // began at the span's start, slot 1 if within it.
-    const int slot = n == nt ? -1 : 2 * span + (at == span * len ? 0 : 1);
+    const int slot = n == np ? -1 : 2 * span + (at == span * len ? 0 : 1);
     end_unit<D, NT>(s, p, rq, h, row0, slot, lane);
     at += n;
   }
 }
 
 // Join the partial results of the units that several spans share, in span
-// order, and write the rows that see no key.  One CTA per query row of a
-// unit; its warps take every fourth span, then warp 0 adds the four sums.
-template <int D, int ROWS>
-__global__ void __launch_bounds__(128) fa2_kv4_combine_kernel(const Attn4Problem p, int max_row_tiles) {
-  griddep_wait();
-  griddep_launch_dependents();
-  __shared__ float s_o[4][D];
-  __shared__ float s_m[4], s_l[4];
+// order, and write the rows that see no key.  A CTA of 8 warps takes 8 / WPR
+// rows of a unit, WPR warps each.  Bound by the latency of what it reads one
+// after the other (where the unit's spans are, their maxima and sums, their
+// rows), so each of the three is one round of loads: a lane per span for the
+// maxima, then the rows of kBatch spans at once.
+template <int D, int ROWS, int WPR>
+__global__ void __launch_bounds__(256) fa2_kv4_combine_kernel(const Attn4Problem p, int max_row_tiles) {
+  constexpr int kCols = D >= 32 ? D / 32 : 1, kRowsCta = 8 / WPR, kBatch = 8;
+  __shared__ float s_o[WPR > 1 ? 8 : 1][D];
+  __shared__ float s_m[8], s_l[8];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int id = blockIdx.x;
-  const int local = id % ROWS;
-  id /= ROWS;
+  const int local = (id % (ROWS / kRowsCta)) * kRowsCta + warp / WPR, part = warp % WPR;
+  id /= ROWS / kRowsCta;
   const int rt = id % max_row_tiles;
   id /= max_row_tiles;
   const int h = id % p.cache.heads, b = id / p.cache.heads;
+  griddep_wait();
+  griddep_launch_dependents();
+  const long long start = p.start[b], total = p.start[p.B];
   const Request rq = request(p, b);
   const int r = rt * ROWS + local;
-  if (!rq.ok || r >= p.G * rq.Lq) return;
-  const int i0 = r / p.G;
-  const long long tok = rq.q0 + i0;
-  const int head = h * p.G + (r - i0 * p.G);
-  __nv_bfloat16* dst = p.o + (tok * p.H + head) * D;
-  float* lse = p.lse + static_cast<long long>(head) * p.total_q + tok;
-  if (rq.Lk == 0) {
-    for (int c = threadIdx.x; c < D; c += 128) dst[c] = __float2bfloat16_rn(0.f);
-    if (threadIdx.x == 0) *lse = -INFINITY;
-    return;
+  const bool live = rq.ok && r < p.G * rq.Lq;
+  const int np = key_pairs(rq);
+  int count = 0;  // spans that share the unit
+  long long s0 = 0, slot0 = 0;
+  if (live && np > 0) {
+    const long long len = span_length(total, p.spans);
+    const long long first = start + (static_cast<long long>(h) * row_tiles<ROWS>(p, rq) + rt) * np;
+    s0 = first >> 32 ? first / len : static_cast<uint32_t>(first) / static_cast<uint32_t>(len);
+    const long long in = first - s0 * len;  // pairs of span s0 before the unit
+    count = static_cast<int>(in + np <= len ? 1 : (in + np - 1) >> 32 ? (in + np - 1) / len + 1
+                                                                      : static_cast<uint32_t>(in + np - 1) / static_cast<uint32_t>(len) + 1);
+    // slot 0 of a span, but slot 1 where the unit begins within it
+    slot0 = (2 * s0 + (in != 0 ? 1 : 0)) * ROWS + local;
   }
-  const int nt = key_tiles(rq);
-  const long long len = span_length(p.start[p.B], p.spans);
-  const long long first = p.start[b] + (static_cast<long long>(h) * row_tiles<ROWS>(p, rq) + rt) * nt;
-  const long long s0 = first / len, s1 = (first + nt - 1) / len;
-  if (s0 == s1) return;  // one warp had it whole
-  auto slot = [&](long long s) { return (2 * s + (s == s0 && first != s * len ? 1 : 0)) * ROWS + local; };
-  constexpr int kCols = D >= 32 ? D / 32 : 1;
-  float m = kNoMax, l = 0.f, o[kCols];
+  // (the same for all warps of a row; rows of one warp need no barrier)
+  if (WPR == 1 && (!live || count == 1)) return;
+  auto at = [&](int i) { return i == 0 ? slot0 : 2 * (s0 + i) * ROWS + local; };
+  float l = 0.f, top = kNoMax, o[kCols];
 #pragma unroll
   for (int k = 0; k < kCols; ++k) o[k] = 0.f;
   const bool active = lane * kCols < D;
-  for (long long s = s0 + warp; s <= s1; s += 4) {
-    const long long at = slot(s);
-    const float2 ml = p.part_ml[at];
-    float v[kCols];
+  // warp `part` takes spans part, part + WPR, ..., 32 at a time
+  for (int i0 = part; count > 1 && i0 < count; i0 += WPR * 32) {
+    float2 ml = make_float2(kNoMax, 0.f);
+    if (i0 + lane * WPR < count) ml = p.part_ml[at(i0 + lane * WPR)];
+    float m = fmaxf(top, ml.x);
 #pragma unroll
-    for (int k = 0; k < kCols; ++k) v[k] = active ? p.part[at * D + lane * kCols + k] : 0.f;
-    const float top = fmaxf(m, ml.x), a = ex2_approx(m - top), e = ex2_approx(ml.x - top);
-    m = top;
-    l = l * a + ml.y * e;
+    for (int sh = 16; sh > 0; sh >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, sh));
+    const float down = ex2_approx(top - m), w = ex2_approx(ml.x - m);
+    top = m;
+    l = l * down + w * ml.y;
 #pragma unroll
-    for (int k = 0; k < kCols; ++k) o[k] = o[k] * a + v[k] * e;
+    for (int k = 0; k < kCols; ++k) o[k] *= down;
+    const int n = min((count - i0 + WPR - 1) / WPR, 32);
+    const float* src = p.part + lane * kCols;
+    for (int c = 0; c < n; c += kBatch) {
+      float v[kBatch][kCols];
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const float* row = src + at(i0 + (c + i) * WPR) * D;
+        if constexpr (kCols == 4) {
+          const float4 t = c + i < n ? *reinterpret_cast<const float4*>(row) : make_float4(0.f, 0.f, 0.f, 0.f);
+          v[i][0] = t.x, v[i][1] = t.y, v[i][2] = t.z, v[i][3] = t.w;
+        } else {
+#pragma unroll
+          for (int k = 0; k < kCols; ++k) v[i][k] = c + i < n && active ? row[k] : 0.f;
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        // (lanes past the last span have weight 0)
+        const float wi = __shfl_sync(0xffffffffu, w, (c + i) & 31);
+#pragma unroll
+        for (int k = 0; k < kCols; ++k) o[k] = fmaf(wi, v[i][k], o[k]);
+      }
+    }
   }
+#pragma unroll
+  for (int sh = 16; sh > 0; sh >>= 1) l += __shfl_xor_sync(0xffffffffu, l, sh);
+  if (WPR > 1) {
+#pragma unroll
+    for (int k = 0; k < kCols; ++k)
+      if (active) s_o[warp][lane * kCols + k] = o[k];
+    if (lane == 0) s_m[warp] = top, s_l[warp] = l;
+    __syncthreads();
+    if (part != 0 || !live || count == 1) return;
+    for (int w = 1; w < WPR; ++w) top = fmaxf(top, s_m[warp + w]);
+    float down = ex2_approx(s_m[warp] - top);
+    l *= down;
+#pragma unroll
+    for (int k = 0; k < kCols; ++k) o[k] *= down;
+#pragma unroll
+    for (int w = 1; w < WPR; ++w) {
+      down = ex2_approx(s_m[warp + w] - top);
+      l += s_l[warp + w] * down;
+#pragma unroll
+      for (int k = 0; k < kCols; ++k)
+        if (active) o[k] = fmaf(s_o[warp + w][lane * kCols + k], down, o[k]);
+    }
+  }
+  const int i0 = r / p.G;
+  const long long tok = rq.q0 + i0;
+  const int head = h * p.G + (r - i0 * p.G);
+  const float f = l == 0.f ? 0.f : p.v_scale / l;
+  __nv_bfloat16* dst = p.o + (tok * p.H + head) * D + lane * kCols;
 #pragma unroll
   for (int k = 0; k < kCols; ++k)
-    if (active) s_o[warp][lane * kCols + k] = o[k];
-  if (lane == 0) s_m[warp] = m, s_l[warp] = l;
-  __syncthreads();
-  if (threadIdx.x >= D) return;
-  float top = fmaxf(fmaxf(s_m[0], s_m[1]), fmaxf(s_m[2], s_m[3])), sum = 0.f, v = 0.f;
-#pragma unroll
-  for (int w = 0; w < 4; ++w) {
-    const float e = ex2_approx(s_m[w] - top);
-    sum += s_l[w] * e;
-    v += s_o[w][threadIdx.x] * e;
-  }
-  dst[threadIdx.x] = __float2bfloat16_rn(sum == 0.f ? 0.f : v * (p.v_scale / sum));
-  if (threadIdx.x == 0) *lse = sum == 0.f ? -INFINITY : row_lse(top, sum);
+    if (active) dst[k] = __float2bfloat16_rn(o[k] * f);
+  if (lane == 0) p.lse[static_cast<long long>(head) * p.total_q + tok] = l == 0.f ? -INFINITY : row_lse(top, l);
 }
 
 // Warps of the whole GPU: as many as are resident at once, so that the spans
 // are one wave.
-constexpr int kCtas1 = 4, kCtas2 = 2;  // resident CTAs per SM, 8 and 16 rows
+constexpr int kCtas1 = 4, kCtas2 = 3;  // resident CTAs per SM, 8 and 16 rows
 constexpr int kSpans1 = 152 * kCtas1 * kWarps, kSpans2 = 152 * kCtas2 * kWarps;
 
 // 16 rows a unit when 8 would read the cache twice.
@@ -666,9 +806,13 @@ int launch_attn_d(Attn4Problem p, long long max_rows, cudaStream_t st) {
   p.spans = NT == 1 ? kSpans1 : kSpans2;
   if (int e = launch_pdl(fa2_kv4_attn_kernel<D, NT, kCtas>, dim3(152 * kCtas), dim3(kWarps * 32), 0, st, p)) return e;
   const int rt = static_cast<int>((max_rows + kRows - 1) / kRows);
-  return launch_pdl(fa2_kv4_combine_kernel<D, kRows>,
-                    dim3(static_cast<unsigned>(static_cast<long long>(p.B) * p.cache.heads * rt * kRows)), dim3(128), 0, st, p,
-                    rt);
+  const long long units = static_cast<long long>(p.B) * p.cache.heads * rt;
+  // Spans of a unit, were all requests of one length: with few, a warp joins
+  // a row alone; with many, a CTA's eight do.
+  if (p.spans / units < 16)
+    return launch_pdl(fa2_kv4_combine_kernel<D, kRows, 1>, dim3(static_cast<unsigned>(units * (kRows / 8))), dim3(256), 0, st, p,
+                      rt);
+  return launch_pdl(fa2_kv4_combine_kernel<D, kRows, 8>, dim3(static_cast<unsigned>(units * kRows)), dim3(256), 0, st, p, rt);
 }
 
 template <int D>
