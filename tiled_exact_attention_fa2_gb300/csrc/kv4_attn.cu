@@ -55,7 +55,12 @@ namespace {
 
 __device__ int g_attn4_status;
 
-constexpr int kWarps = 4;  // warps of a CTA
+// Warps of a CTA (one CTA per SM): as many as the registers of 8 and of 16
+// rows allow.
+template <int NT>
+constexpr int kWarps = NT == 1 ? 16 : 12;
+template <int NT>
+constexpr int kSpans = 152 * kWarps<NT>;  // one wave
 constexpr float kNoMax = -1.7e38f;  // running maximum of a row that has seen no key (finite: no inf - inf)
 constexpr float kLift = 11.f;   // weights are held 2^11 up
 constexpr float kLag = 4.f;     // a score may pass the running maximum by 2^4
@@ -75,7 +80,6 @@ struct Attn4Problem {
   float2* part_ml;    // [2 * spans][rows] maximum (log2), sum
   long long* start;   // [B + 1] first tile pair of each request on the line
   int B, H, G, total_q, uniform_q, max_q, width;
-  int spans;
   float scale_log2, v_scale;
   int causal;
 };
@@ -112,10 +116,18 @@ __device__ __forceinline__ long long pairs_of(const Attn4Problem& p, const Reque
   return r.ok ? static_cast<long long>(p.cache.heads) * row_tiles<ROWS>(p, r) * key_pairs(r) : 0;
 }
 
-__device__ __forceinline__ long long span_length(long long total, int spans) {
-  const long long s = (total + spans - 1) / spans;
-  return s < kMinPairs ? kMinPairs : s;
-}
+// The line of all units' pairs cut into equal spans.
+template <int NT>
+struct Line {
+  long long len;
+  __device__ __forceinline__ explicit Line(long long total) {
+    len = total >> 32 ? (total + kSpans<NT> - 1) / kSpans<NT> : (static_cast<uint32_t>(total) + (kSpans<NT> - 1LL)) / kSpans<NT>;
+    if (len < kMinPairs) len = kMinPairs;
+  }
+  __device__ __forceinline__ int span_of(long long pair) const {
+    return static_cast<int>(pair >> 32 ? pair / len : static_cast<uint32_t>(pair) / static_cast<uint32_t>(len));
+  }
+};
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
@@ -345,12 +357,11 @@ __device__ __forceinline__ void step(Rows<D, NT>& s, uint32_t tiles, int key0, i
 #pragma unroll
   for (int i = 0; i < kPair; ++i)
 #pragma unroll
-    for (int j = 0; j < NT; ++j)
+    for (int j = 0; j < NT; ++j) {
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        y[i][j][u] = fmaf(x[i][j][u], s.cs[j][u & 1], s.off[j][u & 1]);
-        top = fmaxf(top, y[i][j][u]);
-      }
+      for (int u = 0; u < 4; ++u) y[i][j][u] = fmaf(x[i][j][u], s.cs[j][u & 1], s.off[j][u & 1]);
+      top = fmax3(fmax3(top, y[i][j][0], y[i][j][1]), y[i][j][2], y[i][j][3]);
+    }
   if (__builtin_expect(__any_sync(0xffffffffu, top > kLift + kLag), 0)) {
 #pragma unroll
     for (int j = 0; j < NT; ++j)
@@ -528,6 +539,7 @@ struct Ring {
   const char* head;      // this head's part of page 0
   int pages, first;      // first: the pair of lane 0
   const char *a, *b;     // the lane's pair: its first (or only) copy, its second or NULL
+  uint32_t bytes;        // of both copies
   uint32_t bad_a, bad_b; // lanes whose first / second tile has a page id out of range (copied from page 0, its keys left out)
   uint32_t bad;          // the slots' bits: first and second tile of slot 0, of slot 1
 };
@@ -545,6 +557,7 @@ __device__ __forceinline__ void look_up(Ring& r, const Attn4Problem& p, int pair
   r.first = pair;
   r.a = r.head + id * p.cache.page_stride + (tile & ((1 << per) - 1)) * kBytes;
   r.b = more ? r.head + id2 * p.cache.page_stride : nullptr;
+  r.bytes = per == 0 && !more ? kBytes : kPair * kBytes;
   r.bad_a = __ballot_sync(0xffffffffu, bad);
   r.bad_b = per == 0 ? __ballot_sync(0xffffffffu, bad2) : r.bad_a;
   if (lane == 0 && (r.bad_a | r.bad_b)) atomicCAS(&g_attn4_status, kDevOk, kDevBadIndex);
@@ -563,36 +576,40 @@ __device__ __forceinline__ void fetch(Ring& r, const Attn4Problem& p, int pair, 
     r.bad = (r.bad & ~(3u << 2 * slot)) | ((r.bad_a >> at & 1u) | (r.bad_b >> at & 1u) << 1) << 2 * slot;
   if (lane == at) {
     const uint32_t dst = r.tiles + slot * (kPair * kBytes);
-    const bool split = p.cache.shift == 4;
-    mbar_arrive_expect_tx(&r.full[slot], split && !r.b ? kBytes : kPair * kBytes);
-    bulk_load(dst, r.a, split ? kBytes : kPair * kBytes, &r.full[slot]);
+    mbar_arrive_expect_tx(&r.full[slot], r.bytes);
+    bulk_load(dst, r.a, r.b ? kBytes : r.bytes, &r.full[slot]);
     if (r.b) bulk_load(dst + kBytes, r.b, kBytes, &r.full[slot]);
   }
 }
 
-template <int D, int NT, int CTAS>
-__global__ void __launch_bounds__(kWarps * 32, CTAS) fa2_kv4_attn_kernel(const Attn4Problem p) {
+template <int D, int NT>
+struct __align__(128) WarpSmem {
+  char tiles[2 * kPair * Kv4<D>::kTileBytes];
+  uint64_t q[NT * (D / 16) * 32];
+  uint64_t full[2];
+};
+
+template <int D, int NT>
+__global__ void __launch_bounds__(kWarps<NT> * 32, 1) fa2_kv4_attn_kernel(const Attn4Problem p) {
   constexpr int kRows = 8 * NT;
-  __shared__ __align__(128) char s_tiles[kWarps][2 * kPair * Kv4<D>::kTileBytes];
-  __shared__ __align__(8) uint64_t s_q[kWarps][NT * (D / 16) * 32];
-  __shared__ __align__(8) uint64_t s_full[kWarps][2];
+  extern __shared__ __align__(128) char smem[];
+  WarpSmem<D, NT>* const ws = reinterpret_cast<WarpSmem<D, NT>*>(smem) + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   // (a warp's barriers are its own: no other warp waits for this)
   if (lane == 0) {
-    for (int i = 0; i < 2; ++i) mbar_init(&s_full[warp][i], 1);
+    for (int i = 0; i < 2; ++i) mbar_init(&ws->full[i], 1);
     fence_mbar_init();
   }
   __syncwarp();
   griddep_wait();
   griddep_launch_dependents();
-  // consecutive spans on different SMs, so that a short line spreads out
-  const int span = warp * gridDim.x + blockIdx.x;
   // Each lane adds up the pairs of its share of the requests.
   const int per = (p.B + 31) / 32;
   const int b_lo = min(lane * per, p.B), b_hi = min(b_lo + per, p.B);
   long long mine = 0;
   bool fine = true;
-  for (int b = b_lo; b < b_hi; ++b) {
+#pragma unroll 4
+  for (int b = b_lo; b < b_hi; ++b) {  // (unrolled: the loads of four requests at once)
     const Request r = request(p, b);
     fine &= r.ok;
     mine += pairs_of<kRows>(p, r);
@@ -604,7 +621,7 @@ __global__ void __launch_bounds__(kWarps * 32, CTAS) fa2_kv4_attn_kernel(const A
     if (lane >= s) upto += v;
   }
   const long long total = __shfl_sync(0xffffffffu, upto, 31);
-  if (span == 0) {  // for the combine kernel
+  if (blockIdx.x == 0 && warp == 0) {  // for the combine kernel
     long long at = upto - mine;
     for (int b = b_lo; b < b_hi; ++b) {
       p.start[b] = at;
@@ -613,9 +630,12 @@ __global__ void __launch_bounds__(kWarps * 32, CTAS) fa2_kv4_attn_kernel(const A
     if (lane == 31) p.start[p.B] = total;
     if (!fine) atomicCAS(&g_attn4_status, kDevOk, kDevBadSeqlens);
   }
-  const long long len = span_length(total, p.spans);
-  long long at = span * len;
-  const long long end = min(at + len, total);
+  const Line<NT> line(total);
+  // A short line spreads over the SMs, a long one gives an SM consecutive
+  // spans (whose units share queries and pages).
+  const int span = line.len == kMinPairs ? warp * gridDim.x + blockIdx.x : blockIdx.x * kWarps<NT> + warp;
+  const long long begin = span * line.len, end = min(begin + line.len, total);
+  long long at = begin;
   if (at >= end) return;
   // the request that holds pair `at`
   const uint32_t holds = __ballot_sync(0xffffffffu, upto > at);
@@ -626,10 +646,10 @@ __global__ void __launch_bounds__(kWarps * 32, CTAS) fa2_kv4_attn_kernel(const A
   long long size = pairs_of<kRows>(p, rq);
 
   Rows<D, NT> s;
-  s.q = smem_u32(s_q[warp]) + lane * 8;
+  s.q = smem_u32(ws->q) + lane * 8;
   Ring ring;
-  ring.tiles = smem_u32(s_tiles[warp]);
-  ring.full = s_full[warp];
+  ring.tiles = smem_u32(ws->tiles);
+  ring.full = ws->full;
   ring.slot = ring.phase = ring.bad = 0;
   while (at < end) {
     while (at >= base + size) {
@@ -672,7 +692,7 @@ __global__ void __launch_bounds__(kWarps * 32, CTAS) fa2_kv4_attn_kernel(const A
     }
     // A unit that is whole goes out; else slot 0 of the span if the part
     // began at the span's start, slot 1 if within it.
-    const int slot = n == np ? -1 : 2 * span + (at == span * len ? 0 : 1);
+    const int slot = n == np ? -1 : 2 * span + (at == begin ? 0 : 1);
     end_unit<D, NT>(s, p, rq, h, row0, slot, lane);
     at += n;
   }
@@ -703,21 +723,19 @@ __global__ void __launch_bounds__(256) fa2_kv4_combine_kernel(const Attn4Problem
   const int r = rt * ROWS + local;
   const bool live = rq.ok && r < p.G * rq.Lq;
   const int np = key_pairs(rq);
-  int count = 0;  // spans that share the unit
-  long long s0 = 0, slot0 = 0;
+  int count = 0, s0 = 0;  // spans that share the unit, the first of them
+  long long slot0 = 0;
   if (live && np > 0) {
-    const long long len = span_length(total, p.spans);
+    const Line<ROWS / 8> line(total);
     const long long first = start + (static_cast<long long>(h) * row_tiles<ROWS>(p, rq) + rt) * np;
-    s0 = first >> 32 ? first / len : static_cast<uint32_t>(first) / static_cast<uint32_t>(len);
-    const long long in = first - s0 * len;  // pairs of span s0 before the unit
-    count = static_cast<int>(in + np <= len ? 1 : (in + np - 1) >> 32 ? (in + np - 1) / len + 1
-                                                                      : static_cast<uint32_t>(in + np - 1) / static_cast<uint32_t>(len) + 1);
+    s0 = line.span_of(first);
+    count = line.span_of(first + np - 1) - s0 + 1;
     // slot 0 of a span, but slot 1 where the unit begins within it
-    slot0 = (2 * s0 + (in != 0 ? 1 : 0)) * ROWS + local;
+    slot0 = (2LL * s0 + (first != s0 * line.len ? 1 : 0)) * ROWS + local;
   }
   // (the same for all warps of a row; rows of one warp need no barrier)
   if (WPR == 1 && (!live || count == 1)) return;
-  auto at = [&](int i) { return i == 0 ? slot0 : 2 * (s0 + i) * ROWS + local; };
+  auto at = [&](int i) { return i == 0 ? slot0 : 2LL * (s0 + i) * ROWS + local; };
   float l = 0.f, top = kNoMax, o[kCols];
 #pragma unroll
   for (int k = 0; k < kCols; ++k) o[k] = 0.f;
@@ -792,24 +810,19 @@ __global__ void __launch_bounds__(256) fa2_kv4_combine_kernel(const Attn4Problem
   if (lane == 0) p.lse[static_cast<long long>(head) * p.total_q + tok] = l == 0.f ? -INFINITY : row_lse(top, l);
 }
 
-// Warps of the whole GPU: as many as are resident at once, so that the spans
-// are one wave.
-constexpr int kCtas1 = 4, kCtas2 = 3;  // resident CTAs per SM, 8 and 16 rows
-constexpr int kSpans1 = 152 * kCtas1 * kWarps, kSpans2 = 152 * kCtas2 * kWarps;
-
 // 16 rows a unit when 8 would read the cache twice.
 inline bool wide_rows(long long rows) { return rows > 8; }
 
 template <int D, int NT>
 int launch_attn_d(Attn4Problem p, long long max_rows, cudaStream_t st) {
-  constexpr int kCtas = NT == 1 ? kCtas1 : kCtas2, kRows = 8 * NT;
-  p.spans = NT == 1 ? kSpans1 : kSpans2;
-  if (int e = launch_pdl(fa2_kv4_attn_kernel<D, NT, kCtas>, dim3(152 * kCtas), dim3(kWarps * 32), 0, st, p)) return e;
+  constexpr int kRows = 8 * NT, kSmem = kWarps<NT> * sizeof(WarpSmem<D, NT>);
+  if (int e = ensure_max_smem(reinterpret_cast<const void*>(fa2_kv4_attn_kernel<D, NT>), kSmem)) return e;
+  if (int e = launch_pdl(fa2_kv4_attn_kernel<D, NT>, dim3(152), dim3(kWarps<NT> * 32), kSmem, st, p)) return e;
   const int rt = static_cast<int>((max_rows + kRows - 1) / kRows);
   const long long units = static_cast<long long>(p.B) * p.cache.heads * rt;
   // Spans of a unit, were all requests of one length: with few, a warp joins
   // a row alone; with many, a CTA's eight do.
-  if (p.spans / units < 16)
+  if (kSpans<NT> / units < 16)
     return launch_pdl(fa2_kv4_combine_kernel<D, kRows, 1>, dim3(static_cast<unsigned>(units * (kRows / 8))), dim3(256), 0, st, p,
                       rt);
   return launch_pdl(fa2_kv4_combine_kernel<D, kRows, 8>, dim3(static_cast<unsigned>(units * kRows)), dim3(256), 0, st, p, rt);
@@ -820,7 +833,7 @@ int launch_attn(const Attn4Problem& p, long long max_rows, cudaStream_t st) {
   return wide_rows(max_rows) ? launch_attn_d<D, 2>(p, max_rows, st) : launch_attn_d<D, 1>(p, max_rows, st);
 }
 
-size_t attn_slots(bool wide) { return wide ? static_cast<size_t>(kSpans2) * 2 * 16 : static_cast<size_t>(kSpans1) * 2 * 8; }
+size_t attn_slots(bool wide) { return wide ? static_cast<size_t>(kSpans<2>) * 2 * 16 : static_cast<size_t>(kSpans<1>) * 2 * 8; }
 
 int check_attn_sizes(int B, int H, int H_kv, int total_q, int max_q, int d) {
   if (B < 1 || H < 1 || total_q < 0 || max_q < 0 || total_q > (1 << 30) || max_q > total_q || (total_q > 0 && max_q < 1))
