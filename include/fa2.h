@@ -358,8 +358,8 @@ int fa2_step_from_host(const void* q, const void* k, const void* v, const void* 
  *             8; the stride of a dimension of size 1 is not looked at), or
  *             NULL: all contiguous.  A packed batch [total, heads, d] is
  *             B = 1, N = total.  Views of one fused projection are fine.
- *   q_weight, k_weight   gains [d], fp32 if weight_fp32 != 0, else bf16;
- *             NULL: ones
+ *   q_weight, k_weight   gains [d], fp32 if weight_fp32 != 0, else bf16,
+ *             16-byte aligned; NULL: ones
  *   rope      fp32 [max_positions, rot_dim], 16-byte aligned: each row the
  *             rot_dim/2 cosines, then the sines.  rot_dim: a multiple of 16,
  *             0 (no rotation; rope may be NULL) to d

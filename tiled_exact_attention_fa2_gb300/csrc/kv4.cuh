@@ -62,16 +62,26 @@ __device__ __forceinline__ uint32_t e4m3x2_to_f16(uint32_t w) {
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<uint16_t>(w)));
   return r;
 }
-// Round to nearest even, saturating: `lo` lands in the low half of the byte.
-__device__ __forceinline__ uint32_t e2m1x2_of(float lo, float hi) {
+// The codes of 8 values given as fp16 pairs, a byte per pair: round to nearest
+// even, saturating, the low half of a pair in the low half of its byte.
+__device__ __forceinline__ uint32_t f16_to_e2m1x8(const uint32_t (&h)[4]) {
   uint32_t r;
-  asm("{\n .reg .b8 a;\n cvt.rn.satfinite.e2m1x2.f32 a, %1, %2;\n cvt.u32.u8 %0, a;\n}" : "=r"(r) : "f"(hi), "f"(lo));
+  asm("{\n .reg .b8 a, b, c, d;\n cvt.rn.satfinite.e2m1x2.f16x2 a, %1;\n cvt.rn.satfinite.e2m1x2.f16x2 b, %2;\n"
+      " cvt.rn.satfinite.e2m1x2.f16x2 c, %3;\n cvt.rn.satfinite.e2m1x2.f16x2 d, %4;\n mov.b32 %0, {a, b, c, d};\n}"
+      : "=r"(r)
+      : "r"(h[0]), "r"(h[1]), "r"(h[2]), "r"(h[3]));
   return r;
 }
 __device__ __forceinline__ uint32_t e4m3_of(float x) {
   uint16_t r;
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(0.f), "f"(x));
   return r & 0xffu;
+}
+// Larger magnitude of bf16 pairs, a NaN if either is one.
+__device__ __forceinline__ uint32_t max_abs_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a & 0x7fff7fffu), "r"(b & 0x7fff7fffu));
+  return r;
 }
 __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
   uint32_t r;

@@ -20,110 +20,113 @@ namespace {
 __device__ int g_cache_status;
 
 struct AppendProblem {
-  const __nv_bfloat16* x[2];  // k, v [T, H_kv, d]
+  const __nv_bfloat16 *k, *v;  // [T, H_kv, d]
   long long token_stride[2], head_stride[2];
-  __nv_bfloat16* out[2];  // stored values [T, H_kv, d], or NULL
-  float factor[2];
+  __nv_bfloat16 *k_out, *v_out;  // stored values [T, H_kv, d], or NULL
+  float k_scale, v_scale;
   const long long* slots;
   PagedCache cache;
-  long long groups;  // T * H_kv * d / 16
+  int tokens, row_threads, block_tokens;  // threads of a token (H_kv d / 8), tokens of a CTA
 };
 
-// One thread per group of 16 columns (K: blockIdx.y = 0, V: 1).  The scale is
-// e4m3(max |x| / (6 f)) and a code e2m1(x / (f s)), f the cache's factor: the
-// quotients are IEEE divisions, whose rounding cannot cross a border of the
-// two formats (the borders have few bits, and x is bf16), so a value is
-// always the nearest one, ties to even.  A group whose scale rounds to zero
-// is stored as zeros; one that holds a NaN gets the NaN scale.
+// 8 columns of a group of 16, the other 8 in the neighbouring lane: the
+// group's scale byte, the columns' four code bytes, and the stored values in
+// place of x.  The scale is e4m3(max |x| / (6 f)), a code e2m1(x / (f s)), f
+// the cache's factor.  Both quotients are products with a rounded reciprocal,
+// off by less than 2^-22; that does not move a value across a border of its
+// format or off it: x is bf16 (8 significant bits), a border times a scale
+// has at most 9, so a quotient that is not on a border is at least 2^-9
+// away; one that is on it comes out exact (a scale's borders) or is rounded
+// back onto it (a code's: fp16 keeps 11 bits).  So every value is the nearest
+// one, ties to even, as an exact division would give it.
+__device__ __forceinline__ void quantize(uint4& x, float f, uint32_t& scale, uint32_t& code, bool want_values) {
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+  uint32_t top = max_abs_bf16x2(max_abs_bf16x2(w[0], w[1]), max_abs_bf16x2(w[2], w[3]));
+  top = max_abs_bf16x2(top, __shfl_xor_sync(0xffffffffu, top, 1));
+  top = max_abs_bf16x2(top, top >> 16);  // (its low half)
+  const float mx = __uint_as_float(top << 16), inv_f = 1.f / f;  // a power of two: exact
+  // a NaN in the group: the NaN scale
+  scale = isnan(mx) ? 0x7fu : e4m3_of(mx * inv_f * (1.f / 6.f));
+  const float s = f16lo_to_f32(e4m3x2_to_f16(scale));
+  code = 0;  // of a group whose scale is 0 or NaN
+  if (s > 0.f) {
+    const float inv = 1.f / s * inv_f;
+    uint32_t q[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 v = unpack_bf16x2(w[i]);
+      q[i] = pack_f16x2(v.x * inv, v.y * inv);
+    }
+    code = f16_to_e2m1x8(q);
+  }
+  if (want_values) {
+    const float sf = s * f;
+    uint32_t hv[4], o[4];
+    e2m1x8_to_f16(code, hv);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 v = f16x2_to_f32(hv[i]);
+      o[i] = pack_bf16x2(v.x * sf, v.y * sf);
+    }
+    x = make_uint4(o[0], o[1], o[2], o[3]);
+  }
+}
+
+// One thread per 8 columns of a token's head, for K and for V: 16-byte loads
+// and stores side by side, two of each in flight.  (One thread per group of
+// 16 with IEEE divisions was bound by instructions: 36 us against 23 of
+// memory for 16385 tokens of 8 heads of 128 columns.)
 template <int D>
 __global__ void __launch_bounds__(256) fa2_kv4_append_kernel(const AppendProblem p) {
   using L = Kv4<D>;
   griddep_wait();
   griddep_launch_dependents();
-  const long long i = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
-  if (i >= p.groups) return;
-  const int which = blockIdx.y;
-  const int grp = static_cast<int>(i % L::kGroups);
-  const long long row = i / L::kGroups;
-  const long long t = row / p.cache.heads;
-  const int h = static_cast<int>(row - t * p.cache.heads);
-  const long long slot = __ldg(p.slots + t);
-  // (selected, not indexed: an indexed parameter array is copied to the stack)
-  const __nv_bfloat16* x = which ? p.x[1] : p.x[0];
-  const long long token_stride = which ? p.token_stride[1] : p.token_stride[0];
-  const long long head_stride = which ? p.head_stride[1] : p.head_stride[0];
-  const uint4* src = reinterpret_cast<const uint4*>(x + t * token_stride + h * head_stride + grp * 16);
-  const uint4 u0 = __ldg(src), u1 = __ldg(src + 1);
-  const uint32_t w[8] = {u0.x, u0.y, u0.z, u0.w, u1.x, u1.y, u1.z, u1.w};
-  const float f = which ? p.factor[1] : p.factor[0], inv = 1.f / f;  // a power of two: exact
-  float y[16];
-  float mx = 0.f;
-  bool nan = false;
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const float2 v = unpack_bf16x2(w[j]);
-    y[2 * j] = v.x * inv;
-    y[2 * j + 1] = v.y * inv;
-    nan |= isnan(v.x) || isnan(v.y);
-    mx = fmaxf(mx, fmaxf(fabsf(y[2 * j]), fabsf(y[2 * j + 1])));
+  // thread -> (token, head, columns); a pair of lanes stays together, since
+  // row_threads is even
+  const int local = threadIdx.x / p.row_threads;
+  const int r = threadIdx.x - local * p.row_threads + blockIdx.y * 256;
+  const int t = blockIdx.x * p.block_tokens + local;
+  const bool live = t < p.tokens && r < p.row_threads && local < p.block_tokens;
+  const int h = r / (D / 8), c8 = r % (D / 8), grp = c8 >> 1;
+  uint4 k = make_uint4(0, 0, 0, 0), v = k;
+  long long slot = -1;
+  if (live) {
+    slot = __ldg(p.slots + t);
+    k = __ldg(reinterpret_cast<const uint4*>(p.k + t * p.token_stride[0] + h * p.head_stride[0] + c8 * 8));
+    v = __ldg(reinterpret_cast<const uint4*>(p.v + t * p.token_stride[1] + h * p.head_stride[1] + c8 * 8));
   }
-  const uint32_t scale = nan ? 0x7fu : e4m3_of(__fdiv_rn(mx, 6.f));
-  const float s = f16lo_to_f32(e4m3x2_to_f16(scale));
-  uint32_t code[2] = {0, 0};
-  if (s > 0.f) {  // (false for the NaN scale)
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      code[j >> 2] |= e2m1x2_of(__fdiv_rn(y[2 * j], s), __fdiv_rn(y[2 * j + 1], s)) << (8 * (j & 3));
-  }
-  if (__nv_bfloat16* out = which ? p.out[1] : p.out[0]) {
-    uint4 o[2];
-    uint32_t* ow = reinterpret_cast<uint32_t*>(o);
-    const float sf = s * f;
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      uint32_t hv[4];
-      e2m1x8_to_f16(code[j], hv);
-#pragma unroll
-      for (int m = 0; m < 4; ++m) {
-        const float2 v = f16x2_to_f32(hv[m]);
-        ow[4 * j + m] = pack_bf16x2(v.x * sf, v.y * sf);
-      }
-    }
-    uint4* dst = reinterpret_cast<uint4*>(out + row * D + grp * 16);
-    dst[0] = o[0];
-    dst[1] = o[1];
-  }
+  uint32_t k_scale, k_code, v_scale, v_code;
+  quantize(k, p.k_scale, k_scale, k_code, p.k_out != nullptr);
+  quantize(v, p.v_scale, v_scale, v_code, p.v_out != nullptr);
+  if (!live) return;
+  const long long out = (static_cast<long long>(t) * p.cache.heads + h) * D + c8 * 8;
+  if (p.k_out) *reinterpret_cast<uint4*>(p.k_out + out) = k;
+  if (p.v_out) *reinterpret_cast<uint4*>(p.v_out + out) = v;
   if (slot < 0) return;  // a padding token
   if (slot >= static_cast<long long>(p.cache.num_pages) << p.cache.shift) {
     atomicCAS(&g_cache_status, kDevOk, kDevBadIndex);
     return;
   }
-  const long long page = slot >> p.cache.shift;
   const int off = static_cast<int>(slot) & ((1 << p.cache.shift) - 1), key = off & 15;
-  char* tile = p.cache.base + page * p.cache.page_stride +
-               (static_cast<long long>(h) * (1 << (p.cache.shift - 4)) + (off >> 4)) * L::kTileBytes;
-  if (which == 0) {
-    *reinterpret_cast<uint2*>(tile + key * (D / 2) + grp * 8) = make_uint2(code[0], code[1]);
-    tile[L::k_scale_at(key, grp)] = static_cast<char>(scale);
+  char* tile = p.cache.base + (slot >> p.cache.shift) * p.cache.page_stride +
+               ((static_cast<long long>(h) << (p.cache.shift - 4)) + (off >> 4)) * L::kTileBytes;
+  *reinterpret_cast<uint32_t*>(tile + key * (D / 2) + c8 * 4) = k_code;
+  constexpr int kPiece = D / 16;  // bytes of a lane's V columns
+  if constexpr (kPiece >= 4) {
+    constexpr int kPer = kPiece / 4;  // threads of a piece
+    *reinterpret_cast<uint32_t*>(tile + L::v_piece_at(key, c8 / kPer) + c8 % kPer * 4) = v_code;
+  } else if constexpr (kPiece == 2) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      *reinterpret_cast<uint16_t*>(tile + L::v_piece_at(key, c8 * 2 + j)) = static_cast<uint16_t>(v_code >> (16 * j));
   } else {
-    // the 16 columns are 128 / D lanes' pieces of D / 16 bytes
-    constexpr int kPiece = D / 16;
-    if constexpr (kPiece == 8) {
-      *reinterpret_cast<uint2*>(tile + L::v_piece_at(key, grp)) = make_uint2(code[0], code[1]);
-    } else if constexpr (kPiece == 4) {
 #pragma unroll
-      for (int j = 0; j < 2; ++j) *reinterpret_cast<uint32_t*>(tile + L::v_piece_at(key, grp * 2 + j)) = code[j];
-    } else if constexpr (kPiece == 2) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        *reinterpret_cast<uint16_t*>(tile + L::v_piece_at(key, grp * 4 + j)) =
-            static_cast<uint16_t>(code[j >> 1] >> (16 * (j & 1)));
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) tile[L::v_piece_at(key, j)] = static_cast<char>(code[j >> 2] >> (8 * (j & 3)));
-    }
-    tile[L::v_scale_at(key, grp)] = static_cast<char>(scale);
+    for (int j = 0; j < 4; ++j) tile[L::v_piece_at(key, c8 * 4 + j)] = static_cast<char>(v_code >> (8 * j));
   }
+  if (c8 & 1)
+    tile[L::v_scale_at(key, grp)] = static_cast<char>(v_scale);
+  else
+    tile[L::k_scale_at(key, grp)] = static_cast<char>(k_scale);
 }
 
 struct GatherProblem {
@@ -133,113 +136,135 @@ struct GatherProblem {
   int width;
   const int* cu;
   int B, total;
-  __nv_bfloat16* out[2];
-  float factor[2];
+  __nv_bfloat16 *k, *v;
+  float k_scale, v_scale;
+  int head_warps;  // of a CTA's 8 warps on one group of tokens
 };
 
-constexpr int kGatherTokens = 16;
+constexpr int kGatherTokens = 16;  // of a warp
 
-// A CTA reads kGatherTokens packed rows back: each row's sequence is found by
-// bisection of the offsets once per CTA and followed from there.  One thread
-// per 8 columns (a 16-byte store), K and V in turn.
+// Where a packed row's values lie: head 0's tile and the key in it, or NULL
+// for a row outside every sequence or not to be found.
+__device__ __forceinline__ const char* find_row(const GatherProblem& p, int t, int tile_bytes, int& key) {
+  if (t >= p.total) return nullptr;
+  int lo = 0, hi = p.B;  // the last b with cu[b] <= t
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (__ldg(p.cu + mid) <= t)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  const int a = __ldg(p.cu + lo), e = __ldg(p.cu + lo + 1);
+  if (a < 0 || a > t || e < a) {
+    atomicCAS(&g_cache_status, kDevOk, kDevBadSeqlens);
+    return nullptr;
+  }
+  if (t >= e) return nullptr;  // behind the last sequence
+  const int pos = t - a, pg = pos >> p.cache.shift, off = pos & ((1 << p.cache.shift) - 1);
+  if (pg >= p.width) {
+    atomicCAS(&g_cache_status, kDevOk, kDevBadSeqlens);
+    return nullptr;
+  }
+  const int id = __ldg(p.table + lo * p.table_stride + pg);
+  if (id < 0 || id >= p.cache.num_pages) {
+    atomicCAS(&g_cache_status, kDevOk, kDevBadIndex);
+    return nullptr;
+  }
+  key = off & 15;
+  return p.cache.base + id * p.cache.page_stride + static_cast<long long>(off >> 4) * tile_bytes;
+}
+
+__device__ __forceinline__ uint4 expand(uint32_t code, uint32_t scale, float f) {
+  const float s = f16lo_to_f32(e4m3x2_to_f16(scale)) * f;
+  uint32_t hv[4], o[4];
+  e2m1x8_to_f16(code, hv);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 v = f16x2_to_f32(hv[i]);
+    o[i] = pack_bf16x2(v.x * s, v.y * s);
+  }
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+// A warp reads kGatherTokens packed rows of one head after another back: a
+// lane takes 8 columns (a 16-byte store) of every (D / 8)-th row, all loads
+// of the rows first.  Where the rows lie is found once per CTA, a thread per
+// row.
 template <int D>
 __global__ void __launch_bounds__(256) fa2_kv4_gather_kernel(const GatherProblem p) {
   using L = Kv4<D>;
+  constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes, kIters = kGatherTokens / kAtOnce;
+  __shared__ const char* s_tile[8 * kGatherTokens];
+  __shared__ int s_key[8 * kGatherTokens];
   griddep_wait();
   griddep_launch_dependents();
-  __shared__ const char* s_tile[kGatherTokens];  // the token's tile of head 0, or NULL
-  __shared__ int s_key[kGatherTokens];
-  const int t0 = blockIdx.x * kGatherTokens;
-  if (threadIdx.x < kGatherTokens) {
-    const int t = t0 + threadIdx.x;
-    const char* tile = nullptr;
+  const int groups = 8 / p.head_warps;  // of tokens
+  const int t0 = blockIdx.x * groups * kGatherTokens;
+  if (threadIdx.x < groups * kGatherTokens) {
     int key = 0;
-    if (t < p.total) {
-      int lo = 0, hi = p.B;  // the last b with cu[b] <= t
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (__ldg(p.cu + mid) <= t)
-          lo = mid;
-        else
-          hi = mid;
-      }
-      const int a = __ldg(p.cu + lo), e = __ldg(p.cu + lo + 1);
-      if (a >= 0 && a <= t && t < e) {
-        const int pos = t - a, pg = pos >> p.cache.shift, off = pos & ((1 << p.cache.shift) - 1);
-        if (pg >= p.width) {
-          atomicCAS(&g_cache_status, kDevOk, kDevBadSeqlens);
-        } else {
-          const int id = __ldg(p.table + lo * p.table_stride + pg);
-          if (id < 0 || id >= p.cache.num_pages) {
-            atomicCAS(&g_cache_status, kDevOk, kDevBadIndex);
-          } else {
-            tile = p.cache.base + id * p.cache.page_stride + static_cast<long long>(off >> 4) * L::kTileBytes;
-            key = off & 15;
-          }
-        }
-      } else if (a > t || a < 0 || e < a) {  // (a row past the last sequence is no error)
-        atomicCAS(&g_cache_status, kDevOk, kDevBadSeqlens);
-      }
-    }
-    s_tile[threadIdx.x] = tile;
+    s_tile[threadIdx.x] = find_row(p, t0 + threadIdx.x, L::kTileBytes, key);
     s_key[threadIdx.x] = key;
   }
   __syncthreads();
-  constexpr int kPer = D / 8;  // threads of a head
-  const int row_threads = p.cache.heads * kPer;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int group = warp / p.head_warps;
+  if (group >= groups) return;
+  const int c8 = lane % kLanes, grp = c8 >> 1;
   const long long head_bytes = static_cast<long long>(L::kTileBytes) << (p.cache.shift - 4);
-  for (int i = threadIdx.x; i < row_threads * kGatherTokens; i += 256) {
-    const int tok = i / row_threads, r = i - tok * row_threads;
-    const char* tile = s_tile[tok];
-    if (!tile) continue;
-    const int h = r / kPer, c8 = r % kPer, key = s_key[tok];
-    tile += h * head_bytes;
-    const long long dst = (static_cast<long long>(t0 + tok) * p.cache.heads + h) * D + c8 * 8;
+  for (int h = warp - group * p.head_warps; h < p.cache.heads; h += p.head_warps) {
+    uint32_t kc[kIters], vc[kIters], ks[kIters], vs[kIters];
 #pragma unroll
-    for (int which = 0; which < 2; ++which) {
-      uint32_t code;
-      int scale_at;
-      if (which == 0) {
-        code = *reinterpret_cast<const uint32_t*>(tile + key * (D / 2) + c8 * 4);
-        scale_at = L::k_scale_at(key, c8 >> 1);
-      } else {
+    for (int i = 0; i < kIters; ++i) {
+      const int row = group * kGatherTokens + i * kAtOnce + lane / kLanes;
+      kc[i] = vc[i] = ks[i] = vs[i] = 0;
+      if (const char* tile = s_tile[row]) {
+        const int key = s_key[row];
+        tile += h * head_bytes;
+        kc[i] = __ldg(reinterpret_cast<const uint32_t*>(tile + key * (D / 2) + c8 * 4));
+        ks[i] = __ldg(reinterpret_cast<const uint8_t*>(tile + L::k_scale_at(key, grp)));
+        vs[i] = __ldg(reinterpret_cast<const uint8_t*>(tile + L::v_scale_at(key, grp)));
         constexpr int kPiece = D / 16;
-        if constexpr (kPiece == 8) {
-          code = *reinterpret_cast<const uint32_t*>(tile + L::v_piece_at(key, c8 >> 1) + (c8 & 1) * 4);
-        } else if constexpr (kPiece == 4) {
-          code = *reinterpret_cast<const uint32_t*>(tile + L::v_piece_at(key, c8));
+        if constexpr (kPiece >= 4) {
+          constexpr int kPer = kPiece / 4;
+          vc[i] = __ldg(reinterpret_cast<const uint32_t*>(tile + L::v_piece_at(key, c8 / kPer) + c8 % kPer * 4));
         } else if constexpr (kPiece == 2) {
-          code = *reinterpret_cast<const uint16_t*>(tile + L::v_piece_at(key, c8 * 2)) |
-                 static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(tile + L::v_piece_at(key, c8 * 2 + 1))) << 16;
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+            vc[i] |= static_cast<uint32_t>(__ldg(reinterpret_cast<const uint16_t*>(tile + L::v_piece_at(key, c8 * 2 + j)))) << (16 * j);
         } else {
-          code = 0;
 #pragma unroll
           for (int j = 0; j < 4; ++j)
-            code |= static_cast<uint32_t>(static_cast<uint8_t>(tile[L::v_piece_at(key, c8 * 4 + j)])) << (8 * j);
+            vc[i] |= static_cast<uint32_t>(__ldg(reinterpret_cast<const uint8_t*>(tile + L::v_piece_at(key, c8 * 4 + j)))) << (8 * j);
         }
-        scale_at = L::v_scale_at(key, c8 >> 1);
       }
-      const float s = f16lo_to_f32(e4m3x2_to_f16(static_cast<uint8_t>(tile[scale_at]))) * p.factor[which];
-      uint32_t hv[4], o[4];
-      e2m1x8_to_f16(code, hv);
+    }
 #pragma unroll
-      for (int m = 0; m < 4; ++m) {
-        const float2 v = f16x2_to_f32(hv[m]);
-        o[m] = pack_bf16x2(v.x * s, v.y * s);
-      }
-      *reinterpret_cast<uint4*>(p.out[which] + dst) = make_uint4(o[0], o[1], o[2], o[3]);
+    for (int i = 0; i < kIters; ++i) {
+      const int row = group * kGatherTokens + i * kAtOnce + lane / kLanes;
+      if (!s_tile[row]) continue;
+      const long long dst = (static_cast<long long>(t0 + row) * p.cache.heads + h) * D + c8 * 8;
+      *reinterpret_cast<uint4*>(p.k + dst) = expand(kc[i], ks[i], p.k_scale);
+      *reinterpret_cast<uint4*>(p.v + dst) = expand(vc[i], vs[i], p.v_scale);
     }
   }
 }
 
 template <int D>
-int launch_append_d(const AppendProblem& p, cudaStream_t st) {
-  return launch_pdl(fa2_kv4_append_kernel<D>, dim3(static_cast<unsigned>((p.groups + 255) / 256), 2), dim3(256), 0, st, p);
+int launch_append_d(AppendProblem p, cudaStream_t st) {
+  // whole tokens to a CTA; a token of more than 256 threads spreads over
+  // blockIdx.y
+  p.row_threads = p.cache.heads * (D / 8);
+  p.block_tokens = p.row_threads >= 256 ? 1 : 256 / p.row_threads;
+  const unsigned parts = (p.row_threads + 255) / 256;
+  return launch_pdl(fa2_kv4_append_kernel<D>, dim3(static_cast<unsigned>((p.tokens + p.block_tokens - 1) / p.block_tokens), parts),
+                    dim3(256), 0, st, p);
 }
 template <int D>
-int launch_gather_d(const GatherProblem& p, cudaStream_t st) {
-  return launch_pdl(fa2_kv4_gather_kernel<D>, dim3(static_cast<unsigned>((p.total + kGatherTokens - 1) / kGatherTokens)),
-                    dim3(256), 0, st, p);
+int launch_gather_d(GatherProblem p, cudaStream_t st) {
+  p.head_warps = p.cache.heads < 8 ? p.cache.heads : 8;
+  const int per = 8 / p.head_warps * kGatherTokens;
+  return launch_pdl(fa2_kv4_gather_kernel<D>, dim3(static_cast<unsigned>((p.total + per - 1) / per)), dim3(256), 0, st, p);
 }
 
 }  // namespace
@@ -258,7 +283,7 @@ int check_cache(const void* cache, long long page_stride, int num_pages, int pag
   if (page_size != 16 && page_size != 32 && page_size != 64 && page_size != 128) return FA2_ERR_SHAPE;
   if (!head_dim_ok(d)) return FA2_ERR_HEADDIM;
   if (!cache) return FA2_ERR_NULL;
-  if (H_kv > (1 << 20) || page_stride < static_cast<long long>(kv4_page_bytes(H_kv, page_size, d)) ||
+  if (H_kv > (1 << 16) || page_stride < static_cast<long long>(kv4_page_bytes(H_kv, page_size, d)) ||
       page_stride > (1LL << 40))
     return FA2_ERR_SHAPE;
   if (!aligned(cache, 16) || page_stride % 16 != 0) return FA2_ERR_ALIGN;
@@ -308,8 +333,7 @@ int fa2_kv4_append(const void* k, const void* v, const long long* strides, void*
   if (!aligned(k, 16) || !aligned(v, 16) || !aligned(slots, 8) || !aligned(k_out, 16) || !aligned(v_out, 16))
     return FA2_ERR_ALIGN;
   AppendProblem p{};
-  p.groups = static_cast<long long>(num_tokens) * H_kv * (d / 16);
-  if ((p.groups + 255) / 256 > 0x7fffffffLL) return FA2_ERR_SHAPE;
+  p.tokens = num_tokens;
   size_t span[2];
   for (int i = 0; i < 2; ++i) {
     p.token_stride[i] = num_tokens > 1 && strides ? strides[2 * i] : static_cast<long long>(H_kv) * d;
@@ -330,12 +354,12 @@ int fa2_kv4_append(const void* k, const void* v, const long long* strides, void*
     for (int j = i + 1; j < 3; ++j)
       if (outs[j].lo != outs[j].hi && overlap(outs[i], outs[j])) return FA2_ERR_ALIAS;
   }
-  p.x[0] = static_cast<const __nv_bfloat16*>(k);
-  p.x[1] = static_cast<const __nv_bfloat16*>(v);
-  p.out[0] = static_cast<__nv_bfloat16*>(k_out);
-  p.out[1] = static_cast<__nv_bfloat16*>(v_out);
-  p.factor[0] = k_scale;
-  p.factor[1] = v_scale;
+  p.k = static_cast<const __nv_bfloat16*>(k);
+  p.v = static_cast<const __nv_bfloat16*>(v);
+  p.k_out = static_cast<__nv_bfloat16*>(k_out);
+  p.v_out = static_cast<__nv_bfloat16*>(v_out);
+  p.k_scale = k_scale;
+  p.v_scale = v_scale;
   p.slots = slots;
   p.cache = paged_cache(cache, page_stride, num_pages, page_size, H_kv);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
@@ -352,7 +376,6 @@ int fa2_kv4_gather(const void* cache, long long page_stride, const int* block_ta
   if (int rc = check_cache(cache, page_stride, num_pages, page_size, H_kv, d)) return rc;
   if (B < 1 || total < 0 || total > (1 << 30) || table_width < 1 || (B > 1 && table_stride < table_width))
     return FA2_ERR_SHAPE;
-  if (H_kv > (1 << 16)) return FA2_ERR_SHAPE;
   if (!power_of_two(k_scale) || !power_of_two(v_scale)) return FA2_ERR_SCALE;
   if (total == 0) return FA2_OK;
   if (!block_table || !cu_seqlens || !k || !v) return FA2_ERR_NULL;
@@ -366,8 +389,7 @@ int fa2_kv4_gather(const void* cache, long long page_stride, const int* block_ta
     if (overlap(rk, r) || overlap(rv, r)) return FA2_ERR_ALIAS;
   if (overlap(rk, rv)) return FA2_ERR_ALIAS;
   const GatherProblem p{paged_cache(cache, page_stride, num_pages, page_size, H_kv), block_table, table_stride, table_width,
-                        cu_seqlens, B, total,
-                        {static_cast<__nv_bfloat16*>(k), static_cast<__nv_bfloat16*>(v)}, {k_scale, v_scale}};
+                        cu_seqlens, B, total, static_cast<__nv_bfloat16*>(k), static_cast<__nv_bfloat16*>(v), k_scale, v_scale, 0};
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   const int e = d == 16    ? launch_gather_d<16>(p, st)
                 : d == 32  ? launch_gather_d<32>(p, st)

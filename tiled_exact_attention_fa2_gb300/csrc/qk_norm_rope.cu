@@ -16,10 +16,12 @@
 // and 20 flops): one read of every input, one write of every output, nothing
 // kept in between (r is recomputed by the backward pass).  A row is held by
 // d / 8 lanes, 8 columns (16 bytes) each, so a warp covers 32 * 8 / d rows
-// with whole 32-byte sectors; the two sums of a row are butterfly shuffles
-// within its lanes and a half-split pair's partner columns come by one
-// shuffle.  A lane group takes several heads of one token, which loads the
-// token's cosines and sines once (they are twice a head's bytes).
+// with whole 32-byte sectors; a row's sums are butterfly shuffles within its
+// lanes.  With a partner column's value (of a half-split pair one shuffle of
+// the packed bf16 words away, of an interleaved one in the same word) a
+// rotated value is x c' + x_partner s', so gain and rotation are folded into
+// two factors per column that a lane makes once per token and uses for
+// several heads; the arithmetic is on packed pairs of fp32.
 //
 // All sums and the arithmetic are fp32; the one rounding to bf16 is at the
 // store.
@@ -47,44 +49,33 @@ struct View {  // [B, heads, N, d] with the last dimension contiguous; strides i
 struct NormProblem {
   View x[2], y[2], g[2];  // of q and k: input, output (dx in the backward pass), dout (backward only)
   const void* w[2];
-  float* partial;  // backward: [CTA][2][d] sums for dw, or NULL
+  float* partial;  // backward: [CTA][d] sums for dw (a CTA works for q or for k), or NULL
   const float* rope;
   const int* positions;
-  int heads[2];  // H, H_kv
+  int heads[2], chunks[2];  // heads, and lane-group items per token, of q and k
+  unsigned items[2];        // B * N * chunks
+  unsigned ctas_q;          // CTAs below this one work for q
   int N, rot, max_pos, w_fp32;
-  int chunks;     // lane-group items per token
-  unsigned items;  // B * N * chunks
   float eps;
 };
 
-__device__ __forceinline__ void load8(const View& v, long long b, int h, int n, int col, uint4* out) {
-  const __nv_bfloat16* p = reinterpret_cast<const __nv_bfloat16*>(v.p) + b * v.sb + h * v.sh + n * v.sn + col;
-  *out = *reinterpret_cast<const uint4*>(p);
-}
-__device__ __forceinline__ void store8(const View& v, long long b, int h, int n, int col, const float (&f)[8]) {
-  __nv_bfloat16* p = reinterpret_cast<__nv_bfloat16*>(v.p) + b * v.sb + h * v.sh + n * v.sn + col;
-  *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]),
-                                            pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
-}
-__device__ __forceinline__ void widen8(const uint4& u, float (&f)[8]) {
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 t = unpack_bf16x2(w[i]);
-    f[2 * i] = t.x;
-    f[2 * i + 1] = t.y;
-  }
-}
-__device__ __forceinline__ void load_gain(const void* w, int fp32, int col, float (&f)[8]) {
+// The gains of 8 columns (16-byte aligned).
+__device__ __forceinline__ void gains(float (&f)[8], const void* w, int fp32, int col) {
   if (!w) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) f[i] = 1.f;
   } else if (fp32) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = static_cast<const float*>(w)[col + i];
+    const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(w) + col);
+    const float4 a = __ldg(p), b = __ldg(p + 1);
+    f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
   } else {
+    const uint4 u = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(w) + col));
+    const uint32_t v[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = __bfloat162float(static_cast<const __nv_bfloat16*>(w)[col + i]);
+    for (int i = 0; i < 4; ++i) {
+      const float2 t = unpack_bf16x2(v[i]);
+      f[2 * i] = t.x, f[2 * i + 1] = t.y;
+    }
   }
 }
 
@@ -95,96 +86,101 @@ __device__ __forceinline__ float sum_lanes(float v) {
   return v;
 }
 
-// What one lane needs of its token's rotation: the cosines and signed sines
-// of its 8 columns.  Half split: one pair per column, out = y c + partner s
-// (s is negative in the low half).  Interleaved: 4 pairs.  Columns past the
-// rotated part get c = 1, s = 0.
-template <bool INTER>
-struct Turn {
-  float c[INTER ? 4 : 8], s[INTER ? 4 : 8];
-  int partner;  // lane that holds the partner columns (half split)
-};
-
-template <int D, bool INTER>
-__device__ __forceinline__ void load_turn(Turn<INTER>& t, const NormProblem& p, int pos, int col, bool back) {
-  constexpr int kN = INTER ? 4 : 8;
-  const int half = p.rot >> 1;
-  const int lane = threadIdx.x & 31;
-  t.partner = lane;
-  if (col < p.rot) {
-    int at;
-    float sign;
-    if (INTER) {
-      at = col >> 1;
-      sign = 1.f;
-    } else {
-      const bool low = col < half;
-      at = low ? col : col - half;
-      sign = low ? -1.f : 1.f;
-      t.partner = lane + (low ? half : -half) / 8;
-    }
-    if (back) sign = -sign;
-    const float* row = p.rope + static_cast<long long>(pos) * p.rot + at;
-#pragma unroll
-    for (int i = 0; i < kN; i += 4) {
-      const float4 c = __ldg(reinterpret_cast<const float4*>(row + i));
-      const float4 s = __ldg(reinterpret_cast<const float4*>(row + half + i));
-      t.c[i] = c.x, t.c[i + 1] = c.y, t.c[i + 2] = c.z, t.c[i + 3] = c.w;
-      t.s[i] = sign * s.x, t.s[i + 1] = sign * s.y, t.s[i + 2] = sign * s.z, t.s[i + 3] = sign * s.w;
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < kN; ++i) t.c[i] = 1.f, t.s[i] = 0.f;
-  }
+// The two bf16 of a word as a packed pair of fp32.
+__device__ __forceinline__ uint64_t widen2(uint32_t w) {
+  return f2_pack(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
 }
 
-// Columns past the rotated part are their own partner with s = 0; an
-// infinity there would turn into NaN through inf * 0, so they are selected.
+// The rotation partners of a lane's 8 columns `col` ..: which lane holds them
+// (half split; of an interleaved pair the other half of the word), and
+// whether these columns turn at all.
+struct Partner {
+  int lane;
+  bool turns, low;
+};
 template <bool INTER>
-__device__ __forceinline__ void rotate(const Turn<INTER>& t, bool turns, const float (&y)[8], float (&o)[8]) {
+__device__ __forceinline__ Partner partner_of(int rot, int col) {
+  Partner t;
+  t.lane = threadIdx.x & 31;
+  t.turns = col < rot;
+  t.low = col < rot / 2;
+  if (!INTER && t.turns) t.lane += t.low ? rot / 16 : -(rot / 16);
+  return t;
+}
+
+// The partners' words (zeros where nothing turns: their factor is 0, and an
+// infinity must not meet it).
+template <bool INTER>
+__device__ __forceinline__ uint32_t partner_word(const Partner& t, uint32_t w) {
+  const uint32_t v = INTER ? __byte_perm(w, 0, 0x1032) : __shfl_sync(0xffffffffu, w, t.lane);
+  return t.turns ? v : 0u;
+}
+
+// Cosines and signed sines of the lane's 8 columns at a position:
+// rotated_j = x_j c_j + partner_j s_j.  `back`: turned the other way.
+template <bool INTER>
+__device__ __forceinline__ void load_turn(float (&c)[8], float (&s)[8], const Partner& t, const NormProblem& p, int pos,
+                                          int col, bool back) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) c[i] = 1.f, s[i] = 0.f;
+  if (!t.turns) return;
+  const int half = p.rot >> 1;
+  const float* row = p.rope + static_cast<long long>(pos) * p.rot;
   if (INTER) {
+    const float4 a = __ldg(reinterpret_cast<const float4*>(row + (col >> 1)));
+    const float4 b = __ldg(reinterpret_cast<const float4*>(row + half + (col >> 1)));
+    const float cc[4] = {a.x, a.y, a.z, a.w}, ss[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float a = y[2 * i], b = y[2 * i + 1];
-      o[2 * i] = turns ? a * t.c[i] - b * t.s[i] : a;
-      o[2 * i + 1] = turns ? b * t.c[i] + a * t.s[i] : b;
+      c[2 * i] = c[2 * i + 1] = cc[i];
+      s[2 * i] = back ? ss[i] : -ss[i];
+      s[2 * i + 1] = back ? -ss[i] : ss[i];
     }
   } else {
+    row += t.low ? col : col - half;
+    const float sign = t.low != back ? -1.f : 1.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float q = __shfl_sync(0xffffffffu, y[i], t.partner);
-      o[i] = turns ? y[i] * t.c[i] + q * t.s[i] : y[i];
+    for (int i = 0; i < 8; i += 4) {
+      const float4 a = __ldg(reinterpret_cast<const float4*>(row + i));
+      const float4 b = __ldg(reinterpret_cast<const float4*>(row + half + i));
+      c[i] = a.x, c[i + 1] = a.y, c[i + 2] = a.z, c[i + 3] = a.w;
+      s[i] = sign * b.x, s[i + 1] = sign * b.y, s[i + 2] = sign * b.z, s[i + 3] = sign * b.w;
     }
   }
 }
 
-// The lane group's item: heads [h0, h0 + ROWS) of token (b, n).  Heads past
-// the last are left out by `h < total`; an item past the end, or at a bad
-// position, does the arithmetic on nothing (shuffles are warp-wide).
+// A lane group's item: `count` heads from h0 on of token (b, n); none for an
+// item past the end or at a bad position (it does its arithmetic on nothing:
+// shuffles are warp-wide).
 struct Item {
   long long b;
-  int n, h0, pos;
-  bool live;
+  int n, h0, pos, count;
 };
 
 template <int ROWS>
-__device__ __forceinline__ Item find_item(const NormProblem& p, unsigned id) {
+__device__ __forceinline__ Item find_item(const NormProblem& p, int which, unsigned id) {
   Item it;
-  it.live = id < p.items;
-  const unsigned tok = it.live ? id / p.chunks : 0;
-  it.h0 = it.live ? static_cast<int>(id - tok * p.chunks) * ROWS : 0;
+  const bool live = id < p.items[which];
+  const unsigned chunks = p.chunks[which];
+  const unsigned tok = live ? id / chunks : 0;
+  it.h0 = live ? static_cast<int>(id - tok * chunks) * ROWS : 0;
+  it.count = live ? min(ROWS, p.heads[which] - it.h0) : 0;
   it.b = tok / static_cast<unsigned>(p.N);
   it.n = static_cast<int>(tok - static_cast<unsigned>(it.b) * p.N);
   it.pos = it.n;
   if (p.rot > 0) {
-    if (p.positions && it.live) it.pos = __ldg(p.positions + tok);
-    if (it.live && (it.pos < 0 || it.pos >= p.max_pos)) {
+    if (p.positions && live) it.pos = __ldg(p.positions + tok);
+    if (live && (it.pos < 0 || it.pos >= p.max_pos)) {
       atomicCAS(&g_norm_status, kDevOk, kDevBadIndex);
-      it.live = false;
+      it.count = 0;
     }
-    if (!it.live) it.pos = 0;
+    if (it.count == 0) it.pos = 0;
   }
   return it;
+}
+
+__device__ __forceinline__ char* row_at(const View& v, const Item& it, int col) {
+  return v.p + 2 * (it.b * v.sb + it.n * v.sn + it.h0 * v.sh + col);
 }
 
 template <int D, bool INTER, int ROWS>
@@ -193,171 +189,222 @@ __global__ void __launch_bounds__(256) fa2_qk_norm_rope_kernel(const NormProblem
   griddep_wait();
   griddep_launch_dependents();
   const int col = (threadIdx.x % kLanes) * 8;
-  const Item it = find_item<ROWS>(p, blockIdx.x * (256u / kLanes) + threadIdx.x / kLanes);
-  const int total = p.heads[0] + p.heads[1];
+  const int which = blockIdx.x >= p.ctas_q;
+  const unsigned cta = which ? blockIdx.x - p.ctas_q : blockIdx.x;
+  const Item it = find_item<ROWS>(p, which, cta * (256u / kLanes) + threadIdx.x / kLanes);
+  const char* src = row_at(p.x[which], it, col);
+  const long long sx = 2 * p.x[which].sh;
   uint4 raw[ROWS];
 #pragma unroll
   for (int i = 0; i < ROWS; ++i) {
-    const int h = it.h0 + i, which = h >= p.heads[0];
     raw[i] = make_uint4(0, 0, 0, 0);
-    if (it.live && h < total) load8(p.x[which], it.b, h - (which ? p.heads[0] : 0), it.n, col, &raw[i]);
+    if (i < it.count) raw[i] = *reinterpret_cast<const uint4*>(src + i * sx);
   }
-  Turn<INTER> turn;
-  load_turn<D, INTER>(turn, p, it.pos, col, false);
+  const Partner partner = partner_of<INTER>(p.rot, col);
+  uint64_t wc[4], ws[4];  // gain times cosine; the partner's gain times sine
+  {
+    float c[8], s[8];
+    load_turn<INTER>(c, s, partner, p, it.pos, col, false);
+    float w[8], pw[8];
+    gains(w, p.w[which], p.w_fp32, col);
+    if (!INTER) gains(pw, p.w[which], p.w_fp32, col + (partner.lane - static_cast<int>(threadIdx.x & 31)) * 8);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      c[j] *= w[j];
+      s[j] *= INTER ? w[j ^ 1] : pw[j];
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) wc[j] = f2_pack(c[2 * j], c[2 * j + 1]), ws[j] = f2_pack(s[2 * j], s[2 * j + 1]);
+  }
+  char* dst = row_at(p.y[which], it, col);
+  const long long sy = 2 * p.y[which].sh;
 #pragma unroll
   for (int i = 0; i < ROWS; ++i) {
-    const int h = it.h0 + i, which = h >= p.heads[0];
-    float x[8], w[8], o[8];
-    widen8(raw[i], x);
-    load_gain(p.w[which], p.w_fp32, col, w);
-    float ss = 0.f;
+    const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+    uint64_t x[4], o[4], sq = 0;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) ss = fmaf(x[j], x[j], ss);
-    const float r = rsqrtf(sum_lanes<kLanes>(ss) * (1.f / D) + p.eps);
+    for (int j = 0; j < 4; ++j) {
+      x[j] = widen2(w[j]);
+      sq = ffma2(x[j], x[j], sq);
+      o[j] = ffma2(widen2(partner_word<INTER>(partner, w[j])), ws[j], fmul2(x[j], wc[j]));
+    }
+    const float2 q = f2_unpack(sq);
+    const float r = rsqrtf(sum_lanes<kLanes>(q.x + q.y) * (1.f / D) + p.eps);
+    const uint64_t rr = f2_pack(r, r);
+    uint32_t out[4];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) x[j] = x[j] * r * w[j];
-    rotate<INTER>(turn, col < p.rot, x, o);
-    if (it.live && h < total) store8(p.y[which], it.b, h - (which ? p.heads[0] : 0), it.n, col, o);
+    for (int j = 0; j < 4; ++j) {
+      const float2 f = f2_unpack(fmul2(o[j], rr));
+      out[j] = pack_bf16x2(f.x, f.y);
+    }
+    if (i < it.count) *reinterpret_cast<uint4*>(dst + i * sy) = make_uint4(out[0], out[1], out[2], out[3]);
   }
 }
 
-// Backward: persistent CTAs, so that each lane sums dw of its 8 columns (of
-// q and of k) in registers over all its rows; the CTA's sums are joined in
-// shared memory and written to its own slot, which dw_kernel adds up in a
-// fixed order (the result does not depend on the order CTAs run in).
+// Backward: persistent CTAs, each for q or for k (in proportion to their
+// heads), so that a lane sums dw of its 8 columns in registers over all its
+// rows; the CTA's sums are joined in shared memory and written to its own
+// slot, which the dw kernel adds up in a fixed order (the result does not
+// depend on the order CTAs run in).
 template <int D, bool INTER, int ROWS>
-__global__ void __launch_bounds__(256) fa2_qk_norm_rope_bwd_kernel(const NormProblem p) {
+__global__ void __launch_bounds__(256, 3) fa2_qk_norm_rope_bwd_kernel(const NormProblem p) {
   constexpr int kLanes = D / 8, kGroups = 256 / kLanes;
   __shared__ float red[kGroups][D];
   griddep_wait();
   griddep_launch_dependents();
   const int col = (threadIdx.x % kLanes) * 8, group = threadIdx.x / kLanes;
-  const int total = p.heads[0] + p.heads[1];
-  float dw[2][8] = {};
-  float w[2][8];
-  load_gain(p.w[0], p.w_fp32, col, w[0]);
-  load_gain(p.w[1], p.w_fp32, col, w[1]);
-  const unsigned step = gridDim.x * kGroups;
+  const int which = blockIdx.x >= p.ctas_q;
+  const unsigned cta = which ? blockIdx.x - p.ctas_q : blockIdx.x;
+  const unsigned step = (which ? gridDim.x - p.ctas_q : p.ctas_q) * kGroups;
+  const Partner partner = partner_of<INTER>(p.rot, col);
+  const long long sx = 2 * p.x[which].sh, sg = 2 * p.g[which].sh, sy = 2 * p.y[which].sh;
+  uint64_t w[4], dw[4];
+  {
+    float f[8];
+    gains(f, p.w[which], p.w_fp32, col);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) w[j] = f2_pack(f[2 * j], f[2 * j + 1]), dw[j] = 0;
+  }
   // (the loop bound is the same for every lane of a warp: shuffles inside)
-  const unsigned rounds = (p.items + step - 1) / step;
+  const unsigned rounds = (p.items[which] + step - 1) / step;
   for (unsigned k = 0; k < rounds; ++k) {
-    const Item it = find_item<ROWS>(p, k * step + blockIdx.x * kGroups + group);
+    const Item it = find_item<ROWS>(p, which, k * step + cta * kGroups + group);
+    const char* px = row_at(p.x[which], it, col);
+    const char* pg = row_at(p.g[which], it, col);
+    char* py = row_at(p.y[which], it, col);
     uint4 rx[ROWS], rg[ROWS];
 #pragma unroll
     for (int i = 0; i < ROWS; ++i) {
-      const int h = it.h0 + i, which = h >= p.heads[0];
       rx[i] = rg[i] = make_uint4(0, 0, 0, 0);
-      if (it.live && h < total) {
-        load8(p.x[which], it.b, h - (which ? p.heads[0] : 0), it.n, col, &rx[i]);
-        load8(p.g[which], it.b, h - (which ? p.heads[0] : 0), it.n, col, &rg[i]);
+      if (i < it.count) {
+        rx[i] = *reinterpret_cast<const uint4*>(px + i * sx);
+        rg[i] = *reinterpret_cast<const uint4*>(pg + i * sg);
       }
     }
-    Turn<INTER> turn;
-    load_turn<D, INTER>(turn, p, it.pos, col, true);
+    uint64_t c[4], s[4];
+    {
+      float cf[8], sf[8];
+      load_turn<INTER>(cf, sf, partner, p, it.pos, col, true);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) c[j] = f2_pack(cf[2 * j], cf[2 * j + 1]), s[j] = f2_pack(sf[2 * j], sf[2 * j + 1]);
+    }
 #pragma unroll
     for (int i = 0; i < ROWS; ++i) {
-      const int h = it.h0 + i, which = h >= p.heads[0];
-      const bool real = it.live && h < total;
-      float x[8], o[8], g[8];
-      widen8(rx[i], x);
-      widen8(rg[i], o);
-      rotate<INTER>(turn, col < p.rot, o, g);
-      float ss = 0.f, hx = 0.f;
+      const uint32_t wx[4] = {rx[i].x, rx[i].y, rx[i].z, rx[i].w}, wg[4] = {rg[i].x, rg[i].y, rg[i].z, rg[i].w};
+      uint64_t x[4], g[4], h[4], sq = 0, hx = 0;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        ss = fmaf(x[j], x[j], ss);
-        o[j] = g[j] * (which ? w[1][j] : w[0][j]);
-        hx = fmaf(o[j], x[j], hx);
+      for (int j = 0; j < 4; ++j) {
+        x[j] = widen2(wx[j]);
+        g[j] = ffma2(widen2(partner_word<INTER>(partner, wg[j])), s[j], fmul2(widen2(wg[j]), c[j]));
+        h[j] = fmul2(g[j], w[j]);
+        sq = ffma2(x[j], x[j], sq);
+        hx = ffma2(h[j], x[j], hx);
       }
-      ss = sum_lanes<kLanes>(ss);
-      hx = sum_lanes<kLanes>(hx);
-      const float r = rsqrtf(ss * (1.f / D) + p.eps);
-      const float along = r * r * (hx * (1.f / D));
+      const float2 q = f2_unpack(sq), v = f2_unpack(hx);
+      const float r = rsqrtf(sum_lanes<kLanes>(q.x + q.y) * (1.f / D) + p.eps);
+      // (a row left out has x = dout = 0 and adds nothing)
+      const float along = -r * r * (sum_lanes<kLanes>(v.x + v.y) * (1.f / D));
+      const uint64_t rr = f2_pack(r, r), aa = f2_pack(along, along);
+      uint32_t out[4];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float t = real ? g[j] * x[j] * r : 0.f;
-        if (which)
-          dw[1][j] += t;
-        else
-          dw[0][j] += t;
-        o[j] = r * (o[j] - x[j] * along);
+      for (int j = 0; j < 4; ++j) {
+        dw[j] = ffma2(g[j], fmul2(x[j], rr), dw[j]);
+        const float2 f = f2_unpack(fmul2(ffma2(x[j], aa, h[j]), rr));
+        out[j] = pack_bf16x2(f.x, f.y);
       }
-      if (real) store8(p.y[which], it.b, h - (which ? p.heads[0] : 0), it.n, col, o);
+      if (i < it.count) *reinterpret_cast<uint4*>(py + i * sy) = make_uint4(out[0], out[1], out[2], out[3]);
     }
   }
   if (!p.partial) return;
 #pragma unroll
-  for (int which = 0; which < 2; ++which) {
-    __syncthreads();
-#pragma unroll
-    for (int j = 0; j < 8; ++j) red[group][col + j] = dw[which][j];
-    __syncthreads();
-    for (int c = threadIdx.x; c < D; c += 256) {
-      float s = 0.f;
+  for (int j = 0; j < 4; ++j) {
+    const float2 f = f2_unpack(dw[j]);
+    red[group][col + 2 * j] = f.x;
+    red[group][col + 2 * j + 1] = f.y;
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < D; i += 256) {
+    float t = 0.f;
 #pragma unroll 8
-      for (int i = 0; i < kGroups; ++i) s += red[i][c];
-      p.partial[(static_cast<size_t>(blockIdx.x) * 2 + which) * D + c] = s;
-    }
+    for (int k = 0; k < kGroups; ++k) t += red[k][i];
+    p.partial[static_cast<size_t>(blockIdx.x) * D + i] = t;
   }
 }
 
-// dw[which][c] = sum over the CTAs' slots: 32 columns per block, 8 warps that
-// each add every eighth slot, then the 8 sums in order.
-__global__ void __launch_bounds__(256) fa2_qk_norm_dw_kernel(const float* __restrict__ partial, int slots, int d,
+// dw of q (blockIdx.y = 0) and k: the sums of their CTAs' slots, 32 columns
+// per block, 8 warps that each add every eighth slot, then the 8 sums in
+// order.
+__global__ void __launch_bounds__(256) fa2_qk_norm_dw_kernel(const float* __restrict__ partial, int slots_q, int slots, int d,
                                                              float* dwq, float* dwk) {
   __shared__ float red[8][32];
   griddep_wait();
   griddep_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int c = blockIdx.x * 32 + lane;  // of 2 d
+  const int c = blockIdx.x * 32 + lane;
+  const int first = blockIdx.y ? slots_q : 0, last = blockIdx.y ? slots : slots_q;
+  float* out = blockIdx.y ? dwk : dwq;
+  if (!out) return;
   float s = 0.f;
-  if (c < 2 * d)
-    for (int i = warp; i < slots; i += 8) s += partial[static_cast<size_t>(i) * 2 * d + c];
+  if (c < d)
+#pragma unroll 8
+    for (int i = first + warp; i < last; i += 8) s += partial[static_cast<size_t>(i) * d + c];
   red[warp][lane] = s;
   __syncthreads();
-  if (warp == 0 && c < 2 * d) {
+  if (warp == 0 && c < d) {
     float t = 0.f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) t += red[i][lane];
-    float* out = c < d ? dwq : dwk;
-    if (out) out[c < d ? c : c - d] = t;
+    out[c] = t;
   }
 }
 
-constexpr int kBwdCtas = 152 * 4;
+constexpr int kBwdCtas = 152 * 3;  // one wave
 // From this many lane groups of four heads on, four heads a group fill the
-// GPU (152 SMs, 2048 threads each); below, one head a group gives shorter
+// GPU (152 SMs, 512 threads each); below, one head a group gives shorter
 // chains of loads.
 inline bool many(long long tokens, int heads, int d) {
-  return tokens * ((heads + 3) / 4) * (d / 8) >= 152LL * 2048;
+  return tokens * ((heads + 3) / 4) * (d / 8) >= 152LL * 512;
+}
+
+// Items of `rows` heads, and the CTAs they fill.
+void divide(NormProblem* p, long long tokens, int rows, int d, unsigned (&ctas)[2]) {
+  const unsigned per = 256 / (d / 8);
+  for (int i = 0; i < 2; ++i) {
+    p->chunks[i] = (p->heads[i] + rows - 1) / rows;
+    p->items[i] = static_cast<unsigned>(tokens * p->chunks[i]);
+    ctas[i] = (p->items[i] + per - 1) / per;
+  }
 }
 
 template <int D, bool INTER>
 int launch_fwd_d(NormProblem p, long long tokens, cudaStream_t st) {
-  const int heads = p.heads[0] + p.heads[1];
-  const bool big = many(tokens, heads, D);
-  p.chunks = big ? (heads + 3) / 4 : heads;
-  p.items = static_cast<unsigned>(tokens * p.chunks);
-  const unsigned per = 256 / (D / 8);
-  const dim3 grid((p.items + per - 1) / per);
+  const bool big = many(tokens, p.heads[0] + p.heads[1], D);
+  unsigned ctas[2];
+  divide(&p, tokens, big ? 4 : 1, D, ctas);
+  p.ctas_q = ctas[0];
+  const dim3 grid(ctas[0] + ctas[1]);
   return big ? launch_pdl(fa2_qk_norm_rope_kernel<D, INTER, 4>, grid, dim3(256), 0, st, p)
              : launch_pdl(fa2_qk_norm_rope_kernel<D, INTER, 1>, grid, dim3(256), 0, st, p);
 }
 
 template <int D, bool INTER>
 int launch_bwd_d(NormProblem p, long long tokens, float* dwq, float* dwk, cudaStream_t st) {
-  const int heads = p.heads[0] + p.heads[1];
-  const bool big = many(tokens, heads, D);
-  p.chunks = big ? (heads + 3) / 4 : heads;
-  p.items = static_cast<unsigned>(tokens * p.chunks);
-  const unsigned per = 256 / (D / 8);
-  unsigned grid = (p.items + per - 1) / per;
-  if (grid > kBwdCtas) grid = kBwdCtas;
+  const bool big = many(tokens, p.heads[0] + p.heads[1], D);
+  unsigned ctas[2];
+  divide(&p, tokens, big ? 4 : 1, D, ctas);
+  if (ctas[0] + ctas[1] > kBwdCtas) {  // q's and k's shares of the persistent CTAs
+    const unsigned q = static_cast<unsigned>(static_cast<unsigned long long>(kBwdCtas) * p.items[0] /
+                                             (static_cast<unsigned long long>(p.items[0]) + p.items[1]));
+    ctas[0] = q < 1 ? 1 : (q > kBwdCtas - 1 ? kBwdCtas - 1 : q);
+    ctas[1] = kBwdCtas - ctas[0];
+  }
+  p.ctas_q = ctas[0];
+  const unsigned grid = ctas[0] + ctas[1];
   int e = big ? launch_pdl(fa2_qk_norm_rope_bwd_kernel<D, INTER, 4>, dim3(grid), dim3(256), 0, st, p)
               : launch_pdl(fa2_qk_norm_rope_bwd_kernel<D, INTER, 1>, dim3(grid), dim3(256), 0, st, p);
   if (e || !p.partial) return e;
-  return launch_pdl(fa2_qk_norm_dw_kernel, dim3((2 * D + 31) / 32), dim3(256), 0, st,
-                    static_cast<const float*>(p.partial), static_cast<int>(grid), D, dwq, dwk);
+  return launch_pdl(fa2_qk_norm_dw_kernel, dim3((D + 31) / 32, 2), dim3(256), 0, st, static_cast<const float*>(p.partial),
+                    static_cast<int>(ctas[0]), static_cast<int>(grid), D, dwq, dwk);
 }
 
 // Where the elements of a strided [B, heads, N, d] tensor can lie, and
@@ -433,7 +480,7 @@ int validate_norm(const NormArgs& a, Layout* t, int count, int outs, const long 
     if (a.max_positions < 1 || (!a.positions && a.N > a.max_positions)) return FA2_ERR_SHAPE;
     if (!aligned(a.rope, 16) || !aligned(a.positions, 4)) return FA2_ERR_ALIGN;
   }
-  if (!aligned(a.q_weight, a.weight_fp32 ? 4 : 2) || !aligned(a.k_weight, a.weight_fp32 ? 4 : 2)) return FA2_ERR_ALIGN;
+  if (!aligned(a.q_weight, 16) || !aligned(a.k_weight, 16)) return FA2_ERR_ALIGN;
   if (tokens == 0) return FA2_OK;
   for (int i = 0; i < count; ++i) {
     if (!t[i].p) return FA2_ERR_NULL;
@@ -534,7 +581,7 @@ int fa2_qk_norm_rope(const void* q, const void* k, const void* q_weight, const v
 }
 
 size_t fa2_qk_norm_rope_bwd_workspace_bytes(int d) {
-  return head_dim_ok(d) ? static_cast<size_t>(kBwdCtas) * 2 * d * sizeof(float) : 0;
+  return head_dim_ok(d) ? round_up(static_cast<size_t>(kBwdCtas) * d * sizeof(float)) : 0;
 }
 
 int fa2_qk_norm_rope_bwd(const void* dq_out, const void* dk_out, const void* q, const void* k, const void* q_weight,
