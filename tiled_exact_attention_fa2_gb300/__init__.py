@@ -592,6 +592,8 @@ def fa2_step_from_host(host: dict, causal: bool = True, scale: Optional[float] =
 # a few microseconds: the checks read each tensor's metadata once, and the
 # stream handle comes from torch without a Stream object.
 _raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
+_LL4, _LL12, _LL18 = _ll * 4, _ll * 12, _ll * 18
 
 
 class _on:
@@ -612,11 +614,6 @@ class _on:
     def __exit__(self, *exc):
         for g in reversed(self.guards):
             g.__exit__(*exc)
-
-
-def _away(device, stream) -> bool:
-    """Whether a call has to change the current device or stream first."""
-    return stream is not None or device.index != torch.cuda.current_device()
 
 
 def _rows(t, name: str, device):
@@ -711,7 +708,7 @@ def fa2_qk_norm_rope(q, k, q_weight=None, k_weight=None, rope=None, positions=No
     (q_out, k_out), new contiguous tensors unless given; q_out may be q.
     """
     dev = _gpu(q, "q")
-    if _away(dev, stream):
+    if stream is not None or dev.index != _current_device():
         with _on(dev, stream):
             return fa2_qk_norm_rope(q, k, q_weight, k_weight, rope, positions, eps, interleaved, q_out, k_out)
     dims, w32, strides = _norm_args(q, k, q_weight, k_weight, rope, positions, interleaved, dev)
@@ -719,7 +716,7 @@ def fa2_qk_norm_rope(q, k, q_weight=None, k_weight=None, rope=None, positions=No
     k_out, sk = _norm_out(k, k_out, "k_out")
     rc = load_library().fa2_qk_norm_rope(
         q.data_ptr(), k.data_ptr(), _dp(q_weight), _dp(k_weight), w32, _dp(rope), _dp(positions), q_out.data_ptr(),
-        k_out.data_ptr(), *dims, eps, (_ll * 12)(*strides, *sq, *sk), _raw_stream(dev.index))
+        k_out.data_ptr(), *dims, eps, _LL12(*strides, *sq, *sk), _raw_stream(dev.index))
     if rc != FA2_OK:
         raise FA2Error("fa2_qk_norm_rope", rc)
     return q_out, k_out
@@ -734,7 +731,7 @@ def fa2_qk_norm_rope_bwd(dq_out, dk_out, q, k, q_weight=None, k_weight=None, rop
     None where there is no weight.
     """
     dev = _gpu(q, "q")
-    if _away(dev, stream):
+    if stream is not None or dev.index != _current_device():
         with _on(dev, stream):
             return fa2_qk_norm_rope_bwd(dq_out, dk_out, q, k, q_weight, k_weight, rope, positions, eps, interleaved, dq, dk,
                                         workspace)
@@ -755,7 +752,7 @@ def fa2_qk_norm_rope_bwd(dq_out, dk_out, q, k, q_weight=None, k_weight=None, rop
         workspace = torch.empty(max(1, lib.fa2_qk_norm_rope_bwd_workspace_bytes(d)), dtype=torch.uint8, device=dev)
     rc = lib.fa2_qk_norm_rope_bwd(
         dq_out.data_ptr(), dk_out.data_ptr(), q.data_ptr(), k.data_ptr(), _dp(q_weight), _dp(k_weight), w32, _dp(rope),
-        _dp(positions), dq.data_ptr(), dk.data_ptr(), _dp(dwq), _dp(dwk), *dims, eps, (_ll * 18)(*grads, *strides, *sq, *sk),
+        _dp(positions), dq.data_ptr(), dk.data_ptr(), _dp(dwq), _dp(dwk), *dims, eps, _LL18(*grads, *strides, *sq, *sk),
         _dp(workspace), 0 if workspace is None else workspace.numel() * workspace.element_size(), _raw_stream(dev.index))
     if rc != FA2_OK:
         raise FA2Error("fa2_qk_norm_rope_bwd", rc)
@@ -777,7 +774,7 @@ def fa2_page_plan(cached_lens, new_lens, free_pages, block_table, page_size: int
     """One step's page plan from request lengths, on the GPU: fills the new entries of ``block_table``
     (int32 [B, width]) and returns the rest.  ``plan``: an earlier call's result to write into."""
     dev = _gpu(cached_lens, "cached_lens")
-    if _away(dev, stream):
+    if stream is not None or dev.index != _current_device():
         with _on(dev, stream):
             return fa2_page_plan(cached_lens, new_lens, free_pages, block_table, page_size, max_tokens, plan)
     B, width, row_stride = _table(block_table, dev)
@@ -795,9 +792,9 @@ def fa2_page_plan(cached_lens, new_lens, free_pages, block_table, page_size: int
         for t, name, n in zip(plan, PagePlan._fields, (B, B + 1, B + 1, max_tokens, max_tokens, 1)):
             _ints(t, "plan." + name, dev, n, torch.int64 if name == "slots" else torch.int32)
     rc = load_library().fa2_page_plan(
-        cached_lens.data_ptr(), new_lens.data_ptr(), free_pages.data_ptr() if num_free else None, block_table.data_ptr(),
-        plan.lens.data_ptr(), plan.cu_new.data_ptr(), plan.cu_total.data_ptr(), plan.slots.data_ptr() if max_tokens else None,
-        plan.positions.data_ptr() if max_tokens else None, plan.pages_needed.data_ptr(), B, num_free, width, row_stride, page_size,
+        cached_lens.data_ptr(), new_lens.data_ptr(), free_pages.data_ptr(), block_table.data_ptr(),
+        plan.lens.data_ptr(), plan.cu_new.data_ptr(), plan.cu_total.data_ptr(), plan.slots.data_ptr(),
+        plan.positions.data_ptr(), plan.pages_needed.data_ptr(), B, num_free, width, row_stride, page_size,
         max_tokens, _raw_stream(dev.index))
     if rc != FA2_OK:
         raise FA2Error("fa2_page_plan", rc)
@@ -831,7 +828,7 @@ def fa2_kv4_append(k, v, cache, slots, k_scale: float = 1.0, v_scale: float = 1.
     """Write keys and values [T, H_kv, d] bf16 (any token and head strides) to their ``slots`` (int64 [T]) of the
     4-bit cache.  ``k_out``, ``v_out``: contiguous tensors that receive the values as stored."""
     dev = _gpu(cache, "cache")
-    if _away(dev, stream):
+    if stream is not None or dev.index != _current_device():
         with _on(dev, stream):
             return fa2_kv4_append(k, v, cache, slots, k_scale, v_scale, k_out, v_out)
     pages, heads, page_size, d, page_stride = _cache_dims(cache)
@@ -848,7 +845,7 @@ def fa2_kv4_append(k, v, cache, slots, k_scale: float = 1.0, v_scale: float = 1.
     if T == 0:
         return
     rc = load_library().fa2_kv4_append(
-        k.data_ptr(), v.data_ptr(), (_ll * 4)(kt, kh, vt, vh), cache.data_ptr(), page_stride, slots.data_ptr(), _dp(k_out),
+        k.data_ptr(), v.data_ptr(), _LL4(kt, kh, vt, vh), cache.data_ptr(), page_stride, slots.data_ptr(), _dp(k_out),
         _dp(v_out), T, heads, pages, page_size, d, k_scale, v_scale, _raw_stream(dev.index))
     if rc != FA2_OK:
         raise FA2Error("fa2_kv4_append", rc)
@@ -859,7 +856,7 @@ def fa2_kv4_gather(cache, block_table, cu_seqlens, total: int, k_scale: float = 
     """The cache's keys and values as packed bf16 [total, H_kv, d] (what fa2_fwd_varlen takes as k and v with
     cu_seqlens_k = ``cu_seqlens``).  Rows outside every sequence of given k, v are left as they are."""
     dev = _gpu(cache, "cache")
-    if _away(dev, stream):
+    if stream is not None or dev.index != _current_device():
         with _on(dev, stream):
             return fa2_kv4_gather(cache, block_table, cu_seqlens, total, k_scale, v_scale, k, v)
     pages, heads, page_size, d, page_stride = _cache_dims(cache)
@@ -872,7 +869,7 @@ def fa2_kv4_gather(cache, block_table, cu_seqlens, total: int, k_scale: float = 
     k = torch.empty((total, heads, d), dtype=torch.bfloat16, device=dev) if k is None else k
     v = torch.empty((total, heads, d), dtype=torch.bfloat16, device=dev) if v is None else v
     rc = load_library().fa2_kv4_gather(
-        cache.data_ptr(), page_stride, block_table.data_ptr(), row_stride, cu_seqlens.data_ptr(), _ptr(k), _ptr(v), B, heads,
+        cache.data_ptr(), page_stride, block_table.data_ptr(), row_stride, cu_seqlens.data_ptr(), k.data_ptr(), v.data_ptr(), B, heads,
         total, pages, page_size, width, d, k_scale, v_scale, _raw_stream(dev.index))
     if rc != FA2_OK:
         raise FA2Error("fa2_kv4_gather", rc)
@@ -896,7 +893,7 @@ def fa2_kv4_attn(q, cache, block_table, lens, cu_seqlens_q=None, max_seqlen_q: O
     max_seqlen_q the maximum is read from the offsets (a device sync).
     """
     dev = _gpu(cache, "cache")
-    if _away(dev, stream):
+    if stream is not None or dev.index != _current_device():
         with _on(dev, stream):
             return fa2_kv4_attn(q, cache, block_table, lens, cu_seqlens_q, max_seqlen_q, o, lse, workspace, scale, k_scale,
                                 v_scale, causal)
@@ -914,7 +911,7 @@ def fa2_kv4_attn(q, cache, block_table, lens, cu_seqlens_q=None, max_seqlen_q: O
         if mq * B != tq:
             raise ValueError("without cu_seqlens_q every request has the same number of queries")
     if o is None:
-        o = torch.empty((tq, H, d), dtype=torch.bfloat16, device=dev)
+        o = torch.empty_like(q)
     elif o.shape != q.shape or o.dtype is not torch.bfloat16 or o.device != dev or not o.is_contiguous():
         raise ValueError("o must be contiguous bfloat16 with q's shape and device")
     if lse is None:
@@ -927,8 +924,8 @@ def fa2_kv4_attn(q, cache, block_table, lens, cu_seqlens_q=None, max_seqlen_q: O
     elif workspace.device != dev:
         raise ValueError("workspace must be on the cache's device")
     rc = lib.fa2_kv4_attn(
-        _ptr(q), cache.data_ptr(), page_stride, block_table.data_ptr(), row_stride, lens.data_ptr(), _dp(cu_seqlens_q), _ptr(o),
-        _ptr(lse), B, H, heads, tq, mq, pages, page_size, width, d, _scale(scale, d), k_scale, v_scale, 1 if causal else 0,
+        q.data_ptr(), cache.data_ptr(), page_stride, block_table.data_ptr(), row_stride, lens.data_ptr(), _dp(cu_seqlens_q),
+        o.data_ptr(), lse.data_ptr(), B, H, heads, tq, mq, pages, page_size, width, d, _scale(scale, d), k_scale, v_scale, 1 if causal else 0,
         workspace.data_ptr(), workspace.numel() * workspace.element_size(), _raw_stream(dev.index))
     if rc != FA2_OK:
         raise FA2Error("fa2_kv4_attn", rc)
