@@ -54,6 +54,7 @@ struct NormProblem {
   const int* positions;
   int heads[2], chunks[2];  // heads, and lane-group items per token, of q and k
   unsigned items[2];        // B * N * chunks
+  unsigned tokens;          // B * N
   unsigned ctas_q;          // CTAs below this one work for q
   int N, rot, max_pos, w_fp32;
   float eps;
@@ -92,38 +93,44 @@ __device__ __forceinline__ uint64_t widen2(uint32_t w) {
 }
 
 // The rotation partners of a lane's 8 columns `col` ..: which lane holds them
-// (half split; of an interleaved pair the other half of the word), and
-// whether these columns turn at all.
+// (half split; of an interleaved pair the other half of the word), whether
+// these columns turn at all, and the sign of their sine.
 struct Partner {
   int lane;
   bool turns, low;
+  uint32_t keep, flip;  // for the partners' packed words
 };
 template <bool INTER>
-__device__ __forceinline__ Partner partner_of(int rot, int col) {
+__device__ __forceinline__ Partner partner_of(int rot, int col, bool back) {
   Partner t;
   t.lane = threadIdx.x & 31;
   t.turns = col < rot;
   t.low = col < rot / 2;
   if (!INTER && t.turns) t.lane += t.low ? rot / 16 : -(rot / 16);
+  t.keep = t.turns ? 0xffffffffu : 0u;
+  // forward: the first of a pair takes minus its partner's sine, the second plus
+  t.flip = !t.turns ? 0u : INTER ? (back ? 0x80000000u : 0x00008000u) : (t.low != back ? 0x80008000u : 0u);
   return t;
 }
 
-// The partners' words (zeros where nothing turns: their factor is 0, and an
-// infinity must not meet it).
+// The partners' words, signed (zeros where nothing turns: their factor is 0,
+// and an infinity must not meet it).
 template <bool INTER>
 __device__ __forceinline__ uint32_t partner_word(const Partner& t, uint32_t w) {
   const uint32_t v = INTER ? __byte_perm(w, 0, 0x1032) : __shfl_sync(0xffffffffu, w, t.lane);
-  return t.turns ? v : 0u;
+  return (v & t.keep) ^ t.flip;
 }
 
-// Cosines and signed sines of the lane's 8 columns at a position:
-// rotated_j = x_j c_j + partner_j s_j.  `back`: turned the other way.
+// Cosines and sines of the lane's 8 columns at a position: rotated_j =
+// x_j c_j + partner_j s_j.
 template <bool INTER>
 __device__ __forceinline__ void load_turn(float (&c)[8], float (&s)[8], const Partner& t, const NormProblem& p, int pos,
-                                          int col, bool back) {
+                                          int col) {
+  if (!t.turns) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) c[i] = 1.f, s[i] = 0.f;
-  if (!t.turns) return;
+    for (int i = 0; i < 8; ++i) c[i] = 1.f, s[i] = 0.f;
+    return;
+  }
   const int half = p.rot >> 1;
   const float* row = p.rope + static_cast<long long>(pos) * p.rot;
   if (INTER) {
@@ -131,56 +138,56 @@ __device__ __forceinline__ void load_turn(float (&c)[8], float (&s)[8], const Pa
     const float4 b = __ldg(reinterpret_cast<const float4*>(row + half + (col >> 1)));
     const float cc[4] = {a.x, a.y, a.z, a.w}, ss[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      c[2 * i] = c[2 * i + 1] = cc[i];
-      s[2 * i] = back ? ss[i] : -ss[i];
-      s[2 * i + 1] = back ? -ss[i] : ss[i];
-    }
+    for (int i = 0; i < 4; ++i) c[2 * i] = c[2 * i + 1] = cc[i], s[2 * i] = s[2 * i + 1] = ss[i];
   } else {
     row += t.low ? col : col - half;
-    const float sign = t.low != back ? -1.f : 1.f;
 #pragma unroll
     for (int i = 0; i < 8; i += 4) {
       const float4 a = __ldg(reinterpret_cast<const float4*>(row + i));
       const float4 b = __ldg(reinterpret_cast<const float4*>(row + half + i));
       c[i] = a.x, c[i + 1] = a.y, c[i + 2] = a.z, c[i + 3] = a.w;
-      s[i] = sign * b.x, s[i + 1] = sign * b.y, s[i + 2] = sign * b.z, s[i + 3] = sign * b.w;
+      s[i] = b.x, s[i + 1] = b.y, s[i + 2] = b.z, s[i + 3] = b.w;
     }
   }
 }
 
-// A lane group's item: `count` heads from h0 on of token (b, n); none for an
-// item past the end or at a bad position (it does its arithmetic on nothing:
-// shuffles are warp-wide).
+// A lane group's item: `count` heads from h0 on of token (b, n), number tok of
+// B * N; none for an item past the end or at a bad position (it does its
+// arithmetic on nothing: shuffles are warp-wide).
 struct Item {
-  long long b;
-  int n, h0, pos, count;
+  unsigned tok, chunk;
+  int b, n, h0, pos, count;
 };
 
 template <int ROWS>
-__device__ __forceinline__ Item find_item(const NormProblem& p, int which, unsigned id) {
-  Item it;
-  const bool live = id < p.items[which];
-  const unsigned chunks = p.chunks[which];
-  const unsigned tok = live ? id / chunks : 0;
-  it.h0 = live ? static_cast<int>(id - tok * chunks) * ROWS : 0;
+__device__ __forceinline__ void place(Item& it, const NormProblem& p, int which) {
+  const bool live = it.tok < p.tokens;
+  it.h0 = static_cast<int>(it.chunk) * ROWS;
   it.count = live ? min(ROWS, p.heads[which] - it.h0) : 0;
-  it.b = tok / static_cast<unsigned>(p.N);
-  it.n = static_cast<int>(tok - static_cast<unsigned>(it.b) * p.N);
   it.pos = it.n;
   if (p.rot > 0) {
-    if (p.positions && live) it.pos = __ldg(p.positions + tok);
+    if (p.positions && live) it.pos = __ldg(p.positions + it.tok);
     if (live && (it.pos < 0 || it.pos >= p.max_pos)) {
       atomicCAS(&g_norm_status, kDevOk, kDevBadIndex);
       it.count = 0;
     }
     if (it.count == 0) it.pos = 0;
   }
+}
+
+template <int ROWS>
+__device__ __forceinline__ Item find_item(const NormProblem& p, int which, unsigned id) {
+  Item it;
+  it.tok = id / static_cast<unsigned>(p.chunks[which]);
+  it.chunk = id - it.tok * p.chunks[which];
+  it.b = static_cast<int>(it.tok / static_cast<unsigned>(p.N));
+  it.n = static_cast<int>(it.tok - static_cast<unsigned>(it.b) * p.N);
+  place<ROWS>(it, p, which);
   return it;
 }
 
 __device__ __forceinline__ char* row_at(const View& v, const Item& it, int col) {
-  return v.p + 2 * (it.b * v.sb + it.n * v.sn + it.h0 * v.sh + col);
+  return it.count > 0 ? v.p + 2 * (it.b * v.sb + it.n * v.sn + it.h0 * v.sh + col) : v.p;
 }
 
 template <int D, bool INTER, int ROWS>
@@ -200,11 +207,11 @@ __global__ void __launch_bounds__(256) fa2_qk_norm_rope_kernel(const NormProblem
     raw[i] = make_uint4(0, 0, 0, 0);
     if (i < it.count) raw[i] = *reinterpret_cast<const uint4*>(src + i * sx);
   }
-  const Partner partner = partner_of<INTER>(p.rot, col);
+  const Partner partner = partner_of<INTER>(p.rot, col, false);
   uint64_t wc[4], ws[4];  // gain times cosine; the partner's gain times sine
   {
     float c[8], s[8];
-    load_turn<INTER>(c, s, partner, p, it.pos, col, false);
+    load_turn<INTER>(c, s, partner, p, it.pos, col);
     float w[8], pw[8];
     gains(w, p.w[which], p.w_fp32, col);
     if (!INTER) gains(pw, p.w[which], p.w_fp32, col + (partner.lane - static_cast<int>(threadIdx.x & 31)) * 8);
@@ -246,9 +253,10 @@ __global__ void __launch_bounds__(256) fa2_qk_norm_rope_kernel(const NormProblem
 // rows; the CTA's sums are joined in shared memory and written to its own
 // slot, which the dw kernel adds up in a fixed order (the result does not
 // depend on the order CTAs run in).
+constexpr int kBwdThreads = 128, kBwdPerSm = 5;
 template <int D, bool INTER, int ROWS>
-__global__ void __launch_bounds__(256, 3) fa2_qk_norm_rope_bwd_kernel(const NormProblem p) {
-  constexpr int kLanes = D / 8, kGroups = 256 / kLanes;
+__global__ void __launch_bounds__(kBwdThreads, kBwdPerSm) fa2_qk_norm_rope_bwd_kernel(const NormProblem p) {
+  constexpr int kLanes = D / 8, kGroups = kBwdThreads / kLanes;
   __shared__ float red[kGroups][D];
   griddep_wait();
   griddep_launch_dependents();
@@ -256,7 +264,7 @@ __global__ void __launch_bounds__(256, 3) fa2_qk_norm_rope_bwd_kernel(const Norm
   const int which = blockIdx.x >= p.ctas_q;
   const unsigned cta = which ? blockIdx.x - p.ctas_q : blockIdx.x;
   const unsigned step = (which ? gridDim.x - p.ctas_q : p.ctas_q) * kGroups;
-  const Partner partner = partner_of<INTER>(p.rot, col);
+  const Partner partner = partner_of<INTER>(p.rot, col, true);
   const long long sx = 2 * p.x[which].sh, sg = 2 * p.g[which].sh, sy = 2 * p.y[which].sh;
   uint64_t w[4], dw[4];
   {
@@ -267,8 +275,23 @@ __global__ void __launch_bounds__(256, 3) fa2_qk_norm_rope_bwd_kernel(const Norm
   }
   // (the loop bound is the same for every lane of a warp: shuffles inside)
   const unsigned rounds = (p.items[which] + step - 1) / step;
+  Item it = find_item<ROWS>(p, which, cta * kGroups + group);
+  // a round is `step` items further: so many tokens and chunks, sequences and tokens
+  const unsigned chunks = p.chunks[which], d_tok = step / chunks, d_chunk = step - d_tok * chunks;
+  const int d_b = static_cast<int>(d_tok / static_cast<unsigned>(p.N)), d_n = static_cast<int>(d_tok) - d_b * p.N;
   for (unsigned k = 0; k < rounds; ++k) {
-    const Item it = find_item<ROWS>(p, which, k * step + cta * kGroups + group);
+    if (k > 0) {
+      const unsigned c = it.chunk + d_chunk, carry = c >= chunks;
+      it.chunk = carry ? c - chunks : c;
+      it.tok += d_tok + carry;
+      it.b += d_b;
+      it.n += d_n + static_cast<int>(carry);
+      if (it.n >= p.N) {
+        it.n -= p.N;
+        ++it.b;
+      }
+      place<ROWS>(it, p, which);
+    }
     const char* px = row_at(p.x[which], it, col);
     const char* pg = row_at(p.g[which], it, col);
     char* py = row_at(p.y[which], it, col);
@@ -284,7 +307,7 @@ __global__ void __launch_bounds__(256, 3) fa2_qk_norm_rope_bwd_kernel(const Norm
     uint64_t c[4], s[4];
     {
       float cf[8], sf[8];
-      load_turn<INTER>(cf, sf, partner, p, it.pos, col, true);
+      load_turn<INTER>(cf, sf, partner, p, it.pos, col);
 #pragma unroll
       for (int j = 0; j < 4; ++j) c[j] = f2_pack(cf[2 * j], cf[2 * j + 1]), s[j] = f2_pack(sf[2 * j], sf[2 * j + 1]);
     }
@@ -323,7 +346,7 @@ __global__ void __launch_bounds__(256, 3) fa2_qk_norm_rope_bwd_kernel(const Norm
     red[group][col + 2 * j + 1] = f.y;
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < D; i += 256) {
+  for (int i = threadIdx.x; i < D; i += kBwdThreads) {
     float t = 0.f;
 #pragma unroll 8
     for (int k = 0; k < kGroups; ++k) t += red[k][i];
@@ -332,11 +355,12 @@ __global__ void __launch_bounds__(256, 3) fa2_qk_norm_rope_bwd_kernel(const Norm
 }
 
 // dw of q (blockIdx.y = 0) and k: the sums of their CTAs' slots, 32 columns
-// per block, 8 warps that each add every eighth slot, then the 8 sums in
-// order.
-__global__ void __launch_bounds__(256) fa2_qk_norm_dw_kernel(const float* __restrict__ partial, int slots_q, int slots, int d,
-                                                             float* dwq, float* dwk) {
-  __shared__ float red[8][32];
+// per block; each of the 32 warps adds every 32nd slot (so the loads of all
+// of a warp's slots are in flight at once), then warp w adds column w's 32
+// sums by a butterfly, whose order is fixed.
+__global__ void __launch_bounds__(1024) fa2_qk_norm_dw_kernel(const float* __restrict__ partial, int slots_q, int slots, int d,
+                                                              float* dwq, float* dwk) {
+  __shared__ float red[32][33];
   griddep_wait();
   griddep_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -347,18 +371,14 @@ __global__ void __launch_bounds__(256) fa2_qk_norm_dw_kernel(const float* __rest
   float s = 0.f;
   if (c < d)
 #pragma unroll 8
-    for (int i = first + warp; i < last; i += 8) s += partial[static_cast<size_t>(i) * d + c];
+    for (int i = first + warp; i < last; i += 32) s += partial[static_cast<size_t>(i) * d + c];
   red[warp][lane] = s;
   __syncthreads();
-  if (warp == 0 && c < d) {
-    float t = 0.f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) t += red[i][lane];
-    out[c] = t;
-  }
+  s = sum_lanes<32>(red[lane][warp]);
+  if (lane == 0 && blockIdx.x * 32 + warp < d) out[blockIdx.x * 32 + warp] = s;
 }
 
-constexpr int kBwdCtas = 152 * 3;  // one wave
+constexpr int kBwdCtas = 152 * kBwdPerSm;  // one wave
 // From this many lane groups of four heads on, four heads a group fill the
 // GPU (152 SMs, 512 threads each); below, one head a group gives shorter
 // chains of loads.
@@ -367,8 +387,9 @@ inline bool many(long long tokens, int heads, int d) {
 }
 
 // Items of `rows` heads, and the CTAs they fill.
-void divide(NormProblem* p, long long tokens, int rows, int d, unsigned (&ctas)[2]) {
-  const unsigned per = 256 / (d / 8);
+void divide(NormProblem* p, long long tokens, int rows, int d, int threads, unsigned (&ctas)[2]) {
+  const unsigned per = threads / (d / 8);
+  p->tokens = static_cast<unsigned>(tokens);
   for (int i = 0; i < 2; ++i) {
     p->chunks[i] = (p->heads[i] + rows - 1) / rows;
     p->items[i] = static_cast<unsigned>(tokens * p->chunks[i]);
@@ -380,7 +401,7 @@ template <int D, bool INTER>
 int launch_fwd_d(NormProblem p, long long tokens, cudaStream_t st) {
   const bool big = many(tokens, p.heads[0] + p.heads[1], D);
   unsigned ctas[2];
-  divide(&p, tokens, big ? 4 : 1, D, ctas);
+  divide(&p, tokens, big ? 4 : 1, D, 256, ctas);
   p.ctas_q = ctas[0];
   const dim3 grid(ctas[0] + ctas[1]);
   return big ? launch_pdl(fa2_qk_norm_rope_kernel<D, INTER, 4>, grid, dim3(256), 0, st, p)
@@ -391,7 +412,7 @@ template <int D, bool INTER>
 int launch_bwd_d(NormProblem p, long long tokens, float* dwq, float* dwk, cudaStream_t st) {
   const bool big = many(tokens, p.heads[0] + p.heads[1], D);
   unsigned ctas[2];
-  divide(&p, tokens, big ? 4 : 1, D, ctas);
+  divide(&p, tokens, big ? 4 : 1, D, kBwdThreads, ctas);
   if (ctas[0] + ctas[1] > kBwdCtas) {  // q's and k's shares of the persistent CTAs
     const unsigned q = static_cast<unsigned>(static_cast<unsigned long long>(kBwdCtas) * p.items[0] /
                                              (static_cast<unsigned long long>(p.items[0]) + p.items[1]));
@@ -400,10 +421,10 @@ int launch_bwd_d(NormProblem p, long long tokens, float* dwq, float* dwk, cudaSt
   }
   p.ctas_q = ctas[0];
   const unsigned grid = ctas[0] + ctas[1];
-  int e = big ? launch_pdl(fa2_qk_norm_rope_bwd_kernel<D, INTER, 4>, dim3(grid), dim3(256), 0, st, p)
-              : launch_pdl(fa2_qk_norm_rope_bwd_kernel<D, INTER, 1>, dim3(grid), dim3(256), 0, st, p);
+  int e = big ? launch_pdl(fa2_qk_norm_rope_bwd_kernel<D, INTER, 4>, dim3(grid), dim3(kBwdThreads), 0, st, p)
+              : launch_pdl(fa2_qk_norm_rope_bwd_kernel<D, INTER, 1>, dim3(grid), dim3(kBwdThreads), 0, st, p);
   if (e || !p.partial) return e;
-  return launch_pdl(fa2_qk_norm_dw_kernel, dim3((D + 31) / 32, 2), dim3(256), 0, st, static_cast<const float*>(p.partial),
+  return launch_pdl(fa2_qk_norm_dw_kernel, dim3((D + 31) / 32, 2), dim3(1024), 0, st, static_cast<const float*>(p.partial),
                     static_cast<int>(ctas[0]), static_cast<int>(grid), D, dwq, dwk);
 }
 
