@@ -279,6 +279,25 @@ def test_append_stores_the_nearest_values(d, P, Hkv, T, factors):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("T,Hkv,d", [(5001, 8, 128), (9000, 20, 64), (70001, 1, 32)])
+def test_append_many_tokens_and_back(T, Hkv, d):
+    """Many tokens (two to a thread), heads beyond a CTA's 256 threads; what is stored is read back."""
+    g = torch.Generator(device="cuda").manual_seed(T)
+    k, v = (torch.randn(T, Hkv, d, generator=g, device="cuda").to(torch.bfloat16) for _ in range(2))
+    pages = -(-T // 64) + 1
+    cache = fa2.fa2_kv4_cache(pages, Hkv, 64, d)
+    slots = torch.arange(T, device="cuda") + 64
+    ko, vo = torch.empty_like(k), torch.empty_like(v)
+    fa2.fa2_kv4_append(k, v, cache, slots, k_out=ko, v_out=vo)
+    some = torch.randint(0, T, (300,), generator=g, device="cuda")
+    some[0] = T - 1
+    for got, x in ((ko, k), (vo, v)):
+        assert np.array_equal(got[some].double().cpu().numpy(), ref.quantize(x[some].double().cpu().numpy(), 1.0)[2])
+    kk, vv = fa2.fa2_kv4_gather(cache, i32(np.arange(1, pages)[None]), i32([0, T]), T)
+    assert torch.equal(kk, ko) and torch.equal(vv, vo)
+
+
+@pytest.mark.gpu
 def test_append_padding_and_bad_slots():
     fa2.fa2_device_status(reset=True)
     cache = fa2.fa2_kv4_cache(2, 2, 32, 64)

@@ -76,7 +76,7 @@ __device__ __forceinline__ void quantize(uint4& x, float f, uint32_t& scale, uin
 // and stores side by side, two of each in flight.  (One thread per group of
 // 16 with IEEE divisions was bound by instructions: 36 us against 23 of
 // memory for 16385 tokens of 8 heads of 128 columns.)
-template <int D>
+template <int D, int TOKENS>
 __global__ void __launch_bounds__(256) fa2_kv4_append_kernel(const AppendProblem p) {
   using L = Kv4<D>;
   griddep_wait();
@@ -85,48 +85,57 @@ __global__ void __launch_bounds__(256) fa2_kv4_append_kernel(const AppendProblem
   // row_threads is even
   const int local = threadIdx.x / p.row_threads;
   const int r = threadIdx.x - local * p.row_threads + blockIdx.y * 256;
-  const int t = blockIdx.x * p.block_tokens + local;
-  const bool live = t < p.tokens && r < p.row_threads && local < p.block_tokens;
+  const bool fits = r < p.row_threads && local < p.block_tokens;
   const int h = r / (D / 8), c8 = r % (D / 8), grp = c8 >> 1;
-  uint4 k = make_uint4(0, 0, 0, 0), v = k;
-  long long slot = -1;
-  if (live) {
-    slot = __ldg(p.slots + t);
-    k = __ldg(reinterpret_cast<const uint4*>(p.k + t * p.token_stride[0] + h * p.head_stride[0] + c8 * 8));
-    v = __ldg(reinterpret_cast<const uint4*>(p.v + t * p.token_stride[1] + h * p.head_stride[1] + c8 * 8));
-  }
-  uint32_t k_scale, k_code, v_scale, v_code;
-  quantize(k, p.k_scale, k_scale, k_code, p.k_out != nullptr);
-  quantize(v, p.v_scale, v_scale, v_code, p.v_out != nullptr);
-  if (!live) return;
-  const long long out = (static_cast<long long>(t) * p.cache.heads + h) * D + c8 * 8;
-  if (p.k_out) *reinterpret_cast<uint4*>(p.k_out + out) = k;
-  if (p.v_out) *reinterpret_cast<uint4*>(p.v_out + out) = v;
-  if (slot < 0) return;  // a padding token
-  if (slot >= static_cast<long long>(p.cache.num_pages) << p.cache.shift) {
-    atomicCAS(&g_cache_status, kDevOk, kDevBadIndex);
-    return;
-  }
-  const int off = static_cast<int>(slot) & ((1 << p.cache.shift) - 1), key = off & 15;
-  char* tile = p.cache.base + (slot >> p.cache.shift) * p.cache.page_stride +
-               ((static_cast<long long>(h) << (p.cache.shift - 4)) + (off >> 4)) * L::kTileBytes;
-  *reinterpret_cast<uint32_t*>(tile + key * (D / 2) + c8 * 4) = k_code;
-  constexpr int kPiece = D / 16;  // bytes of a lane's V columns
-  if constexpr (kPiece >= 4) {
-    constexpr int kPer = kPiece / 4;  // threads of a piece
-    *reinterpret_cast<uint32_t*>(tile + L::v_piece_at(key, c8 / kPer) + c8 % kPer * 4) = v_code;
-  } else if constexpr (kPiece == 2) {
+  uint4 k[TOKENS], v[TOKENS];
+  long long slot[TOKENS];
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
-      *reinterpret_cast<uint16_t*>(tile + L::v_piece_at(key, c8 * 2 + j)) = static_cast<uint16_t>(v_code >> (16 * j));
-  } else {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) tile[L::v_piece_at(key, c8 * 4 + j)] = static_cast<char>(v_code >> (8 * j));
+  for (int i = 0; i < TOKENS; ++i) {
+    const int t = (blockIdx.x * TOKENS + i) * p.block_tokens + local;
+    k[i] = v[i] = make_uint4(0, 0, 0, 0);
+    slot[i] = -1;
+    if (fits && t < p.tokens) {
+      slot[i] = __ldg(p.slots + t);
+      k[i] = __ldg(reinterpret_cast<const uint4*>(p.k + t * p.token_stride[0] + h * p.head_stride[0] + c8 * 8));
+      v[i] = __ldg(reinterpret_cast<const uint4*>(p.v + t * p.token_stride[1] + h * p.head_stride[1] + c8 * 8));
+    }
   }
-  if (c8 & 1)
-    tile[L::v_scale_at(key, grp)] = static_cast<char>(v_scale);
-  else
-    tile[L::k_scale_at(key, grp)] = static_cast<char>(k_scale);
+#pragma unroll
+  for (int i = 0; i < TOKENS; ++i) {
+    const int t = (blockIdx.x * TOKENS + i) * p.block_tokens + local;
+    uint32_t k_scale, k_code, v_scale, v_code;
+    quantize(k[i], p.k_scale, k_scale, k_code, p.k_out != nullptr);
+    quantize(v[i], p.v_scale, v_scale, v_code, p.v_out != nullptr);
+    if (!fits || t >= p.tokens) continue;
+    const long long out = (static_cast<long long>(t) * p.cache.heads + h) * D + c8 * 8;
+    if (p.k_out) *reinterpret_cast<uint4*>(p.k_out + out) = k[i];
+    if (p.v_out) *reinterpret_cast<uint4*>(p.v_out + out) = v[i];
+    if (slot[i] < 0) continue;  // a padding token
+    if (slot[i] >= static_cast<long long>(p.cache.num_pages) << p.cache.shift) {
+      atomicCAS(&g_cache_status, kDevOk, kDevBadIndex);
+      continue;
+    }
+    const int off = static_cast<int>(slot[i]) & ((1 << p.cache.shift) - 1), key = off & 15;
+    char* tile = p.cache.base + (slot[i] >> p.cache.shift) * p.cache.page_stride +
+                 ((static_cast<long long>(h) << (p.cache.shift - 4)) + (off >> 4)) * L::kTileBytes;
+    *reinterpret_cast<uint32_t*>(tile + key * (D / 2) + c8 * 4) = k_code;
+    constexpr int kPiece = D / 16;  // bytes of a lane's V columns
+    if constexpr (kPiece >= 4) {
+      constexpr int kPer = kPiece / 4;  // threads of a piece
+      *reinterpret_cast<uint32_t*>(tile + L::v_piece_at(key, c8 / kPer) + c8 % kPer * 4) = v_code;
+    } else if constexpr (kPiece == 2) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        *reinterpret_cast<uint16_t*>(tile + L::v_piece_at(key, c8 * 2 + j)) = static_cast<uint16_t>(v_code >> (16 * j));
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) tile[L::v_piece_at(key, c8 * 4 + j)] = static_cast<char>(v_code >> (8 * j));
+    }
+    if (c8 & 1)
+      tile[L::v_scale_at(key, grp)] = static_cast<char>(v_scale);
+    else
+      tile[L::k_scale_at(key, grp)] = static_cast<char>(k_scale);
+  }
 }
 
 struct GatherProblem {
@@ -257,8 +266,11 @@ int launch_append_d(AppendProblem p, cudaStream_t st) {
   p.row_threads = p.cache.heads * (D / 8);
   p.block_tokens = p.row_threads >= 256 ? 1 : 256 / p.row_threads;
   const unsigned parts = (p.row_threads + 255) / 256;
-  return launch_pdl(fa2_kv4_append_kernel<D>, dim3(static_cast<unsigned>((p.tokens + p.block_tokens - 1) / p.block_tokens), parts),
-                    dim3(256), 0, st, p);
+  // Many tokens: two to a thread, for twice the loads in flight.
+  const long long ctas = (p.tokens + p.block_tokens - 1LL) / p.block_tokens;
+  if (ctas * parts >= 152 * 16)
+    return launch_pdl(fa2_kv4_append_kernel<D, 2>, dim3(static_cast<unsigned>((ctas + 1) / 2), parts), dim3(256), 0, st, p);
+  return launch_pdl(fa2_kv4_append_kernel<D, 1>, dim3(static_cast<unsigned>(ctas), parts), dim3(256), 0, st, p);
 }
 template <int D>
 int launch_gather_d(GatherProblem p, cudaStream_t st) {
