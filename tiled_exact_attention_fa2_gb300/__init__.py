@@ -616,11 +616,12 @@ class _on:
             g.__exit__(*exc)
 
 
-def _rows(t, name: str, device):
+# (devices are compared by index: -1 is the CPU)
+def _rows(t, name: str, dev: int):
     """((B, heads, N, d), (batch, head, token) strides) of a bf16 [B, heads, N, d] tensor, or of a packed [total, heads,
     d] one as B = 1."""
-    if t.dtype is not torch.bfloat16 or t.device != device:
-        raise ValueError(f"{name} must be bfloat16 on {device}")
+    if t.dtype is not torch.bfloat16 or t.get_device() != dev:
+        raise ValueError(f"{name} must be bfloat16 on cuda:{dev}")
     shape, stride = t.shape, t.stride()
     if len(shape) == 4:
         B, h, N, d = shape
@@ -634,25 +635,26 @@ def _rows(t, name: str, device):
     return (B, h, N, d), (sb, sh, sn)
 
 
-def _ints(t, name: str, device, count: int, dtype=torch.int32):
-    if t.dtype is not dtype or t.device != device or t.dim() != 1 or t.shape[0] != count or (count > 1 and t.stride(0) != 1):
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of {count} entries on {device}")
+def _ints(t, name: str, dev: int, count: int, dtype=torch.int32):
+    if t.dtype is not dtype or t.get_device() != dev or t.shape != (count,) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of {count} entries on cuda:{dev}")
 
 
-def _table(t, device):
+def _table(t, dev: int):
     """(rows, width, row stride) of an int32 block table."""
-    if t.dtype is not torch.int32 or t.device != device or t.dim() != 2:
-        raise ValueError(f"block_table must be an int32 [B, width] tensor on {device}")
+    if t.dtype is not torch.int32 or t.get_device() != dev or t.dim() != 2:
+        raise ValueError(f"block_table must be an int32 [B, width] tensor on cuda:{dev}")
     (rows, width), (sr, sc) = t.shape, t.stride()
     if width > 1 and sc != 1:
         raise ValueError("block_table's rows must be contiguous")
     return rows, width, sr
 
 
-def _gpu(t, name: str):
-    if not t.is_cuda:
+def _gpu(t, name: str) -> int:
+    dev = t.get_device()
+    if dev < 0:
         raise ValueError(f"{name} must be a CUDA tensor")
-    return t.device
+    return dev
 
 
 def _norm_args(q, k, q_weight, k_weight, rope, positions, interleaved, dev):
@@ -668,29 +670,31 @@ def _norm_args(q, k, q_weight, k_weight, rope, positions, interleaved, dev):
                 w32 = 1
             elif w.dtype is not torch.bfloat16:
                 raise ValueError("a weight must be bfloat16 or float32")
-            if w.shape != (d,) or w.device != dev or not w.is_contiguous():
+            if w.shape != (d,) or w.get_device() != dev or not w.is_contiguous():
                 raise ValueError("a weight must be a contiguous tensor of d values on q's device")
     if q_weight is not None and k_weight is not None and q_weight.dtype is not k_weight.dtype:
         raise ValueError("q_weight and k_weight must have the same type")
     rot = max_pos = 0
     if rope is not None:
-        if rope.dtype is not torch.float32 or rope.dim() != 2 or rope.device != dev or not rope.is_contiguous():
+        if rope.dtype is not torch.float32 or rope.dim() != 2 or rope.get_device() != dev or not rope.is_contiguous():
             raise ValueError("rope must be a contiguous float32 [max_positions, rot_dim] tensor on q's device")
         max_pos, rot = rope.shape
     if positions is not None:
-        if (positions.dtype is not torch.int32 or positions.device != dev or not positions.is_contiguous()
+        if (positions.dtype is not torch.int32 or positions.get_device() != dev or not positions.is_contiguous()
                 or positions.shape != ((N,) if q.dim() == 3 else (B, N))):
             raise ValueError("positions must be a contiguous int32 tensor, one per token, on q's device")
     return (B, H, Hkv, N, d, rot, 1 if interleaved else 0, max_pos), w32, sq + sk
 
 
-def _norm_out(like, out, name: str):
+def _norm_out(like, out, name: str, dev: int):
     """(`out` checked against `like`, or a new contiguous tensor; its strides)."""
     if out is None:
         out = torch.empty(like.shape, dtype=torch.bfloat16, device=like.device)
-    elif out.shape != like.shape:
+        stride = out.stride()
+        return out, (stride[:3] if len(stride) == 4 else (0, stride[1], stride[0]))
+    if out.shape != like.shape:
         raise ValueError(f"{name} must have its input's shape")
-    return out, _rows(out, name, like.device)[1]
+    return out, _rows(out, name, dev)[1]
 
 
 def _dp(t):
@@ -708,15 +712,15 @@ def fa2_qk_norm_rope(q, k, q_weight=None, k_weight=None, rope=None, positions=No
     (q_out, k_out), new contiguous tensors unless given; q_out may be q.
     """
     dev = _gpu(q, "q")
-    if stream is not None or dev.index != _current_device():
+    if stream is not None or dev != _current_device():
         with _on(dev, stream):
             return fa2_qk_norm_rope(q, k, q_weight, k_weight, rope, positions, eps, interleaved, q_out, k_out)
     dims, w32, strides = _norm_args(q, k, q_weight, k_weight, rope, positions, interleaved, dev)
-    q_out, sq = _norm_out(q, q_out, "q_out")
-    k_out, sk = _norm_out(k, k_out, "k_out")
+    q_out, sq = _norm_out(q, q_out, "q_out", dev)
+    k_out, sk = _norm_out(k, k_out, "k_out", dev)
     rc = load_library().fa2_qk_norm_rope(
         q.data_ptr(), k.data_ptr(), _dp(q_weight), _dp(k_weight), w32, _dp(rope), _dp(positions), q_out.data_ptr(),
-        k_out.data_ptr(), *dims, eps, _LL12(*strides, *sq, *sk), _raw_stream(dev.index))
+        k_out.data_ptr(), *dims, eps, _LL12(*strides, *sq, *sk), _raw_stream(dev))
     if rc != FA2_OK:
         raise FA2Error("fa2_qk_norm_rope", rc)
     return q_out, k_out
@@ -731,7 +735,7 @@ def fa2_qk_norm_rope_bwd(dq_out, dk_out, q, k, q_weight=None, k_weight=None, rop
     None where there is no weight.
     """
     dev = _gpu(q, "q")
-    if stream is not None or dev.index != _current_device():
+    if stream is not None or dev != _current_device():
         with _on(dev, stream):
             return fa2_qk_norm_rope_bwd(dq_out, dk_out, q, k, q_weight, k_weight, rope, positions, eps, interleaved, dq, dk,
                                         workspace)
@@ -739,21 +743,21 @@ def fa2_qk_norm_rope_bwd(dq_out, dk_out, q, k, q_weight=None, k_weight=None, rop
     if dq_out.shape != q.shape or dk_out.shape != k.shape:
         raise ValueError("dq_out and dk_out must have q's and k's shapes")
     grads = _rows(dq_out, "dq_out", dev)[1] + _rows(dk_out, "dk_out", dev)[1]
-    dq, sq = _norm_out(q, dq, "dq")
-    dk, sk = _norm_out(k, dk, "dk")
+    dq, sq = _norm_out(q, dq, "dq", dev)
+    dk, sk = _norm_out(k, dk, "dk", dev)
     d = dims[4]
     lib = load_library()
-    dwq = None if q_weight is None else torch.empty(d, dtype=torch.float32, device=dev)
-    dwk = None if k_weight is None else torch.empty(d, dtype=torch.float32, device=dev)
+    dwq = None if q_weight is None else torch.empty(d, dtype=torch.float32, device=q.device)
+    dwk = None if k_weight is None else torch.empty(d, dtype=torch.float32, device=q.device)
     if workspace is not None:
-        if workspace.device != dev:
+        if workspace.get_device() != dev:
             raise ValueError("workspace must be on q's device")
     elif dwq is not None or dwk is not None:
-        workspace = torch.empty(max(1, lib.fa2_qk_norm_rope_bwd_workspace_bytes(d)), dtype=torch.uint8, device=dev)
+        workspace = torch.empty(max(1, lib.fa2_qk_norm_rope_bwd_workspace_bytes(d)), dtype=torch.uint8, device=q.device)
     rc = lib.fa2_qk_norm_rope_bwd(
         dq_out.data_ptr(), dk_out.data_ptr(), q.data_ptr(), k.data_ptr(), _dp(q_weight), _dp(k_weight), w32, _dp(rope),
         _dp(positions), dq.data_ptr(), dk.data_ptr(), _dp(dwq), _dp(dwk), *dims, eps, _LL18(*grads, *strides, *sq, *sk),
-        _dp(workspace), 0 if workspace is None else workspace.numel() * workspace.element_size(), _raw_stream(dev.index))
+        _dp(workspace), 0 if workspace is None else workspace.numel() * workspace.element_size(), _raw_stream(dev))
     if rc != FA2_OK:
         raise FA2Error("fa2_qk_norm_rope_bwd", rc)
     return dq, dk, dwq, dwk
@@ -774,7 +778,7 @@ def fa2_page_plan(cached_lens, new_lens, free_pages, block_table, page_size: int
     """One step's page plan from request lengths, on the GPU: fills the new entries of ``block_table``
     (int32 [B, width]) and returns the rest.  ``plan``: an earlier call's result to write into."""
     dev = _gpu(cached_lens, "cached_lens")
-    if stream is not None or dev.index != _current_device():
+    if stream is not None or dev != _current_device():
         with _on(dev, stream):
             return fa2_page_plan(cached_lens, new_lens, free_pages, block_table, page_size, max_tokens, plan)
     B, width, row_stride = _table(block_table, dev)
@@ -786,8 +790,9 @@ def fa2_page_plan(cached_lens, new_lens, free_pages, block_table, page_size: int
         raise ValueError("max_tokens must be at least 0")
     if plan is None:
         lens, cu_new, cu_total, positions, needed = torch.empty(
-            3 * B + 3 + max_tokens, dtype=torch.int32, device=dev).split_with_sizes((B, B + 1, B + 1, max_tokens, 1))
-        plan = PagePlan(lens, cu_new, cu_total, torch.empty(max_tokens, dtype=torch.int64, device=dev), positions, needed)
+            3 * B + 3 + max_tokens, dtype=torch.int32, device=cached_lens.device).split_with_sizes((B, B + 1, B + 1, max_tokens, 1))
+        plan = PagePlan(lens, cu_new, cu_total, torch.empty(max_tokens, dtype=torch.int64, device=cached_lens.device),
+                        positions, needed)
     else:
         for t, name, n in zip(plan, PagePlan._fields, (B, B + 1, B + 1, max_tokens, max_tokens, 1)):
             _ints(t, "plan." + name, dev, n, torch.int64 if name == "slots" else torch.int32)
@@ -795,7 +800,7 @@ def fa2_page_plan(cached_lens, new_lens, free_pages, block_table, page_size: int
         cached_lens.data_ptr(), new_lens.data_ptr(), free_pages.data_ptr(), block_table.data_ptr(),
         plan.lens.data_ptr(), plan.cu_new.data_ptr(), plan.cu_total.data_ptr(), plan.slots.data_ptr(),
         plan.positions.data_ptr(), plan.pages_needed.data_ptr(), B, num_free, width, row_stride, page_size,
-        max_tokens, _raw_stream(dev.index))
+        max_tokens, _raw_stream(dev))
     if rc != FA2_OK:
         raise FA2Error("fa2_page_plan", rc)
     return plan
@@ -828,25 +833,27 @@ def fa2_kv4_append(k, v, cache, slots, k_scale: float = 1.0, v_scale: float = 1.
     """Write keys and values [T, H_kv, d] bf16 (any token and head strides) to their ``slots`` (int64 [T]) of the
     4-bit cache.  ``k_out``, ``v_out``: contiguous tensors that receive the values as stored."""
     dev = _gpu(cache, "cache")
-    if stream is not None or dev.index != _current_device():
+    if stream is not None or dev != _current_device():
         with _on(dev, stream):
             return fa2_kv4_append(k, v, cache, slots, k_scale, v_scale, k_out, v_out)
     pages, heads, page_size, d, page_stride = _cache_dims(cache)
     T = slots.numel()
     _ints(slots, "slots", dev, T, torch.int64)
     want = (T, heads, d)
+    if k.dim() != 3 or v.dim() != 3:
+        raise ValueError("k and v must be [tokens, H_kv, d]")
     (kt, kh, kd), (vt, vh, vd) = k.stride(), v.stride()
-    if (k.dtype is not torch.bfloat16 or v.dtype is not torch.bfloat16 or k.device != dev or v.device != dev
+    if (k.dtype is not torch.bfloat16 or v.dtype is not torch.bfloat16 or k.get_device() != dev or v.get_device() != dev
             or k.shape != want or v.shape != want or kd != 1 or vd != 1):
         raise ValueError("k and v must be bfloat16 [tokens, H_kv, d] on the cache's device, the last dimension contiguous")
     for t in (k_out, v_out):
-        if t is not None and (t.dtype is not torch.bfloat16 or t.device != dev or t.shape != want or not t.is_contiguous()):
+        if t is not None and (t.dtype is not torch.bfloat16 or t.get_device() != dev or t.shape != want or not t.is_contiguous()):
             raise ValueError("k_out and v_out must be contiguous bfloat16 tensors of k's shape")
     if T == 0:
         return
     rc = load_library().fa2_kv4_append(
         k.data_ptr(), v.data_ptr(), _LL4(kt, kh, vt, vh), cache.data_ptr(), page_stride, slots.data_ptr(), _dp(k_out),
-        _dp(v_out), T, heads, pages, page_size, d, k_scale, v_scale, _raw_stream(dev.index))
+        _dp(v_out), T, heads, pages, page_size, d, k_scale, v_scale, _raw_stream(dev))
     if rc != FA2_OK:
         raise FA2Error("fa2_kv4_append", rc)
 
@@ -856,21 +863,21 @@ def fa2_kv4_gather(cache, block_table, cu_seqlens, total: int, k_scale: float = 
     """The cache's keys and values as packed bf16 [total, H_kv, d] (what fa2_fwd_varlen takes as k and v with
     cu_seqlens_k = ``cu_seqlens``).  Rows outside every sequence of given k, v are left as they are."""
     dev = _gpu(cache, "cache")
-    if stream is not None or dev.index != _current_device():
+    if stream is not None or dev != _current_device():
         with _on(dev, stream):
             return fa2_kv4_gather(cache, block_table, cu_seqlens, total, k_scale, v_scale, k, v)
     pages, heads, page_size, d, page_stride = _cache_dims(cache)
     B, width, row_stride = _table(block_table, dev)
     _ints(cu_seqlens, "cu_seqlens", dev, B + 1)
     for t in (k, v):
-        if t is not None and (t.device != dev or t.dtype is not torch.bfloat16 or t.shape != (total, heads, d)
+        if t is not None and (t.get_device() != dev or t.dtype is not torch.bfloat16 or t.shape != (total, heads, d)
                               or not t.is_contiguous()):
             raise ValueError("k and v must be contiguous bfloat16 [total, H_kv, d] on the cache's device")
-    k = torch.empty((total, heads, d), dtype=torch.bfloat16, device=dev) if k is None else k
-    v = torch.empty((total, heads, d), dtype=torch.bfloat16, device=dev) if v is None else v
+    k = torch.empty((total, heads, d), dtype=torch.bfloat16, device=cache.device) if k is None else k
+    v = torch.empty((total, heads, d), dtype=torch.bfloat16, device=cache.device) if v is None else v
     rc = load_library().fa2_kv4_gather(
         cache.data_ptr(), page_stride, block_table.data_ptr(), row_stride, cu_seqlens.data_ptr(), k.data_ptr(), v.data_ptr(), B, heads,
-        total, pages, page_size, width, d, k_scale, v_scale, _raw_stream(dev.index))
+        total, pages, page_size, width, d, k_scale, v_scale, _raw_stream(dev))
     if rc != FA2_OK:
         raise FA2Error("fa2_kv4_gather", rc)
     return k, v
@@ -893,12 +900,12 @@ def fa2_kv4_attn(q, cache, block_table, lens, cu_seqlens_q=None, max_seqlen_q: O
     max_seqlen_q the maximum is read from the offsets (a device sync).
     """
     dev = _gpu(cache, "cache")
-    if stream is not None or dev.index != _current_device():
+    if stream is not None or dev != _current_device():
         with _on(dev, stream):
             return fa2_kv4_attn(q, cache, block_table, lens, cu_seqlens_q, max_seqlen_q, o, lse, workspace, scale, k_scale,
                                 v_scale, causal)
     pages, heads, page_size, d, page_stride = _cache_dims(cache)
-    if q.dim() != 3 or q.dtype is not torch.bfloat16 or q.device != dev or not q.is_contiguous() or q.shape[2] != d:
+    if q.dim() != 3 or q.dtype is not torch.bfloat16 or q.get_device() != dev or not q.is_contiguous() or q.shape[2] != d:
         raise ValueError("q must be contiguous bfloat16 [total_q, H, d] on the cache's device, with its head dim")
     tq, H, _ = q.shape
     B, width, row_stride = _table(block_table, dev)
@@ -912,21 +919,22 @@ def fa2_kv4_attn(q, cache, block_table, lens, cu_seqlens_q=None, max_seqlen_q: O
             raise ValueError("without cu_seqlens_q every request has the same number of queries")
     if o is None:
         o = torch.empty_like(q)
-    elif o.shape != q.shape or o.dtype is not torch.bfloat16 or o.device != dev or not o.is_contiguous():
+    elif o.shape != q.shape or o.dtype is not torch.bfloat16 or o.get_device() != dev or not o.is_contiguous():
         raise ValueError("o must be contiguous bfloat16 with q's shape and device")
     if lse is None:
-        lse = torch.empty((H, tq), dtype=torch.float32, device=dev)
-    elif lse.dtype is not torch.float32 or lse.device != dev or not lse.is_contiguous() or lse.shape != (H, tq):
+        lse = torch.empty((H, tq), dtype=torch.float32, device=cache.device)
+    elif lse.dtype is not torch.float32 or lse.get_device() != dev or not lse.is_contiguous() or lse.shape != (H, tq):
         raise ValueError("lse must be a contiguous fp32 [H, total_q] tensor")
     lib = load_library()
     if workspace is None:
-        workspace = torch.empty(max(1, lib.fa2_kv4_attn_workspace_bytes(B, H, heads, mq, d)), dtype=torch.uint8, device=dev)
-    elif workspace.device != dev:
+        workspace = torch.empty(max(1, lib.fa2_kv4_attn_workspace_bytes(B, H, heads, mq, d)), dtype=torch.uint8,
+                                device=cache.device)
+    elif workspace.get_device() != dev:
         raise ValueError("workspace must be on the cache's device")
     rc = lib.fa2_kv4_attn(
         q.data_ptr(), cache.data_ptr(), page_stride, block_table.data_ptr(), row_stride, lens.data_ptr(), _dp(cu_seqlens_q),
         o.data_ptr(), lse.data_ptr(), B, H, heads, tq, mq, pages, page_size, width, d, _scale(scale, d), k_scale, v_scale, 1 if causal else 0,
-        workspace.data_ptr(), workspace.numel() * workspace.element_size(), _raw_stream(dev.index))
+        workspace.data_ptr(), workspace.numel() * workspace.element_size(), _raw_stream(dev))
     if rc != FA2_OK:
         raise FA2Error("fa2_kv4_attn", rc)
     return o, lse
