@@ -74,6 +74,7 @@ struct Attn4Problem {
   PagedCache cache;
   const int* table;
   long long table_stride;
+  size_t table_bytes, q_bytes;
   const int* lens;
   const int* cu_q;    // or NULL: every request has uniform_q queries
   float* part;        // [2 * spans][rows][d] unnormalised O
@@ -603,6 +604,14 @@ __global__ void __launch_bounds__(kWarps<NT> * 32, 1) fa2_kv4_attn_kernel(const 
   __syncwarp();
   griddep_wait();
   griddep_launch_dependents();
+  // Every warp needs, one after the other, the lengths, its request's page
+  // ids and its queries: the lines of the latter two start on their way to
+  // L2 while the first is being read.
+  {
+    const size_t line = (static_cast<size_t>(blockIdx.x) * blockDim.x + threadIdx.x) * 128;
+    if (line < p.table_bytes) prefetch_l2(reinterpret_cast<const char*>(p.table) + line);
+    if (line < p.q_bytes) prefetch_l2(reinterpret_cast<const char*>(p.q) + line);
+  }
   // Each lane adds up the pairs of its share of the requests.
   const int per = (p.B + 31) / 32;
   const int b_lo = min(lane * per, p.B), b_hi = min(b_lo + per, p.B);
@@ -908,6 +917,8 @@ int fa2_kv4_attn(const void* q, const void* cache, long long page_stride, const 
   p.cache = paged_cache(cache, page_stride, num_pages, page_size, H_kv);
   p.table = block_table;
   p.table_stride = table_stride;
+  p.table_bytes = tb;
+  p.q_bytes = qb;
   p.lens = lens;
   p.cu_q = cu_seqlens_q;
   char* ws = static_cast<char*>(workspace);

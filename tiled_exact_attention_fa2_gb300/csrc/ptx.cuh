@@ -182,6 +182,10 @@ __device__ __forceinline__ void bulk_load(uint32_t smem_dst, const void* src, ui
                : "memory");
 }
 
+__device__ __forceinline__ void prefetch_l2(const void* p) {
+  asm volatile("prefetch.global.L2 [%0];" ::"l"(reinterpret_cast<uint64_t>(p)));
+}
+
 // Four fp32 adds into global memory, performed at L2 (no return value).
 __device__ __forceinline__ void red_add_f32(float* addr, float a) {
   asm volatile("red.global.add.f32 [%0], %1;" ::"l"(addr), "f"(a) : "memory");
