@@ -3,7 +3,10 @@
 //
 // Both are bound by HBM: the append reads 2 bytes a value and writes 4.5
 // bits (and 2 bytes more where the caller wants the stored values), the
-// gather reads 4.5 bits and writes 2 bytes.
+// gather reads 4.5 bits and writes 2 bytes.  Measured on a GB300 (device
+// time): append of 16385 tokens x 8 heads of 128 columns with the stored
+// values 25.6 us (6.0 TB/s, 88 % of a copy's rate), gather of 20000 tokens of
+// the same 21.4 us (5.4 TB/s; 1258 CTAs in 2.8 waves).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -29,6 +32,20 @@ struct AppendProblem {
   int tokens, row_threads, block_tokens;  // threads of a token (H_kv d / 8), tokens of a CTA
 };
 
+// The values of four code bytes as bf16 (exact: 6 significant bits).
+__device__ __forceinline__ uint4 expand(uint32_t code, float scale) {
+  uint32_t hv[4], o[4];
+  e2m1x8_to_f16(code, hv);
+  const uint64_t s2 = f2_pack(scale, scale);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 v = f16x2_to_f32(hv[i]), u = f2_unpack(fmul2(f2_pack(v.x, v.y), s2));
+    o[i] = pack_bf16x2(u.x, u.y);
+  }
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
+__device__ __forceinline__ float scale_of(uint32_t byte) { return f16lo_to_f32(e4m3x2_to_f16(byte)); }
+
 // 8 columns of a group of 16, the other 8 in the neighbouring lane: the
 // group's scale byte, the columns' four code bytes, and the stored values in
 // place of x.  The scale is e4m3(max |x| / (6 f)), a code e2m1(x / (f s)), f
@@ -41,34 +58,28 @@ struct AppendProblem {
 // one, ties to even, as an exact division would give it.
 __device__ __forceinline__ void quantize(uint4& x, float f, uint32_t& scale, uint32_t& code, bool want_values) {
   const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-  uint32_t top = max_abs_bf16x2(max_abs_bf16x2(w[0], w[1]), max_abs_bf16x2(w[2], w[3]));
-  top = max_abs_bf16x2(top, __shfl_xor_sync(0xffffffffu, top, 1));
-  top = max_abs_bf16x2(top, top >> 16);  // (its low half)
+  constexpr uint32_t kAbs = 0x7fff7fffu;
+  uint32_t top = max_bf16x2(max_bf16x2(w[0] & kAbs, w[1] & kAbs), max_bf16x2(w[2] & kAbs, w[3] & kAbs));
+  top = max_bf16x2(top, __shfl_xor_sync(0xffffffffu, top, 1));
+  top = max_bf16x2(top, top >> 16);  // (its low half)
   const float mx = __uint_as_float(top << 16), inv_f = 1.f / f;  // a power of two: exact
   // a NaN in the group: the NaN scale
   scale = isnan(mx) ? 0x7fu : e4m3_of(mx * inv_f * (1.f / 6.f));
-  const float s = f16lo_to_f32(e4m3x2_to_f16(scale));
+  const float s = scale_of(scale);
   code = 0;  // of a group whose scale is 0 or NaN
   if (s > 0.f) {
-    const float inv = 1.f / s * inv_f;
+    const float inv = __frcp_rn(s) * inv_f;
+    const uint64_t inv2 = f2_pack(inv, inv);
     uint32_t q[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float2 v = unpack_bf16x2(w[i]);
-      q[i] = pack_f16x2(v.x * inv, v.y * inv);
+      const float2 v = unpack_bf16x2(w[i]), u = f2_unpack(fmul2(f2_pack(v.x, v.y), inv2));
+      q[i] = pack_f16x2(u.x, u.y);
     }
     code = f16_to_e2m1x8(q);
   }
   if (want_values) {
-    const float sf = s * f;
-    uint32_t hv[4], o[4];
-    e2m1x8_to_f16(code, hv);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 v = f16x2_to_f32(hv[i]);
-      o[i] = pack_bf16x2(v.x * sf, v.y * sf);
-    }
-    x = make_uint4(o[0], o[1], o[2], o[3]);
+    x = expand(code, s * f);
   }
 }
 
@@ -77,7 +88,7 @@ __device__ __forceinline__ void quantize(uint4& x, float f, uint32_t& scale, uin
 // 16 with IEEE divisions was bound by instructions: 36 us against 23 of
 // memory for 16385 tokens of 8 heads of 128 columns.)
 template <int D, int TOKENS>
-__global__ void __launch_bounds__(256) fa2_kv4_append_kernel(const AppendProblem p) {
+__global__ void __launch_bounds__(256, 5) fa2_kv4_append_kernel(const AppendProblem p) {
   using L = Kv4<D>;
   griddep_wait();
   griddep_launch_dependents();
@@ -184,18 +195,6 @@ __device__ __forceinline__ const char* find_row(const GatherProblem& p, int t, i
   return p.cache.base + id * p.cache.page_stride + static_cast<long long>(off >> 4) * tile_bytes;
 }
 
-__device__ __forceinline__ uint4 expand(uint32_t code, uint32_t scale, float f) {
-  const float s = f16lo_to_f32(e4m3x2_to_f16(scale)) * f;
-  uint32_t hv[4], o[4];
-  e2m1x8_to_f16(code, hv);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 v = f16x2_to_f32(hv[i]);
-    o[i] = pack_bf16x2(v.x * s, v.y * s);
-  }
-  return make_uint4(o[0], o[1], o[2], o[3]);
-}
-
 // A warp reads kGatherTokens packed rows of one head after another back: a
 // lane takes 8 columns (a 16-byte store) of every (D / 8)-th row, all loads
 // of the rows first.  Where the rows lie is found once per CTA, a thread per
@@ -253,8 +252,8 @@ __global__ void __launch_bounds__(256) fa2_kv4_gather_kernel(const GatherProblem
       const int row = group * kGatherTokens + i * kAtOnce + lane / kLanes;
       if (!s_tile[row]) continue;
       const long long dst = (static_cast<long long>(t0 + row) * p.cache.heads + h) * D + c8 * 8;
-      *reinterpret_cast<uint4*>(p.k + dst) = expand(kc[i], ks[i], p.k_scale);
-      *reinterpret_cast<uint4*>(p.v + dst) = expand(vc[i], vs[i], p.v_scale);
+      *reinterpret_cast<uint4*>(p.k + dst) = expand(kc[i], scale_of(ks[i]) * p.k_scale);
+      *reinterpret_cast<uint4*>(p.v + dst) = expand(vc[i], scale_of(vs[i]) * p.v_scale);
     }
   }
 }

@@ -15,6 +15,8 @@
 // for another's, and then writes its share of the tokens and table entries,
 // finding each one's request by bisection.  A new token's page comes from the
 // free list directly, never from the table entry another CTA writes.
+// Measured on a GB300 (device time): 64 requests with one new token each 2.9
+// us, 333 requests with 130 thousand new tokens 6.3 us.
 #include <cuda_runtime.h>
 
 #include <climits>

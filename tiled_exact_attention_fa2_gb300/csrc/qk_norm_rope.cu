@@ -23,6 +23,15 @@
 // two factors per column that a lane makes once per token and uses for
 // several heads; the arithmetic is on packed pairs of fp32.
 //
+// Measured on a GB300 (device time): 4 x 1023 tokens x 32 heads of 64 columns
+// forward 5.8 us (5.8 TB/s); the gradient for 16384 tokens x 40 heads of 128
+// 90.6 us (5.65 TB/s, 83 % of a copy's rate; the same bytes through an
+// elementwise sum take 74 us), of which the sums of the gains' gradients are
+// about 3 us; 48 tokens x 40 heads 2.2 us.  The backward pass issues about
+// 0.6 instructions a cycle and scheduler: what is left is neither memory nor
+// issue alone (24 warps an SM with spills or 16 with the next item's loads in
+// flight were slower than 20 without either).
+//
 // All sums and the arithmetic are fp32; the one rounding to bf16 is at the
 // store.
 #include <cuda_bf16.h>
