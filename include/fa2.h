@@ -489,19 +489,24 @@ int fa2_kv4_gather(const void* cache, long long page_stride, const int* block_ta
  * j iff j <= i + Lk - Lq; a query that sees no key gets o = 0 and lse = -inf.
  * Rows outside every request are not written.  What the pages hold past a
  * request's length has no influence, not even a NaN.
- * A request whose lengths are out of range (negative, more tokens than its
- * table row has room for, query rows outside [0, total_q] or more than
- * max_seqlen_q) is skipped and the device status word becomes 3; a page id
+ * max_seqlen_k >= 1 bounds the lengths (table_width * page_size where it is
+ * larger); a tight bound lets short requests take one launch.
+ * A request whose lengths are out of range (negative, more than max_seqlen_k
+ * tokens or than its table row has room for, query rows outside [0, total_q]
+ * or more than max_seqlen_q) is skipped and the device status word becomes 3; a page id
  * outside [0, num_pages) leaves its keys out and sets 5.
- * workspace: 256-byte aligned, fa2_kv4_attn_workspace_bytes(...) bytes (0 for
- * invalid sizes), whatever it holds.  Two launches.  Results do not vary
- * from run to run.  total_q = 0 is allowed and does nothing.
+ * workspace: 256-byte aligned, fa2_kv4_attn_workspace_bytes(...) bytes for the
+ * same sizes (max_seqlen_k not above the table's room), whatever it holds; NULL
+ * where that is 0: small calls (few key/value heads and rows of short
+ * requests) need none and take one launch, others two.  (It is 0 for invalid
+ * sizes as well.)  Results do not vary from run to run.  total_q = 0 is
+ * allowed and does nothing.
  */
-size_t fa2_kv4_attn_workspace_bytes(int B, int H, int H_kv, int max_seqlen_q, int d);
+size_t fa2_kv4_attn_workspace_bytes(int B, int H, int H_kv, int max_seqlen_q, int max_seqlen_k, int d);
 int fa2_kv4_attn(const void* q, const void* cache, long long page_stride, const int* block_table, long long table_stride,
                  const int* lens, const int* cu_seqlens_q, void* o, float* lse, int B, int H, int H_kv, int total_q,
-                 int max_seqlen_q, int num_pages, int page_size, int table_width, int d, float scale, float k_scale,
-                 float v_scale, int causal, void* workspace, size_t workspace_bytes, void* stream);
+                 int max_seqlen_q, int max_seqlen_k, int num_pages, int page_size, int table_width, int d, float scale,
+                 float k_scale, float v_scale, int causal, void* workspace, size_t workspace_bytes, void* stream);
 
 /* Static description of a status code (never NULL). */
 const char* fa2_status_string(int status);

@@ -59,10 +59,10 @@ def gather(lib, cache=A, table=2 * A, cu=3 * A, k=4 * A, v=5 * A, B=2, Hkv=2, to
                               vs, None)
 
 
-def attn(lib, q=A, cache=2 * A, table=3 * A, lens=4 * A, cu=5 * A, o=6 * A, lse=7 * A, B=2, H=4, Hkv=2, tq=8, mq=4, pages=4, P=16,
-         W=2, tstride=None, d=64, scale=0.1, ks=1.0, vs=1.0, ws=8 * A, wsb=1 << 30, stride=None):
+def attn(lib, q=A, cache=2 * A, table=3 * A, lens=4 * A, cu=5 * A, o=6 * A, lse=7 * A, B=2, H=4, Hkv=2, tq=8, mq=4, mk=1 << 30, pages=4,
+         P=16, W=2, tstride=None, d=64, scale=0.1, ks=1.0, vs=1.0, ws=8 * A, wsb=1 << 30, stride=None):
     stride = Hkv * (P // 16) * 18 * d if stride is None else stride
-    return lib.fa2_kv4_attn(q, cache, stride, table, W if tstride is None else tstride, lens, cu, o, lse, B, H, Hkv, tq, mq, pages,
+    return lib.fa2_kv4_attn(q, cache, stride, table, W if tstride is None else tstride, lens, cu, o, lse, B, H, Hkv, tq, mq, mk, pages,
                             P, W, d, scale, ks, vs, 1, ws, wsb, None)
 
 
@@ -111,18 +111,24 @@ def test_attention_refusals(lib):
     for name in ("q", "table", "lens", "o", "lse"):
         assert attn(lib, **{name: None}) == 1
     for bad in (dict(B=0), dict(H=0), dict(H=3), dict(tq=-1), dict(mq=0), dict(mq=9), dict(W=0), dict(tstride=1),
-                dict(cu=None, tq=7), dict(tq=(1 << 30) + 1)):
+                dict(cu=None, tq=7), dict(tq=(1 << 30) + 1), dict(mk=0), dict(mk=-5)):
         assert attn(lib, **bad) == 2, bad
     for s in (0.0, -0.1, float("nan"), float("inf")):
         assert attn(lib, scale=s) == 5
     for bad in (dict(q=A + 8), dict(o=6 * A + 2), dict(lse=7 * A + 2), dict(lens=4 * A + 1), dict(cu=5 * A + 2)):
         assert attn(lib, **bad) == 4, bad
-    need = lib.fa2_kv4_attn_workspace_bytes(2, 4, 2, 4, 64)
-    assert need > 0 and attn(lib, ws=None) == 8 and attn(lib, ws=8 * A + 16) == 8 and attn(lib, wsb=need - 1) == 8
-    for bad in (dict(o=A), dict(o=2 * A), dict(lse=6 * A), dict(ws=A), dict(ws=2 * A), dict(lse=4 * A)):
+    for bad in (dict(o=A), dict(o=2 * A), dict(lse=6 * A), dict(lse=4 * A)):
         assert attn(lib, **bad) == 9, bad
-    for bad in ((0, 4, 2, 1, 64), (1, 4, 3, 1, 64), (1, 4, 2, 0, 64), (1, 4, 2, 1, 60)):
-        assert lib.fa2_kv4_attn_workspace_bytes(*bad) == 0
+    # tables of more than 2048 keys, or more than 152 units: two launches and a workspace
+    need = lib.fa2_kv4_attn_workspace_bytes(2, 4, 2, 4, 129 * 16, 64)
+    assert need > 0 and attn(lib, W=129, ws=None) == 8 and attn(lib, W=129, ws=8 * A + 16) == 8
+    assert attn(lib, W=129, wsb=need - 1) == 8 and attn(lib, W=129, ws=A) == 9 and attn(lib, W=129, ws=2 * A) == 9
+    ws = lib.fa2_kv4_attn_workspace_bytes
+    assert ws(77, 4, 2, 4, 32, 64) > 0 and ws(76, 4, 2, 4, 32, 64) == 0 and ws(1, 4, 2, 4, 2048, 64) == 0
+    assert ws(76, 4, 2, 4, 54 * 152, 64) == 0 and ws(76, 4, 2, 4, 54 * 152 + 1, 64) > 0
+    assert attn(lib, W=129, mk=2048, ws=None, o=A) == 9  # (a tight bound: no workspace asked for)
+    for bad in ((0, 4, 2, 1, 99, 64), (1, 4, 3, 1, 99, 64), (1, 4, 2, 0, 99, 64), (1, 4, 2, 1, 0, 64), (1, 4, 2, 1, 99999, 60)):
+        assert ws(*bad) == 0
 
 
 def test_plan_refusals(lib):
@@ -402,22 +408,28 @@ ATTN = [  # d, H, Hkv, P, lens, queries, causal
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("wide", [False, True])  # room for at most 2048 / for more keys: one CTA per unit / the line
 @pytest.mark.parametrize("case", ATTN, ids=str)
-def test_attention(case):
+def test_attention(case, wide):
     d, H, Hkv, P, lens, nq, causal = case
     rng = np.random.default_rng(sum(lens) + d)
-    cache, table, kv = filled(rng, lens, Hkv, P, d, width=1)
+    cache, table, kv = filled(rng, lens, Hkv, P, d, width=8192 // P if wide else 1)
     cu = np.r_[0, np.cumsum(nq)]
     total = int(cu[-1])
     q = torch.from_numpy(rng.standard_normal((total + 3, H, d)) * 2).to(torch.bfloat16).cuda()
     o, lse = torch.full_like(q, 9.0), torch.full((H, total + 3), 9.0, device="cuda")
     fa2.fa2_device_status(reset=True)
-    ws = torch.full((fa2.fa2_kv4_attn_workspace_bytes(len(lens), H, Hkv, max(nq), d),), 255, dtype=torch.uint8, device="cuda")
+    need = fa2.fa2_kv4_attn_workspace_bytes(len(lens), H, Hkv, max(nq), table.shape[1] * P, d)
+    assert (need > 0) == wide
+    ws = torch.full((need,), 255, dtype=torch.uint8, device="cuda") if need else None
     fa2.fa2_kv4_attn(q, cache, i32(table), i32(lens), i32(cu), max(nq), o=o, lse=lse, workspace=ws, causal=causal)
     assert fa2.fa2_device_status() == 0
     assert torch.all(o[total:] == 9) and torch.all(lse[:, total:] == 9)  # rows behind the last request
     rows = [(int(cu[b]), int(cu[b + 1])) for b in range(len(lens))]
     check_attention(o, lse, rows, q.double().cpu().numpy(), kv, 1 / math.sqrt(d), causal, H)
+    if wide:  # the same bound given: the other form, within the same tolerances
+        short = fa2.fa2_kv4_attn(q, cache, i32(table), i32(lens), i32(cu), max(nq), max_seqlen_k=max(max(lens), 1), causal=causal)
+        check_attention(*short, rows, q.double().cpu().numpy(), kv, 1 / math.sqrt(d), causal, H)
     o2, lse2 = fa2.fa2_kv4_attn(q, cache, i32(table), i32(lens), i32(cu), causal=causal)
     assert torch.equal(o2[:total], o[:total]) and torch.equal(lse2[:, :total], lse[:, :total])
     if len(set(nq)) == 1:
@@ -426,8 +438,8 @@ def test_attention(case):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("B,n,H,Hkv,nq,d", [(3, 20011, 8, 2, 1, 128), (1, 40000, 16, 1, 2, 64), (70, 350, 4, 2, 1, 128),
-                                            (2, 9000, 8, 1, 6, 128)])
+@pytest.mark.parametrize("B,n,H,Hkv,nq,d", [(3, 20011, 8, 2, 1, 128), (1, 40000, 16, 1, 2, 64), (90, 350, 4, 2, 1, 128),
+                                            (2, 9000, 8, 1, 6, 128), (5, 2048, 8, 2, 3, 128), (19, 2000, 16, 8, 1, 64)])
 def test_attention_long_and_shared_units(B, n, H, Hkv, nq, d):
     """Units cut over many spans, and many units in a span; scores that grow along the keys (late maxima)."""
     rng = np.random.default_rng(n)
@@ -472,12 +484,13 @@ def test_attention_scales_and_page_stride():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("wide", [0, 128])
 @pytest.mark.parametrize("d", [16, 64, 128])
-def test_nan_reaches_only_the_rows_that_see_it(d):
-    """A NaN value or key at position 20 of 24 with 8 causal queries: the first three do not see it."""
+def test_nan_reaches_only_the_rows_that_see_it(d, wide):
+    """A NaN value or key at position 20 of 24 with 8 causal queries: the first four do not see it."""
     rng = np.random.default_rng(d)
     for where in ("v", "k"):
-        cache, table, kv = filled(rng, [24, 24], 1, 16, d)
+        cache, table, kv = filled(rng, [24, 24], 1, 16, d, width=wide)
         slot = int(table[0, 1]) * 16 + 4
         k, v = rng.standard_normal((2, 1, d))
         (v if where == "v" else k)[0, 3] = np.nan
@@ -519,19 +532,23 @@ def test_large_queries_and_zero_rows():
 
 
 @pytest.mark.gpu
-def test_bad_lengths_and_pages_are_reported():
+@pytest.mark.parametrize("wide", [0, 128])
+def test_bad_lengths_and_pages_are_reported(wide):
     rng = np.random.default_rng(9)
     lens = [40, 50, 60]
-    cache, table, kv = filled(rng, lens, 2, 16, 64)
+    cache, table, kv = filled(rng, lens, 2, 16, 64, width=wide)
     q = torch.from_numpy(rng.standard_normal((3, 4, 64))).to(torch.bfloat16).cuda()
     q64 = q.double().cpu().numpy()
     fa2.fa2_device_status(reset=True)
-    for bad in ([40, -1, 60], [40, 65, 60]):  # 4 pages of 16 a row
+    for bad in ([40, -1, 60], [40, 65 + 16 * wide, 60]):  # 4 (and `wide`) pages of 16 a row
         o, lse = torch.full_like(q, 9.0), torch.full((4, 3), 9.0, device="cuda")
         fa2.fa2_kv4_attn(q, cache, i32(table), i32(bad), o=o, lse=lse)
         assert fa2.fa2_device_status(reset=True) == 3
         assert torch.all(o[1] == 9) and torch.all(lse[:, 1] == 9)
         check_attention(o, lse, [(0, 1), (1, 1), (2, 3)], q64, kv, 0.125, True, 4)
+    o = torch.full_like(q, 9.0)
+    fa2.fa2_kv4_attn(q, cache, i32(table), i32(lens), o=o, max_seqlen_k=50)  # longer than the bound
+    assert fa2.fa2_device_status(reset=True) == 3 and torch.all(o[2] == 9) and not torch.any(o[:2] == 9)
     # query offsets: backwards, past the end, longer than stated
     for cu in ([0, 2, 1, 3], [0, 1, 2, 5], [-1, 1, 2, 3], [0, 2, 3, 3]):
         o = torch.full_like(q, 9.0)
@@ -555,7 +572,10 @@ def test_graphs_that_share_a_workspace_and_streams():
     t, n = i32(table), i32(lens)
     qs = [torch.from_numpy(rng.standard_normal((2, 8, 128))).to(torch.bfloat16).cuda() for _ in range(2)]
     want = [fa2.fa2_kv4_attn(q, cache, t, n) for q in qs]
-    ws = torch.empty(fa2.fa2_kv4_attn_workspace_bytes(2, 8, 2, 1, 128), dtype=torch.uint8, device="cuda")
+    t = torch.cat([t, torch.full((2, 128), -1, dtype=torch.int32, device="cuda")], 1)  # more than 2048 keys: needs a workspace
+    want = [fa2.fa2_kv4_attn(q, cache, t, n) for q in qs]
+    ws = torch.empty(fa2.fa2_kv4_attn_workspace_bytes(2, 8, 2, 1, t.shape[1] * 16, 128), dtype=torch.uint8, device="cuda")
+    assert ws.numel() > 0
     graphs, outs = [], []
     for q in qs:
         graphs.append(torch.cuda.CUDAGraph())
@@ -570,11 +590,12 @@ def test_graphs_that_share_a_workspace_and_streams():
             assert torch.equal(o, wo) and torch.equal(lse, wl)
     # other lengths in a captured step
     n.copy_(i32([17, 299]))
-    t.copy_(i32(table[::-1].copy()))
+    t[:, :table.shape[1]] = i32(table[::-1].copy())
     graphs[0].replay()
     check_attention(*outs[0], [(0, 1), (1, 2)], qs[0].double().cpu().numpy(),
                     [tuple(x[:, :17] for x in kv[1]), tuple(x[:, :299] for x in kv[0])], 128 ** -0.5, True, 8)
-    n.copy_(i32(lens)), t.copy_(i32(table))
+    n.copy_(i32(lens))
+    t[:, :table.shape[1]] = i32(table)
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
     a = fa2.fa2_kv4_attn(qs[0], cache, t, n, stream=side)

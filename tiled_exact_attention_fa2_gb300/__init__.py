@@ -85,9 +85,9 @@ _SIGNATURES = {
     "fa2_kv4_page_bytes": (_sz, [_i, _i, _i]),
     "fa2_kv4_append": (_i, [_vp, _vp, _llp, _vp, _ll, _vp, _vp, _vp, _i, _i, _i, _i, _i, _f, _f, _vp]),
     "fa2_kv4_gather": (_i, [_vp, _ll, _vp, _ll, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _f, _f, _vp]),
-    "fa2_kv4_attn_workspace_bytes": (_sz, [_i, _i, _i, _i, _i]),
-    "fa2_kv4_attn": (_i, [_vp, _vp, _ll, _vp, _ll, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _i, _i, _f, _f, _f, _i,
-                          _vp, _sz, _vp]),
+    "fa2_kv4_attn_workspace_bytes": (_sz, [_i, _i, _i, _i, _i, _i]),
+    "fa2_kv4_attn": (_i, [_vp, _vp, _ll, _vp, _ll, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _i, _i, _i, _f, _f, _f,
+                          _i, _vp, _sz, _vp]),
 }
 
 
@@ -883,13 +883,14 @@ def fa2_kv4_gather(cache, block_table, cu_seqlens, total: int, k_scale: float = 
     return k, v
 
 
-def fa2_kv4_attn_workspace_bytes(B: int, H: int, H_kv: int, max_seqlen_q: int, d: int) -> int:
-    return load_library().fa2_kv4_attn_workspace_bytes(B, H, H_kv, max_seqlen_q, d)
+def fa2_kv4_attn_workspace_bytes(B: int, H: int, H_kv: int, max_seqlen_q: int, max_seqlen_k: int, d: int) -> int:
+    """Scratch of fa2_kv4_attn (0: none); max_seqlen_k at most width * page_size of the block table."""
+    return load_library().fa2_kv4_attn_workspace_bytes(B, H, H_kv, max_seqlen_q, max_seqlen_k, d)
 
 
-def fa2_kv4_attn(q, cache, block_table, lens, cu_seqlens_q=None, max_seqlen_q: Optional[int] = None, o=None, lse=None,
-                 workspace=None, scale: Optional[float] = None, k_scale: float = 1.0, v_scale: float = 1.0,
-                 causal: bool = True, stream=None):
+def fa2_kv4_attn(q, cache, block_table, lens, cu_seqlens_q=None, max_seqlen_q: Optional[int] = None,
+                 max_seqlen_k: Optional[int] = None, o=None, lse=None, workspace=None, scale: Optional[float] = None,
+                 k_scale: float = 1.0, v_scale: float = 1.0, causal: bool = True, stream=None):
     """Attention of packed queries q [total_q, H, d] over the 4-bit paged cache: (o [total_q, H, d] bf16,
     lse [H, total_q] fp32).
 
@@ -898,12 +899,14 @@ def fa2_kv4_attn(q, cache, block_table, lens, cu_seqlens_q=None, max_seqlen_q: O
     positions where ``causal``.  Without cu_seqlens_q every request has
     ``max_seqlen_q`` queries (default: total_q / B).  With cu_seqlens_q and no
     max_seqlen_q the maximum is read from the offsets (a device sync).
+    ``max_seqlen_k`` bounds lens (default: what block_table has room for); a
+    tight bound lets short requests take a single launch without workspace.
     """
     dev = _gpu(cache, "cache")
     if stream is not None or dev != _current_device():
         with _on(dev, stream):
-            return fa2_kv4_attn(q, cache, block_table, lens, cu_seqlens_q, max_seqlen_q, o, lse, workspace, scale, k_scale,
-                                v_scale, causal)
+            return fa2_kv4_attn(q, cache, block_table, lens, cu_seqlens_q, max_seqlen_q, max_seqlen_k, o, lse, workspace,
+                                scale, k_scale, v_scale, causal)
     pages, heads, page_size, d, page_stride = _cache_dims(cache)
     if q.dim() != 3 or q.dtype is not torch.bfloat16 or q.get_device() != dev or not q.is_contiguous() or q.shape[2] != d:
         raise ValueError("q must be contiguous bfloat16 [total_q, H, d] on the cache's device, with its head dim")
@@ -926,15 +929,19 @@ def fa2_kv4_attn(q, cache, block_table, lens, cu_seqlens_q=None, max_seqlen_q: O
     elif lse.dtype is not torch.float32 or lse.get_device() != dev or not lse.is_contiguous() or lse.shape != (H, tq):
         raise ValueError("lse must be a contiguous fp32 [H, total_q] tensor")
     lib = load_library()
+    mk = min(width * page_size, 2 ** 31 - 1)
+    if max_seqlen_k is not None and max_seqlen_k < mk:
+        mk = int(max_seqlen_k)
     if workspace is None:
-        workspace = torch.empty(max(1, lib.fa2_kv4_attn_workspace_bytes(B, H, heads, mq, d)), dtype=torch.uint8,
-                                device=cache.device)
+        need = lib.fa2_kv4_attn_workspace_bytes(B, H, heads, mq, mk, d)
+        if need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=cache.device)
     elif workspace.get_device() != dev:
         raise ValueError("workspace must be on the cache's device")
     rc = lib.fa2_kv4_attn(
         q.data_ptr(), cache.data_ptr(), page_stride, block_table.data_ptr(), row_stride, lens.data_ptr(), _dp(cu_seqlens_q),
-        o.data_ptr(), lse.data_ptr(), B, H, heads, tq, mq, pages, page_size, width, d, _scale(scale, d), k_scale, v_scale, 1 if causal else 0,
-        workspace.data_ptr(), workspace.numel() * workspace.element_size(), _raw_stream(dev))
+        o.data_ptr(), lse.data_ptr(), B, H, heads, tq, mq, mk, pages, page_size, width, d, _scale(scale, d), k_scale, v_scale, 1 if causal else 0,
+        _dp(workspace), 0 if workspace is None else workspace.numel() * workspace.element_size(), _raw_stream(dev))
     if rc != FA2_OK:
         raise FA2Error("fa2_kv4_attn", rc)
     return o, lse

@@ -17,7 +17,9 @@
 // A unit inside one span is finished by its warp; one that spans share leaves
 // a partial result per span (unnormalised O, running maximum and sum), which
 // the combine kernel joins in span order.  Warps share nothing, so there are
-// no barriers, and the result does not depend on the order they run in.
+// no barriers, and the result does not depend on the order they run in.  Few
+// units of short requests take one CTA each instead, whose warps share the
+// unit's keys and join in shared memory.
 //
 // Operands (lane (g, c) = (lane / 4, lane % 4)).  The first product is
 // S^T = K Q^T: a tile's 16 keys are the rows of the instruction and the 8
@@ -39,7 +41,7 @@
 // by instruction issue: an mma.m16n8k16 takes about 8 issue slots of its
 // scheduler, and 32 of them with the 64 decodes and 64 scalings of a tile at
 // least 107 cycles of an SM against 98 for the tile's bytes; one request of
-// 1000 keys 8.9 us, bound by latency.
+// 1000 keys 7.7 us, bound by latency.
 //
 // Precision.  Cache values are exact in fp16 (6 significant bits), Q (8 bits)
 // is divided by a power of two per row so that its largest value is in
@@ -91,7 +93,7 @@ struct Attn4Problem {
   float* part;        // [2 * spans][rows][d] unnormalised O
   float2* part_ml;    // [2 * spans][rows] maximum (log2), sum
   long long* start;   // [B + 1] first tile pair of each request on the line
-  int B, H, G, total_q, uniform_q, max_q, width;
+  int B, H, G, total_q, uniform_q, max_q, max_k;
   float scale_log2, v_scale;
   int causal;
 };
@@ -112,8 +114,7 @@ __device__ __forceinline__ Request request(const Attn4Problem& p, int b) {
     r.q0 = b * p.uniform_q;
     r.Lq = p.uniform_q;
   }
-  r.ok = r.Lk >= 0 && (r.Lk + ((1LL << p.cache.shift) - 1)) >> p.cache.shift <= p.width && r.q0 >= 0 && r.Lq >= 0 &&
-         r.Lq <= p.max_q && r.q0 <= p.total_q - r.Lq;
+  r.ok = r.Lk >= 0 && r.Lk <= p.max_k && r.q0 >= 0 && r.Lq >= 0 && r.Lq <= p.max_q && r.q0 <= p.total_q - r.Lq;
   return r;
 }
 
@@ -480,10 +481,12 @@ __device__ __forceinline__ void step(Rows<D, NT>& s, uint32_t tiles, int key0, i
 // o and lse of a row from its sums (a row that saw no key: zeros, -inf).
 __device__ __forceinline__ float row_lse(float m, float l) { return (m - kLift + log2f(l)) * 0.69314718055994531f; }
 
+// The end of a unit's keys: its rows go out, or, where `part` is given, leave
+// a partial result there ([rows][D]) and in `ml`.
 template <int D, int NT>
 __device__ __forceinline__ void end_unit(Rows<D, NT>& s, const Attn4Problem& p, const Request& rq, int h, int row0,
-                                         int slot, int lane) {
-  constexpr int kPer = D / 8, kRows = 8 * NT;
+                                         float* part, float2* ml, int lane) {
+  constexpr int kPer = D / 8;
   const int g = lane >> 2, c = lane & 3;
   const int rows = p.G * rq.Lq;
 #pragma unroll
@@ -502,8 +505,8 @@ __device__ __forceinline__ void end_unit(Rows<D, NT>& s, const Attn4Problem& p, 
         v[2 * i] = s.o[j][i][u];
         v[2 * i + 1] = s.o[j][i][u + 2];
       }
-      if (slot >= 0) {
-        float* dst = p.part + (static_cast<long long>(slot) * kRows + local) * D + g * kPer;
+      if (part) {
+        float* dst = part + local * D + g * kPer;
 #pragma unroll
         for (int i = 0; i < kPer; i += (kPer >= 4 ? 4 : 2)) {
           if constexpr (kPer >= 4)
@@ -511,7 +514,7 @@ __device__ __forceinline__ void end_unit(Rows<D, NT>& s, const Attn4Problem& p, 
           else
             *reinterpret_cast<float2*>(dst + i) = make_float2(v[i], v[i + 1]);
         }
-        if (g == 0) p.part_ml[static_cast<long long>(slot) * kRows + local] = make_float2(m, l);
+        if (g == 0) ml[local] = make_float2(m, l);
         continue;
       }
       const float k = l == 0.f ? 0.f : p.v_scale / l;
@@ -598,8 +601,74 @@ template <int D, int NT>
 struct __align__(128) WarpSmem {
   char tiles[2 * kPair * Kv4<D>::kTileBytes];
   uint64_t q[NT * (D / 16) * 32];
+  float2 ml[8 * NT];  // of a partial result (its rows are put into `tiles`)
   uint64_t full[2];
 };
+static_assert(sizeof(WarpSmem<16, 2>::tiles) >= 16 * 16 * 4 && sizeof(WarpSmem<128, 2>::tiles) >= 16 * 128 * 4, "rows fit");
+
+template <int D, int NT>
+__device__ __forceinline__ void start_warp(WarpSmem<D, NT>* ws, Rows<D, NT>& s, Ring& ring, int lane) {
+  // (a warp's barriers are its own: no other warp waits for this)
+  if (lane == 0) {
+    for (int i = 0; i < 2; ++i) mbar_init(&ws->full[i], 1);
+    fence_mbar_init();
+  }
+  __syncwarp();
+  s.q = smem_u32(ws->q) + lane * 8;
+  ring.tiles = smem_u32(ws->tiles);
+  ring.full = ws->full;
+  ring.slot = ring.phase = ring.bad = 0;
+}
+
+// Pairs first .. first + n - 1 (n > 0) of a unit's keys into fresh row states.
+// False (and a status word) if a copy did not come in time.
+template <int D, int NT>
+__device__ __forceinline__ bool run_pairs(Rows<D, NT>& s, Ring& ring, const Attn4Problem& p, const Request& rq, int b, int h,
+                                          int row0, int first, int n, int lane) {
+  ring.row = p.table + b * p.table_stride;
+  ring.pages = static_cast<int>((rq.Lk + ((1LL << p.cache.shift) - 1)) >> p.cache.shift);
+  ring.head = p.cache.base + (static_cast<long long>(h) << (p.cache.shift - 4)) * Kv4<D>::kTileBytes;
+  // (both slots are free here: the part before has been read to its end)
+  look_up<D>(ring, p, first, lane);
+  fetch<D>(ring, p, first, ring.slot, lane);
+  if (n > 1) fetch<D>(ring, p, first + 1, ring.slot ^ 1, lane);
+  start_unit<D, NT>(s, p, rq, h, row0, lane);
+  const int whole = s.min_vis / kPairKeys;  // every row sees all keys of the pairs below
+  for (int pair = first; pair < first + n; ++pair) {
+    if (!mbar_wait(&ring.full[ring.slot], ring.phase, &g_attn4_status)) {
+      // a copy that never came: wait (as long again) for the other, then give up
+      if (pair + 1 < first + n) mbar_wait(&ring.full[ring.slot ^ 1], ring.phase ^ ring.slot, &g_attn4_status);
+      return false;
+    }
+    const uint32_t tiles = ring.tiles + ring.slot * (kPair * Kv4<D>::kTileBytes);
+    if (__builtin_expect(pair < whole && !ring.bad, 1))
+      step<D, NT, false>(s, tiles, 0, 0, 0, lane);
+    else
+      step<D, NT, true>(s, tiles, pair * kPairKeys, rq.Lk, ring.bad >> 2 * ring.slot & 3u, lane);
+    __syncwarp();  // every lane has read the slot
+    if (pair + 2 < first + n) fetch<D>(ring, p, pair + 2, ring.slot, lane);
+    ring.phase ^= ring.slot;  // (the parity changes when the ring has gone round)
+    ring.slot ^= 1;
+  }
+  return true;
+}
+
+// A joined row: `o` the lane's columns of the sum of weighted partial rows, l
+// and top of the same.
+template <int D>
+__device__ __forceinline__ void write_row(const Attn4Problem& p, const Request& rq, int h, int r, const float* o, float l,
+                                          float top, int lane) {
+  constexpr int kCols = D >= 32 ? D / 32 : 1;
+  const int i = r / p.G;
+  const long long tok = rq.q0 + i;
+  const int head = h * p.G + (r - i * p.G);
+  const float f = l == 0.f ? 0.f : p.v_scale / l;
+  __nv_bfloat16* dst = p.o + (tok * p.H + head) * D + lane * kCols;
+#pragma unroll
+  for (int k = 0; k < kCols; ++k)
+    if (lane * kCols < D) dst[k] = __float2bfloat16_rn(o[k] * f);
+  if (lane == 0) p.lse[static_cast<long long>(head) * p.total_q + tok] = l == 0.f ? -INFINITY : row_lse(top, l);
+}
 
 template <int D, int NT>
 __global__ void __launch_bounds__(kWarps<NT> * 32, 1) fa2_kv4_attn_kernel(const Attn4Problem p) {
@@ -607,12 +676,9 @@ __global__ void __launch_bounds__(kWarps<NT> * 32, 1) fa2_kv4_attn_kernel(const 
   extern __shared__ __align__(128) char smem[];
   WarpSmem<D, NT>* const ws = reinterpret_cast<WarpSmem<D, NT>*>(smem) + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  // (a warp's barriers are its own: no other warp waits for this)
-  if (lane == 0) {
-    for (int i = 0; i < 2; ++i) mbar_init(&ws->full[i], 1);
-    fence_mbar_init();
-  }
-  __syncwarp();
+  Rows<D, NT> s;
+  Ring ring;
+  start_warp(ws, s, ring, lane);
   griddep_wait();
   griddep_launch_dependents();
   // Every warp needs, one after the other, the lengths, its request's page
@@ -665,12 +731,6 @@ __global__ void __launch_bounds__(kWarps<NT> * 32, 1) fa2_kv4_attn_kernel(const 
   Request rq = request(p, b);
   long long size = pairs_of<kRows>(p, rq);
 
-  Rows<D, NT> s;
-  s.q = smem_u32(ws->q) + lane * 8;
-  Ring ring;
-  ring.tiles = smem_u32(ws->tiles);
-  ring.full = ws->full;
-  ring.slot = ring.phase = ring.bad = 0;
   while (at < end) {
     while (at >= base + size) {
       base += size;
@@ -685,35 +745,11 @@ __global__ void __launch_bounds__(kWarps<NT> * 32, 1) fa2_kv4_attn_kernel(const 
     const int first = static_cast<int>(rel - static_cast<long long>(unit) * np);
     const int h = unit / rt, row0 = (unit - h * rt) * kRows;
     const int n = static_cast<int>(min(static_cast<long long>(np - first), end - at));
-    ring.row = p.table + b * p.table_stride;
-    ring.pages = static_cast<int>((rq.Lk + ((1LL << p.cache.shift) - 1)) >> p.cache.shift);
-    ring.head = p.cache.base + (static_cast<long long>(h) << (p.cache.shift - 4)) * Kv4<D>::kTileBytes;
-    // (both slots are free here: the part before has been read to its end)
-    look_up<D>(ring, p, first, lane);
-    fetch<D>(ring, p, first, ring.slot, lane);
-    if (n > 1) fetch<D>(ring, p, first + 1, ring.slot ^ 1, lane);
-    start_unit<D, NT>(s, p, rq, h, row0, lane);
-    const int whole = s.min_vis / kPairKeys;  // every row sees all keys of the pairs below
-    for (int pair = first; pair < first + n; ++pair) {
-      if (!mbar_wait(&ring.full[ring.slot], ring.phase, &g_attn4_status)) {
-        // a copy that never came: wait (as long again) for the other, then give up
-        if (pair + 1 < first + n) mbar_wait(&ring.full[ring.slot ^ 1], ring.phase ^ ring.slot, &g_attn4_status);
-        return;
-      }
-      const uint32_t tiles = ring.tiles + ring.slot * (kPair * Kv4<D>::kTileBytes);
-      if (__builtin_expect(pair < whole && !ring.bad, 1))
-        step<D, NT, false>(s, tiles, 0, 0, 0, lane);
-      else
-        step<D, NT, true>(s, tiles, pair * kPairKeys, rq.Lk, ring.bad >> 2 * ring.slot & 3u, lane);
-      __syncwarp();  // every lane has read the slot
-      if (pair + 2 < first + n) fetch<D>(ring, p, pair + 2, ring.slot, lane);
-      ring.phase ^= ring.slot;  // (the parity changes when the ring has gone round)
-      ring.slot ^= 1;
-    }
+    if (!run_pairs<D, NT>(s, ring, p, rq, b, h, row0, first, n, lane)) return;
     // A unit that is whole goes out; else slot 0 of the span if the part
     // began at the span's start, slot 1 if within it.
-    const int slot = n == np ? -1 : 2 * span + (at == begin ? 0 : 1);
-    end_unit<D, NT>(s, p, rq, h, row0, slot, lane);
+    const long long slot = (2LL * span + (at == begin ? 0 : 1)) * kRows;
+    end_unit<D, NT>(s, p, rq, h, row0, n == np ? nullptr : p.part + slot * D, p.part_ml + slot, lane);
     at += n;
   }
 }
@@ -819,33 +855,106 @@ __global__ void __launch_bounds__(256) fa2_kv4_combine_kernel(const Attn4Problem
         if (active) o[k] = fmaf(s_o[warp + w][lane * kCols + k], down, o[k]);
     }
   }
-  const int i0 = r / p.G;
-  const long long tok = rq.q0 + i0;
-  const int head = h * p.G + (r - i0 * p.G);
-  const float f = l == 0.f ? 0.f : p.v_scale / l;
-  __nv_bfloat16* dst = p.o + (tok * p.H + head) * D + lane * kCols;
+  write_row<D>(p, rq, h, r, o, l, top, lane);
+}
+
+// Short requests: one CTA per unit, whose warps take equal parts of its keys
+// and join their partial results in shared memory, in the order of the keys:
+// one launch, no line to lay out first, no workspace.
+template <int D, int NT>
+__global__ void __launch_bounds__(kWarps<NT> * 32, 1) fa2_kv4_attn_unit_kernel(const Attn4Problem p, int max_row_tiles) {
+  constexpr int kRows = 8 * NT, kCols = D >= 32 ? D / 32 : 1;
+  extern __shared__ __align__(128) char smem[];
+  WarpSmem<D, NT>* const all = reinterpret_cast<WarpSmem<D, NT>*>(smem);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  WarpSmem<D, NT>* const ws = all + warp;
+  Rows<D, NT> s;
+  Ring ring;
+  start_warp(ws, s, ring, lane);
+  griddep_wait();
+  griddep_launch_dependents();
+  const int rt = blockIdx.x % max_row_tiles, bh = blockIdx.x / max_row_tiles;
+  const int h = bh % p.cache.heads, b = bh / p.cache.heads;
+  const Request rq = request(p, b);
+  const int row0 = rt * kRows, rows = p.G * rq.Lq;
+  if (!rq.ok) {
+    if (h == 0 && rt == 0 && threadIdx.x == 0) atomicCAS(&g_attn4_status, kDevOk, kDevBadSeqlens);
+    return;
+  }
+  if (row0 >= rows) return;
+  const int np = key_pairs(rq), each = (np + kWarps<NT> - 1) / kWarps<NT>;
+  const int first = warp * each, n = min(each, np - first);
+  // (a warp whose copy did not come leaves its part out, with the status
+  // word set: the others must not wait for it)
+  if (n > 0 && run_pairs<D, NT>(s, ring, p, rq, b, h, row0, first, n, lane))
+    end_unit<D, NT>(s, p, rq, h, row0, reinterpret_cast<float*>(ws->tiles), ws->ml, lane);
+  __syncthreads();
+  const int parts = each > 0 ? (np + each - 1) / each : 0;
+  for (int local = warp; local < kRows && row0 + local < rows; local += kWarps<NT>) {
+    const float2 ml = lane < parts ? all[lane].ml[local] : make_float2(kNoMax, 0.f);
+    float top = ml.x;
 #pragma unroll
-  for (int k = 0; k < kCols; ++k)
-    if (active) dst[k] = __float2bfloat16_rn(o[k] * f);
-  if (lane == 0) p.lse[static_cast<long long>(head) * p.total_q + tok] = l == 0.f ? -INFINITY : row_lse(top, l);
+    for (int sh = 16; sh > 0; sh >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, sh));
+    const float w = ex2_approx(ml.x - top);
+    float l = w * ml.y, o[kCols];
+#pragma unroll
+    for (int sh = 16; sh > 0; sh >>= 1) l += __shfl_xor_sync(0xffffffffu, l, sh);
+#pragma unroll
+    for (int k = 0; k < kCols; ++k) o[k] = 0.f;
+    for (int i = 0; i < parts; ++i) {
+      const float wi = __shfl_sync(0xffffffffu, w, i);
+      const float* row = reinterpret_cast<const float*>(all[i].tiles) + local * D + lane * kCols;
+#pragma unroll
+      for (int k = 0; k < kCols; ++k)
+        if (lane * kCols < D) o[k] = fmaf(wi, row[k], o[k]);
+    }
+    write_row<D>(p, rq, h, row0 + local, o, l, top, lane);
+  }
 }
 
 // 16 rows a unit when 8 would read the cache twice.
 inline bool wide_rows(long long rows) { return rows > 8; }
 
+// Units of the largest size the call allows.
+inline long long max_units(int B, int H_kv, long long max_rows) {
+  const int rows = wide_rows(max_rows) ? 16 : 8;
+  return static_cast<long long>(B) * H_kv * ((max_rows + rows - 1) / rows);
+}
+
+// One CTA per unit where every unit finds an SM and the longest request is
+// short for the number of units.  Measured, lengths from a quarter of the
+// longest to it, 128 columns, 8 rows a unit, one CTA per unit / the line in us:
+//   8 units    1024 keys  7.6 / 8.5   2048 10.7 / 8.7   4096 16.9 / 9.0
+//   64 units   1024 keys  7.9 / 11.7  2048 11.1 / 12.4  4096 17.2 / 15.4
+//   152 units  1024 keys  8.1 / 15.2  4096 17.7 / 22.8  8192 32.2 / 33.3
+//   304 units  1024 keys 14.3 / 15.8  2048 19.6 / 19.0
+// (the line spreads the bytes over all SMs but has its layout, its partial
+// results and a second launch to pay for: the few units' bound is set where
+// that launch's host time is still saved).
+inline bool one_cta_units(int B, int H_kv, long long max_rows, long long max_keys) {
+  const long long units = max_units(B, H_kv, max_rows);
+  return units <= 152 && max_keys <= (54 * units > 2048 ? 54 * units : 2048);
+}
+
 template <int D, int NT>
 int launch_attn_d(Attn4Problem p, long long max_rows, cudaStream_t st) {
   constexpr int kRows = 8 * NT, kSmem = kWarps<NT> * sizeof(WarpSmem<D, NT>);
+  const int row_tiles = static_cast<int>((max_rows + kRows - 1) / kRows);
+  const long long units = max_units(p.B, p.cache.heads, max_rows);
+  if (one_cta_units(p.B, p.cache.heads, max_rows, p.max_k)) {
+    if (int e = ensure_max_smem(reinterpret_cast<const void*>(fa2_kv4_attn_unit_kernel<D, NT>), kSmem)) return e;
+    return launch_pdl(fa2_kv4_attn_unit_kernel<D, NT>, dim3(static_cast<unsigned>(units)), dim3(kWarps<NT> * 32), kSmem, st, p,
+                      row_tiles);
+  }
   if (int e = ensure_max_smem(reinterpret_cast<const void*>(fa2_kv4_attn_kernel<D, NT>), kSmem)) return e;
   if (int e = launch_pdl(fa2_kv4_attn_kernel<D, NT>, dim3(152), dim3(kWarps<NT> * 32), kSmem, st, p)) return e;
-  const int rt = static_cast<int>((max_rows + kRows - 1) / kRows);
-  const long long units = static_cast<long long>(p.B) * p.cache.heads * rt;
   // Spans of a unit, were all requests of one length: with few, a warp joins
   // a row alone; with many, a CTA's eight do.
   if (kSpans<NT> / units < 16)
     return launch_pdl(fa2_kv4_combine_kernel<D, kRows, 1>, dim3(static_cast<unsigned>(units * (kRows / 8))), dim3(256), 0, st, p,
-                      rt);
-  return launch_pdl(fa2_kv4_combine_kernel<D, kRows, 8>, dim3(static_cast<unsigned>(units * kRows)), dim3(256), 0, st, p, rt);
+                      row_tiles);
+  return launch_pdl(fa2_kv4_combine_kernel<D, kRows, 8>, dim3(static_cast<unsigned>(units * kRows)), dim3(256), 0, st, p,
+                    row_tiles);
 }
 
 template <int D>
@@ -883,20 +992,24 @@ using namespace fa2;
 
 extern "C" {
 
-size_t fa2_kv4_attn_workspace_bytes(int B, int H, int H_kv, int max_seqlen_q, int d) {
-  if (max_seqlen_q < 1 || check_attn_sizes(B, H, H_kv, max_seqlen_q, max_seqlen_q, d) != FA2_OK) return 0;
-  const size_t rows = attn_slots(wide_rows(static_cast<long long>(H / H_kv) * max_seqlen_q));
+size_t fa2_kv4_attn_workspace_bytes(int B, int H, int H_kv, int max_seqlen_q, int max_seqlen_k, int d) {
+  if (max_seqlen_q < 1 || max_seqlen_k < 1 || check_attn_sizes(B, H, H_kv, max_seqlen_q, max_seqlen_q, d) != FA2_OK) return 0;
+  const long long max_rows = static_cast<long long>(H / H_kv) * max_seqlen_q;
+  if (one_cta_units(B, H_kv, max_rows, max_seqlen_k)) return 0;
+  const size_t rows = attn_slots(wide_rows(max_rows));
   return round_up(rows * d * sizeof(float)) + round_up(rows * sizeof(float2)) +
          round_up((static_cast<size_t>(B) + 1) * sizeof(long long));
 }
 
 int fa2_kv4_attn(const void* q, const void* cache, long long page_stride, const int* block_table, long long table_stride,
                  const int* lens, const int* cu_seqlens_q, void* o, float* lse, int B, int H, int H_kv, int total_q,
-                 int max_seqlen_q, int num_pages, int page_size, int table_width, int d, float scale, float k_scale,
-                 float v_scale, int causal, void* workspace, size_t workspace_bytes, void* stream) {
+                 int max_seqlen_q, int max_seqlen_k, int num_pages, int page_size, int table_width, int d, float scale,
+                 float k_scale, float v_scale, int causal, void* workspace, size_t workspace_bytes, void* stream) {
   if (int rc = check_attn_sizes(B, H, H_kv, total_q, max_seqlen_q, d)) return rc;
   if (int rc = check_cache(cache, page_stride, num_pages, page_size, H_kv, d)) return rc;
   if (table_width < 1 || table_width > (1 << 26) || (B > 1 && table_stride < table_width)) return FA2_ERR_SHAPE;
+  if (max_seqlen_k < 1) return FA2_ERR_SHAPE;
+  if (static_cast<long long>(table_width) * page_size < max_seqlen_k) max_seqlen_k = table_width * page_size;
   if (!cu_seqlens_q && total_q != 0 && static_cast<long long>(B) * max_seqlen_q != total_q) return FA2_ERR_SHAPE;
   if (check_scale(scale) || !power_of_two(k_scale) || !power_of_two(v_scale) || check_scale(scale * k_scale))
     return FA2_ERR_SCALE;
@@ -905,22 +1018,22 @@ int fa2_kv4_attn(const void* q, const void* cache, long long page_stride, const 
   if (!aligned(q, 16) || !aligned(o, 16) || !aligned(block_table, 4) || !aligned(lens, 4) || !aligned(cu_seqlens_q, 4) ||
       !aligned(lse, 4))
     return FA2_ERR_ALIGN;
-  const size_t need = fa2_kv4_attn_workspace_bytes(B, H, H_kv, max_seqlen_q, d);
-  if (!workspace || !aligned(workspace, kWsAlign) || workspace_bytes < need) return FA2_ERR_WORKSPACE;
+  const size_t need = fa2_kv4_attn_workspace_bytes(B, H, H_kv, max_seqlen_q, max_seqlen_k, d);
+  if (need > 0 && (!workspace || !aligned(workspace, kWsAlign) || workspace_bytes < need)) return FA2_ERR_WORKSPACE;
   const size_t qb = static_cast<size_t>(total_q) * H * d * 2;
   const size_t tb = (static_cast<size_t>(B - 1) * (B > 1 ? table_stride : 0) + table_width) * 4;
   const Range outs[] = {range_of(o, qb), range_of(lse, static_cast<size_t>(total_q) * H * 4), range_of(workspace, need)};
   const Range ins[] = {range_of(q, qb), range_of(cache, cache_span(page_stride, num_pages, page_size, H_kv, d)),
                        range_of(block_table, tb), range_of(lens, static_cast<size_t>(B) * 4),
                        range_of(cu_seqlens_q, cu_seqlens_q ? static_cast<size_t>(B + 1) * 4 : 0)};
-  for (int i = 0; i < 3; ++i) {
+  for (int i = 0; i < (need > 0 ? 3 : 2); ++i) {
     for (const Range& r : ins)
       if (r.lo != r.hi && overlap(outs[i], r)) return FA2_ERR_ALIAS;
-    for (int j = i + 1; j < 3; ++j)
+    for (int j = i + 1; j < (need > 0 ? 3 : 2); ++j)
       if (overlap(outs[i], outs[j])) return FA2_ERR_ALIAS;
   }
   const long long max_rows = static_cast<long long>(H / H_kv) * max_seqlen_q;
-  const size_t rows = attn_slots(wide_rows(max_rows));
+  const size_t rows = attn_slots(wide_rows(max_rows));  // (not touched where need is 0)
   Attn4Problem p{};
   p.q = static_cast<const __nv_bfloat16*>(q);
   p.o = static_cast<__nv_bfloat16*>(o);
@@ -944,7 +1057,7 @@ int fa2_kv4_attn(const void* q, const void* cache, long long page_stride, const 
   p.total_q = total_q;
   p.uniform_q = max_seqlen_q;
   p.max_q = max_seqlen_q;
-  p.width = table_width;
+  p.max_k = max_seqlen_k;
   p.scale_log2 = scale * k_scale * 1.44269504088896341f;
   p.v_scale = v_scale;
   p.causal = causal != 0;
