@@ -489,8 +489,8 @@ int fa2_kv4_gather(const void* cache, long long page_stride, const int* block_ta
  * j iff j <= i + Lk - Lq; a query that sees no key gets o = 0 and lse = -inf.
  * Rows outside every request are not written.  What the pages hold past a
  * request's length has no influence, not even a NaN.
- * max_seqlen_k >= 1 bounds the lengths (table_width * page_size where it is
- * larger); a tight bound lets short requests take one launch.
+ * max_seqlen_k >= 1 bounds the lengths (table_width * page_size or 2^30 where
+ * it is larger); a tight bound lets short requests take one launch.
  * A request whose lengths are out of range (negative, more than max_seqlen_k
  * tokens or than its table row has room for, query rows outside [0, total_q]
  * or more than max_seqlen_q) is skipped and the device status word becomes 3; a page id

@@ -74,7 +74,8 @@ def plan(lib, p=None, B=4, F=3, W=5, tstride=None, P=16, T=10):
 def test_cache_refusals_are_the_same_everywhere(lib):
     assert append(lib, T=0) == 0 and gather(lib, total=0) == 0 and attn(lib, tq=0, mq=0) == 0
     for f in (append, gather, attn):
-        for bad in (dict(pages=0), dict(P=8), dict(P=48), dict(P=256), dict(Hkv=0), dict(stride=100), dict(stride=1 << 50)):
+        for bad in (dict(pages=0), dict(P=8), dict(P=48), dict(P=256), dict(Hkv=0), dict(stride=100), dict(stride=1 << 50),
+                    dict(stride=-4096), dict(stride=1 << 44, pages=5)):
             assert f(lib, **bad) == 2, (f.__name__, bad)
         for d in (0, 8, 48, 96, 256):
             assert f(lib, d=d) == 3
@@ -90,6 +91,7 @@ def test_append_refusals(lib):
     for name in ("k", "v", "slots"):
         assert append(lib, **{name: None}) == 1
     assert append(lib, T=-1) == 2 and append(lib, strides=[-8, 64, 128, 64]) == 2
+    assert append(lib, strides=[1 << 44, 64, 128, 64]) == 2 and append(lib, strides=[128, 64, 128, 1 << 60]) == 2
     for bad in (dict(k=A + 8), dict(vo=6 * A + 2), dict(slots=4 * A + 4), dict(strides=[132, 64, 128, 64])):
         assert append(lib, **bad) == 4, bad
     for bad in (dict(k=3 * A), dict(ko=A), dict(ko=3 * A), dict(vo=5 * A), dict(slots=3 * A + 64)):
@@ -99,7 +101,7 @@ def test_append_refusals(lib):
 def test_gather_refusals(lib):
     for name in ("table", "cu", "k", "v"):
         assert gather(lib, **{name: None}) == 1
-    for bad in (dict(B=0), dict(total=-1), dict(W=0), dict(tstride=1)):
+    for bad in (dict(B=0), dict(total=-1), dict(W=0), dict(tstride=1), dict(tstride=1 << 50)):
         assert gather(lib, **bad) == 2, bad
     for bad in (dict(k=4 * A + 2), dict(table=2 * A + 2), dict(cu=3 * A + 1)):
         assert gather(lib, **bad) == 4, bad
@@ -111,7 +113,7 @@ def test_attention_refusals(lib):
     for name in ("q", "table", "lens", "o", "lse"):
         assert attn(lib, **{name: None}) == 1
     for bad in (dict(B=0), dict(H=0), dict(H=3), dict(tq=-1), dict(mq=0), dict(mq=9), dict(W=0), dict(tstride=1),
-                dict(cu=None, tq=7), dict(tq=(1 << 30) + 1), dict(mk=0), dict(mk=-5)):
+                dict(cu=None, tq=7), dict(tq=(1 << 30) + 1), dict(mk=0), dict(mk=-5), dict(tstride=1 << 50)):
         assert attn(lib, **bad) == 2, bad
     for s in (0.0, -0.1, float("nan"), float("inf")):
         assert attn(lib, scale=s) == 5
@@ -136,7 +138,7 @@ def test_plan_refusals(lib):
         p = [A * (j + 1) for j in range(10)]
         p[i] = None
         assert plan(lib, p) == 1, i
-    for bad in (dict(B=0), dict(B=16385), dict(F=-1), dict(W=0), dict(tstride=4), dict(P=0), dict(P=20), dict(T=-1)):
+    for bad in (dict(B=0), dict(B=16385), dict(F=-1), dict(W=0), dict(tstride=4), dict(tstride=1 << 50), dict(P=0), dict(P=20), dict(T=-1)):
         assert plan(lib, **bad) == 2, bad
     p = [A * (j + 1) for j in range(10)]
     p[7] += 4

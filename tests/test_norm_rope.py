@@ -78,6 +78,9 @@ def test_forward_refusals(lib):
     neg = own + own
     neg[0] = -8
     assert fwd(lib, strides=neg) == 2
+    far = own + own
+    far[2] = 1 << 44
+    assert fwd(lib, strides=far) == 2        # further than any memory reaches
     flat = own + own
     flat[7] = 0                              # q_out's heads on one another
     assert fwd(lib, strides=flat) == 9

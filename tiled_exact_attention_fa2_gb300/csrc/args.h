@@ -26,6 +26,12 @@ inline bool head_dim_ok(int d) { return d == 16 || d == 32 || d == 64 || d == 12
 constexpr size_t kWsAlign = 256;
 inline size_t round_up(size_t x) { return (x + kWsAlign - 1) / kWsAlign * kWsAlign; }
 
+// Whether `count` steps of `stride` (both >= 0) stay within 2^46: products of
+// sizes and strides that pass this do not overflow.
+inline bool stride_ok(long long stride, long long count) {
+  return stride >= 0 && (count <= 0 || stride <= (1LL << 46) / count);
+}
+
 // Query heads H, key/value heads Hkv (H a multiple of Hkv).
 inline int check_heads(int H, int Hkv) { return (Hkv >= 1 && Hkv <= H && H % Hkv == 0) ? FA2_OK : FA2_ERR_SHAPE; }
 

@@ -964,6 +964,8 @@ int launch_attn(const Attn4Problem& p, long long max_rows, cudaStream_t st) {
 
 size_t attn_slots(bool wide) { return wide ? static_cast<size_t>(kSpans<2>) * 2 * 16 : static_cast<size_t>(kSpans<1>) * 2 * 8; }
 
+constexpr int kMaxKeys = 1 << 30;  // of a request: positions, rounded up, in 32 bits
+
 int check_attn_sizes(int B, int H, int H_kv, int total_q, int max_q, int d) {
   if (B < 1 || H < 1 || total_q < 0 || max_q < 0 || total_q > (1 << 30) || max_q > total_q || (total_q > 0 && max_q < 1))
     return FA2_ERR_SHAPE;
@@ -993,6 +995,7 @@ using namespace fa2;
 extern "C" {
 
 size_t fa2_kv4_attn_workspace_bytes(int B, int H, int H_kv, int max_seqlen_q, int max_seqlen_k, int d) {
+  if (max_seqlen_k > kMaxKeys) max_seqlen_k = kMaxKeys;
   if (max_seqlen_q < 1 || max_seqlen_k < 1 || check_attn_sizes(B, H, H_kv, max_seqlen_q, max_seqlen_q, d) != FA2_OK) return 0;
   const long long max_rows = static_cast<long long>(H / H_kv) * max_seqlen_q;
   if (one_cta_units(B, H_kv, max_rows, max_seqlen_k)) return 0;
@@ -1007,8 +1010,9 @@ int fa2_kv4_attn(const void* q, const void* cache, long long page_stride, const 
                  float k_scale, float v_scale, int causal, void* workspace, size_t workspace_bytes, void* stream) {
   if (int rc = check_attn_sizes(B, H, H_kv, total_q, max_seqlen_q, d)) return rc;
   if (int rc = check_cache(cache, page_stride, num_pages, page_size, H_kv, d)) return rc;
-  if (table_width < 1 || table_width > (1 << 26) || (B > 1 && table_stride < table_width)) return FA2_ERR_SHAPE;
+  if (table_width < 1 || (B > 1 && (table_stride < table_width || !stride_ok(table_stride, B)))) return FA2_ERR_SHAPE;
   if (max_seqlen_k < 1) return FA2_ERR_SHAPE;
+  if (max_seqlen_k > kMaxKeys) max_seqlen_k = kMaxKeys;
   if (static_cast<long long>(table_width) * page_size < max_seqlen_k) max_seqlen_k = table_width * page_size;
   if (!cu_seqlens_q && total_q != 0 && static_cast<long long>(B) * max_seqlen_q != total_q) return FA2_ERR_SHAPE;
   if (check_scale(scale) || !power_of_two(k_scale) || !power_of_two(v_scale) || check_scale(scale * k_scale))

@@ -295,7 +295,7 @@ int check_cache(const void* cache, long long page_stride, int num_pages, int pag
   if (!head_dim_ok(d)) return FA2_ERR_HEADDIM;
   if (!cache) return FA2_ERR_NULL;
   if (H_kv > (1 << 16) || page_stride < static_cast<long long>(kv4_page_bytes(H_kv, page_size, d)) ||
-      page_stride > (1LL << 40))
+      !stride_ok(page_stride, num_pages))
     return FA2_ERR_SHAPE;
   if (!aligned(cache, 16) || page_stride % 16 != 0) return FA2_ERR_ALIGN;
   return FA2_OK;
@@ -349,8 +349,7 @@ int fa2_kv4_append(const void* k, const void* v, const long long* strides, void*
   for (int i = 0; i < 2; ++i) {
     p.token_stride[i] = num_tokens > 1 && strides ? strides[2 * i] : static_cast<long long>(H_kv) * d;
     p.head_stride[i] = H_kv > 1 && strides ? strides[2 * i + 1] : d;
-    if (p.token_stride[i] < 0 || p.head_stride[i] < 0 || p.token_stride[i] > (1LL << 40) || p.head_stride[i] > (1LL << 40))
-      return FA2_ERR_SHAPE;
+    if (!stride_ok(p.token_stride[i], num_tokens - 1) || !stride_ok(p.head_stride[i], H_kv - 1)) return FA2_ERR_SHAPE;
     if (p.token_stride[i] % 8 != 0 || p.head_stride[i] % 8 != 0) return FA2_ERR_ALIGN;
     span[i] = static_cast<size_t>((num_tokens - 1) * p.token_stride[i] + (H_kv - 1) * p.head_stride[i] + d) * 2;
   }
@@ -385,7 +384,8 @@ int fa2_kv4_gather(const void* cache, long long page_stride, const int* block_ta
                    const int* cu_seqlens, void* k, void* v, int B, int H_kv, int total, int num_pages, int page_size,
                    int table_width, int d, float k_scale, float v_scale, void* stream) {
   if (int rc = check_cache(cache, page_stride, num_pages, page_size, H_kv, d)) return rc;
-  if (B < 1 || total < 0 || total > (1 << 30) || table_width < 1 || (B > 1 && table_stride < table_width))
+  if (B < 1 || total < 0 || total > (1 << 30) || table_width < 1 ||
+      (B > 1 && (table_stride < table_width || !stride_ok(table_stride, B))))
     return FA2_ERR_SHAPE;
   if (!power_of_two(k_scale) || !power_of_two(v_scale)) return FA2_ERR_SCALE;
   if (total == 0) return FA2_OK;

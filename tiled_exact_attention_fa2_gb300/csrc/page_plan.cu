@@ -212,7 +212,7 @@ extern "C" int fa2_page_plan(const int* cached_lens, const int* new_lens, const 
                              int* pages_needed, int B, int num_free, int table_width, long long table_stride,
                              int page_size, int max_tokens, void* stream) {
   if (B < 1 || B > kMaxRequests || num_free < 0 || table_width < 1 || max_tokens < 0) return FA2_ERR_SHAPE;
-  if (B > 1 && table_stride < table_width) return FA2_ERR_SHAPE;
+  if (B > 1 && (table_stride < table_width || !stride_ok(table_stride, B))) return FA2_ERR_SHAPE;
   if (page_size != 16 && page_size != 32 && page_size != 64 && page_size != 128) return FA2_ERR_SHAPE;
   if (!cached_lens || !new_lens || !block_table || !lens || !cu_new || !cu_total || !pages_needed) return FA2_ERR_NULL;
   if ((num_free > 0 && !free_pages) || (max_tokens > 0 && (!slots || !positions))) return FA2_ERR_NULL;

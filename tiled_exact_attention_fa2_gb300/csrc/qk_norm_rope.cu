@@ -519,7 +519,7 @@ int validate_norm(const NormArgs& a, Layout* t, int count, int outs, const long 
     const long long own[3] = {static_cast<long long>(t[i].heads) * a.N * a.d, static_cast<long long>(a.N) * a.d, a.d};
     for (int j = 0; j < 3; ++j) {
       t[i].s[j] = size[j] == 1 ? own[j] : (strides ? strides[3 * i + j] : own[j]);
-      if (t[i].s[j] < 0 || t[i].s[j] > (1LL << 40)) return FA2_ERR_SHAPE;
+      if (!stride_ok(t[i].s[j], size[j] - 1)) return FA2_ERR_SHAPE;
       if (t[i].s[j] % 8 != 0) return FA2_ERR_ALIGN;
     }
     if (!aligned(t[i].p, 16)) return FA2_ERR_ALIGN;
