@@ -605,3 +605,51 @@ def test_graphs_that_share_a_workspace_and_streams():
     torch.cuda.current_stream().wait_stream(side)
     for got, w in ((a, want[0]), (b, want[1])):
         assert torch.equal(got[0], w[0]) and torch.equal(got[1], w[1])
+
+
+@pytest.mark.gpu
+def test_empty_batch_and_foreign_stream_are_refused():
+    cache = fa2.fa2_kv4_cache(2, 1, 16, 16)
+    none, table = torch.zeros(0, dtype=torch.int32, device="cuda"), torch.zeros((0, 1), dtype=torch.int32, device="cuda")
+    q = torch.zeros((0, 1, 16), dtype=torch.bfloat16, device="cuda")
+    for call in (lambda: fa2.fa2_kv4_attn(q, cache, table, none),
+                 lambda: fa2.fa2_kv4_attn(q, cache, table, none, i32([0]), 1),
+                 lambda: fa2.fa2_kv4_gather(cache, table, i32([0]), 0),
+                 lambda: fa2.fa2_page_plan(none, none, none, table, 16, 0)):
+        with pytest.raises(fa2.FA2Error):
+            call()
+    with pytest.raises(ValueError):
+        fa2._on(torch.cuda.current_device() + 1, torch.cuda.Stream())
+
+
+@pytest.mark.gpu
+def test_cache_past_32_bits():
+    """Pages beyond 4 GB and slots beyond 2^31: what is written at the far end is read there by both readers."""
+    P, d, T = 128, 16, 200
+    pages = (1 << 24) + 3  # 39 GB
+    cache = torch.empty((pages, 1, P // 16, 18 * d), dtype=torch.uint8, device="cuda")
+    table = i32([[pages - 1, (1 << 24) - 1]])
+    at = torch.arange(T, device="cuda")
+    slots = table[0].long()[at // P] * P + at % P
+    assert int(slots.max()) >= 1 << 31 and cache.numel() > 1 << 32
+    near = fa2.fa2_kv4_cache(2, 1, P, d)
+    k, v, q = (torch.randn(T, 1, d, device="cuda", generator=torch.Generator("cuda").manual_seed(i)).to(torch.bfloat16) for i in range(3))
+    fa2.fa2_device_status(reset=True)
+    plan = fa2.fa2_page_plan(i32([0]), i32([T]), table[0].contiguous(), table.clone().fill_(-1), P, T)
+    assert torch.equal(plan.slots, slots)
+    fa2.fa2_kv4_append(k, v, cache, slots)
+    fa2.fa2_kv4_append(k, v, near, at)
+    two = i32([[0, 1]])
+    for a, b in zip(fa2.fa2_kv4_gather(cache, table, i32([0, T]), T), fa2.fa2_kv4_gather(near, two, i32([0, T]), T)):
+        assert torch.equal(a, b)
+    for bound in (T, 2 ** 20):  # (the table's room is the bound where it is less: the same form)
+        got = fa2.fa2_kv4_attn(q[:4], cache, table, i32([T]), max_seqlen_k=bound)
+        want = fa2.fa2_kv4_attn(q[:4], near, two, i32([T]), max_seqlen_k=bound)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    # the line's form, which a wide table brings
+    width = 64
+    far, close = (torch.cat([t, t.new_zeros(1, width - 2)], 1) for t in (table, two))
+    assert fa2.fa2_kv4_attn_workspace_bytes(1, 1, 1, 4, width * P, d) > 0
+    got, want = fa2.fa2_kv4_attn(q[:4], cache, far, i32([T])), fa2.fa2_kv4_attn(q[:4], near, close, i32([T]))
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    assert fa2.fa2_device_status() == 0

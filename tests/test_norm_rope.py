@@ -322,3 +322,20 @@ def test_other_stream_and_graph():
         graph.replay()
         for a, b in zip(got + gotb, want + wantb):
             assert torch.equal(a, b)
+
+
+@pytest.mark.gpu
+def test_strides_past_32_bits():
+    """Rows more than 2^31 elements apart give what their contiguous copies give."""
+    B, H, N, d, far = 2, 2, 5, 64, (1 << 31) + 512
+    buf = torch.empty(2 * far, dtype=torch.bfloat16, device="cuda")
+    q, k, out_q, out_k = (buf.as_strided((B, H, N, d), (far, d, 4 * H * d, 1), i * H * d) for i in range(4))
+    q.copy_(torch.randn(B, H, N, d, device="cuda"))
+    k.copy_(torch.randn(B, H, N, d, device="cuda"))
+    w, rope = torch.rand(d, device="cuda") + 0.5, torch.randn(N, d, device="cuda")
+    want = fa2.fa2_qk_norm_rope(q.contiguous(), k.contiguous(), w, w, rope)
+    fa2.fa2_qk_norm_rope(q, k, w, w, rope, q_out=out_q, k_out=out_k)
+    assert torch.equal(out_q, want[0]) and torch.equal(out_k, want[1])
+    grads = fa2.fa2_qk_norm_rope_bwd(out_q.contiguous(), out_k.contiguous(), q.contiguous(), k.contiguous(), w, w, rope)
+    got = fa2.fa2_qk_norm_rope_bwd(out_q, out_k, q, k, w, w, rope, dq=out_q, dk=out_k)
+    assert all(torch.equal(a, b) for a, b in zip(got, grads))

@@ -601,6 +601,8 @@ class _on:
     that uses it."""
 
     def __init__(self, device, stream):
+        if isinstance(stream, torch.cuda.Stream) and stream.device_index != device:
+            raise ValueError(f"the stream belongs to cuda:{stream.device_index}, the tensors to cuda:{device}")
         self.guards = [torch.cuda.device(device)]
         if stream is not None:
             if not isinstance(stream, torch.cuda.Stream):
@@ -917,7 +919,7 @@ def fa2_kv4_attn(q, cache, block_table, lens, cu_seqlens_q=None, max_seqlen_q: O
         _ints(cu_seqlens_q, "cu_seqlens_q", dev, B + 1)
         mq = _max_len(cu_seqlens_q, max_seqlen_q)
     else:
-        mq = tq // B if max_seqlen_q is None else int(max_seqlen_q)
+        mq = tq // max(B, 1) if max_seqlen_q is None else int(max_seqlen_q)
         if mq * B != tq:
             raise ValueError("without cu_seqlens_q every request has the same number of queries")
     if o is None:
