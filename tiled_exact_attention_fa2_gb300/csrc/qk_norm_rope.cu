@@ -168,20 +168,27 @@ struct Item {
   int b, n, h0, pos, count;
 };
 
+// The item's heads, and its position as it stands in memory.
 template <int ROWS>
 __device__ __forceinline__ void place(Item& it, const NormProblem& p, int which) {
   const bool live = it.tok < p.tokens;
   it.h0 = static_cast<int>(it.chunk) * ROWS;
   it.count = live ? min(ROWS, p.heads[which] - it.h0) : 0;
   it.pos = it.n;
+  if (p.rot > 0 && p.positions && live) it.pos = __ldg(p.positions + it.tok);
+}
+// Whether the position is one; if not the item has no rows.
+__device__ __forceinline__ bool check_position(Item& it, const NormProblem& p) {
+  bool fine = true;
   if (p.rot > 0) {
-    if (p.positions && live) it.pos = __ldg(p.positions + it.tok);
-    if (live && (it.pos < 0 || it.pos >= p.max_pos)) {
+    if (it.count > 0 && (it.pos < 0 || it.pos >= p.max_pos)) {
       atomicCAS(&g_norm_status, kDevOk, kDevBadIndex);
       it.count = 0;
+      fine = false;
     }
     if (it.count == 0) it.pos = 0;
   }
+  return fine;
 }
 
 template <int ROWS>
@@ -207,7 +214,8 @@ __global__ void __launch_bounds__(256) fa2_qk_norm_rope_kernel(const NormProblem
   const int col = (threadIdx.x % kLanes) * 8;
   const int which = blockIdx.x >= p.ctas_q;
   const unsigned cta = which ? blockIdx.x - p.ctas_q : blockIdx.x;
-  const Item it = find_item<ROWS>(p, which, cta * (256u / kLanes) + threadIdx.x / kLanes);
+  Item it = find_item<ROWS>(p, which, cta * (256u / kLanes) + threadIdx.x / kLanes);
+  check_position(it, p);
   const char* src = row_at(p.x[which], it, col);
   const long long sx = 2 * p.x[which].sh;
   uint4 raw[ROWS];
@@ -257,6 +265,10 @@ __global__ void __launch_bounds__(256) fa2_qk_norm_rope_kernel(const NormProblem
   }
 }
 
+__device__ __forceinline__ void load16(uint32_t (&w)[4], uint32_t at) {
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(at) : "memory");
+}
+
 // Backward: persistent CTAs, each for q or for k (in proportion to their
 // heads), so that a lane sums dw of its 8 columns in registers over all its
 // rows; the CTA's sums are joined in shared memory and written to its own
@@ -266,6 +278,7 @@ constexpr int kBwdThreads = 128, kBwdPerSm = 5;
 template <int D, bool INTER, int ROWS>
 __global__ void __launch_bounds__(kBwdThreads, kBwdPerSm) fa2_qk_norm_rope_bwd_kernel(const NormProblem p) {
   constexpr int kLanes = D / 8, kGroups = kBwdThreads / kLanes;
+  __shared__ uint4 ring[2 * 2 * ROWS * kBwdThreads];  // [stage][row][x, dout][thread]
   __shared__ float red[kGroups][D];
   griddep_wait();
   griddep_launch_dependents();
@@ -282,37 +295,45 @@ __global__ void __launch_bounds__(kBwdThreads, kBwdPerSm) fa2_qk_norm_rope_bwd_k
 #pragma unroll
     for (int j = 0; j < 4; ++j) w[j] = f2_pack(f[2 * j], f[2 * j + 1]), dw[j] = 0;
   }
+  const uint32_t mine = smem_u32(ring) + threadIdx.x * 16;
+  constexpr uint32_t kPiece = kBwdThreads * 16, kStage = 2 * ROWS * kPiece;
+  auto fetch = [&](const Item& it, uint32_t at) {
+    const char* px = row_at(p.x[which], it, col);
+    const char* pg = row_at(p.g[which], it, col);
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) {
+      const bool there = i < it.count;
+      copy16_async(at + 2 * i * kPiece, there ? px + i * sx : px, there);
+      copy16_async(at + (2 * i + 1) * kPiece, there ? pg + i * sg : pg, there);
+    }
+  };
   // (the loop bound is the same for every lane of a warp: shuffles inside)
   const unsigned rounds = (p.items[which] + step - 1) / step;
-  Item it = find_item<ROWS>(p, which, cta * kGroups + group);
+  Item next = find_item<ROWS>(p, which, cta * kGroups + group);
+  fetch(next, mine);
+  copy_async_commit();
   // a round is `step` items further: so many tokens and chunks, sequences and tokens
   const unsigned chunks = p.chunks[which], d_tok = step / chunks, d_chunk = step - d_tok * chunks;
   const int d_b = static_cast<int>(d_tok / static_cast<unsigned>(p.N)), d_n = static_cast<int>(d_tok) - d_b * p.N;
   for (unsigned k = 0; k < rounds; ++k) {
-    if (k > 0) {
-      const unsigned c = it.chunk + d_chunk, carry = c >= chunks;
-      it.chunk = carry ? c - chunks : c;
-      it.tok += d_tok + carry;
-      it.b += d_b;
-      it.n += d_n + static_cast<int>(carry);
-      if (it.n >= p.N) {
-        it.n -= p.N;
-        ++it.b;
+    Item it = next;
+    const uint32_t at = mine + (k & 1) * kStage;
+    if (k + 1 < rounds) {
+      const unsigned c = next.chunk + d_chunk, carry = c >= chunks;
+      next.chunk = carry ? c - chunks : c;
+      next.tok += d_tok + carry;
+      next.b += d_b;
+      next.n += d_n + static_cast<int>(carry);
+      if (next.n >= p.N) {
+        next.n -= p.N;
+        ++next.b;
       }
-      place<ROWS>(it, p, which);
+      place<ROWS>(next, p, which);
+      fetch(next, mine + (~k & 1) * kStage);
     }
-    const char* px = row_at(p.x[which], it, col);
-    const char* pg = row_at(p.g[which], it, col);
+    copy_async_commit();
+    const bool fine = check_position(it, p);
     char* py = row_at(p.y[which], it, col);
-    uint4 rx[ROWS], rg[ROWS];
-#pragma unroll
-    for (int i = 0; i < ROWS; ++i) {
-      rx[i] = rg[i] = make_uint4(0, 0, 0, 0);
-      if (i < it.count) {
-        rx[i] = *reinterpret_cast<const uint4*>(px + i * sx);
-        rg[i] = *reinterpret_cast<const uint4*>(pg + i * sg);
-      }
-    }
     uint64_t c[4], s[4];
     {
       float cf[8], sf[8];
@@ -320,9 +341,13 @@ __global__ void __launch_bounds__(kBwdThreads, kBwdPerSm) fa2_qk_norm_rope_bwd_k
 #pragma unroll
       for (int j = 0; j < 4; ++j) c[j] = f2_pack(cf[2 * j], cf[2 * j + 1]), s[j] = f2_pack(sf[2 * j], sf[2 * j + 1]);
     }
+    copy_async_wait<1>();
 #pragma unroll
     for (int i = 0; i < ROWS; ++i) {
-      const uint32_t wx[4] = {rx[i].x, rx[i].y, rx[i].z, rx[i].w}, wg[4] = {rg[i].x, rg[i].y, rg[i].z, rg[i].w};
+      uint32_t wx[4], wg[4];
+      load16(wx, at + 2 * i * kPiece);
+      load16(wg, at + (2 * i + 1) * kPiece);
+      if (!fine) wx[0] = wx[1] = wx[2] = wx[3] = wg[0] = wg[1] = wg[2] = wg[3] = 0;
       uint64_t x[4], g[4], h[4], sq = 0, hx = 0;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
