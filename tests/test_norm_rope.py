@@ -339,3 +339,18 @@ def test_strides_past_32_bits():
     grads = fa2.fa2_qk_norm_rope_bwd(out_q.contiguous(), out_k.contiguous(), q.contiguous(), k.contiguous(), w, w, rope)
     got = fa2.fa2_qk_norm_rope_bwd(out_q, out_k, q, k, w, w, rope, dq=out_q, dk=out_k)
     assert all(torch.equal(a, b) for a, b in zip(got, grads))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("case", [(1, 8, 8, 7301, 128, 128, False, "bf16", "packed"),   # eight heads a group
+                                  (2, 39, 39, 3001, 32, 16, False, "fp32", "fused"),    # and a last group of seven
+                                  (2, 16, 8, 5000, 64, 64, False, "none", "bhnd")], ids=str)
+def test_forward_many_tokens(case):
+    q, k, q64, k64, four, wq, wk, w64, rope, pos, cos, sin, inter = setup(case, 13)
+    qo, ko = fa2.fa2_qk_norm_rope(q, k, wq, wk, rope, pos, eps=1e-5)
+    for got, x, w in ((qo, q64, w64[0]), (ko, k64, w64[1])):
+        want = ref.forward(x, w, cos, sin, 1e-5, inter)
+        close(four(got), want, np.abs(want).max(-1, keepdims=True), "out")
+    a, b = q.clone() if q.is_contiguous() else q, k.clone() if k.is_contiguous() else k
+    fa2.fa2_qk_norm_rope(a, b, wq, wk, rope, pos, eps=1e-5, q_out=a, k_out=b)  # in place
+    assert torch.equal(a, qo) and torch.equal(b, ko) and fa2.fa2_device_status() == 0

@@ -25,12 +25,12 @@
 //
 // Measured on a GB300 (device time): 4 x 1023 tokens x 32 heads of 64 columns
 // forward 5.8 us (5.8 TB/s); the gradient for 16384 tokens x 40 heads of 128
-// 90.6 us (5.65 TB/s, 83 % of a copy's rate; the same bytes through an
+// 87.6 us (5.84 TB/s, 86 % of a copy's rate; the same bytes through an
 // elementwise sum take 74 us), of which the sums of the gains' gradients are
-// about 3 us; 48 tokens x 40 heads 2.2 us.  The backward pass issues about
-// 0.6 instructions a cycle and scheduler: what is left is neither memory nor
-// issue alone (24 warps an SM with spills or 16 with the next item's loads in
-// flight were slower than 20 without either).
+// about 3 us, forward 53.9 us (6.2 TB/s, 92 %); 48 tokens x 40 heads 2.2 us.
+// A form of the gradient with 16 columns a lane took 84 of its 89.5 us without
+// its arithmetic (loads, one addition, stores): what is left is how the rows
+// come and go, not what is done with them.
 //
 // All sums and the arithmetic are fp32; the one rounding to bf16 is at the
 // store.
@@ -207,7 +207,7 @@ __device__ __forceinline__ char* row_at(const View& v, const Item& it, int col) 
 }
 
 template <int D, bool INTER, int ROWS>
-__global__ void __launch_bounds__(256) fa2_qk_norm_rope_kernel(const NormProblem p) {
+__global__ void __launch_bounds__(256, ROWS == 8 ? 3 : 0) fa2_qk_norm_rope_kernel(const NormProblem p) {
   constexpr int kLanes = D / 8;
   griddep_wait();
   griddep_launch_dependents();
@@ -273,7 +273,11 @@ __device__ __forceinline__ void load16(uint32_t (&w)[4], uint32_t at) {
 // heads), so that a lane sums dw of its 8 columns in registers over all its
 // rows; the CTA's sums are joined in shared memory and written to its own
 // slot, which the dw kernel adds up in a fixed order (the result does not
-// depend on the order CTAs run in).
+// depend on the order CTAs run in).  The next item's rows are on their way
+// into shared memory, each thread's own pieces, while this one's are worked
+// on, so no registers wait for memory (without this 90.6 us; 20 warps an SM
+// with it, since 16 columns a lane, three stages, the angles fetched the same
+// way or the partners read from shared memory all cost more: 89-116).
 constexpr int kBwdThreads = 128, kBwdPerSm = 5;
 template <int D, bool INTER, int ROWS>
 __global__ void __launch_bounds__(kBwdThreads, kBwdPerSm) fa2_qk_norm_rope_bwd_kernel(const NormProblem p) {
@@ -412,12 +416,26 @@ __global__ void __launch_bounds__(1024) fa2_qk_norm_dw_kernel(const float* __res
   if (lane == 0 && blockIdx.x * 32 + warp < d) out[blockIdx.x * 32 + warp] = s;
 }
 
+
 constexpr int kBwdCtas = 152 * kBwdPerSm;  // one wave
 // From this many lane groups of four heads on, four heads a group fill the
 // GPU (152 SMs, 512 threads each); below, one head a group gives shorter
 // chains of loads.
 inline bool many(long long tokens, int heads, int d) {
   return tokens * ((heads + 3) / 4) * (d / 8) >= 152LL * 512;
+}
+
+// Heads a lane group of the forward pass takes.  With eight the angles and
+// the addresses are made half as often: of half-split pairs, 128 columns, 53.9
+// against 57.0 us for 16384 tokens x 40 heads, 15.9 / 16.8 for 4096, 9.7 / 9.6
+// for 2048 (1.4 rounds of CTAs: so from two rounds on, and where at most one
+// head in nine of the groups is missing); interleaved pairs, whose angles are
+// half the bytes, gain nothing (54.6 / 54.4), rows of 16 columns neither.
+template <int D, bool INTER>
+int forward_rows(long long tokens, int hq, int hk) {
+  if (!many(tokens, hq + hk, D)) return 1;
+  const long long groups = (hq + 7) / 8 + (hk + 7) / 8;
+  return !INTER && D >= 32 && 9 * (hq + hk) >= 64 * groups && tokens * groups * (D / 8) >= 152LL * 3 * 256 * 2 ? 8 : 4;
 }
 
 // Items of `rows` heads, and the CTAs they fill.
@@ -433,13 +451,15 @@ void divide(NormProblem* p, long long tokens, int rows, int d, int threads, unsi
 
 template <int D, bool INTER>
 int launch_fwd_d(NormProblem p, long long tokens, cudaStream_t st) {
-  const bool big = many(tokens, p.heads[0] + p.heads[1], D);
+  const int rows = forward_rows<D, INTER>(tokens, p.heads[0], p.heads[1]);
   unsigned ctas[2];
-  divide(&p, tokens, big ? 4 : 1, D, 256, ctas);
+  divide(&p, tokens, rows, D, 256, ctas);
   p.ctas_q = ctas[0];
   const dim3 grid(ctas[0] + ctas[1]);
-  return big ? launch_pdl(fa2_qk_norm_rope_kernel<D, INTER, 4>, grid, dim3(256), 0, st, p)
-             : launch_pdl(fa2_qk_norm_rope_kernel<D, INTER, 1>, grid, dim3(256), 0, st, p);
+  if constexpr (!INTER && D >= 32)
+    if (rows == 8) return launch_pdl(fa2_qk_norm_rope_kernel<D, INTER, 8>, grid, dim3(256), 0, st, p);
+  return rows == 4 ? launch_pdl(fa2_qk_norm_rope_kernel<D, INTER, 4>, grid, dim3(256), 0, st, p)
+                   : launch_pdl(fa2_qk_norm_rope_kernel<D, INTER, 1>, grid, dim3(256), 0, st, p);
 }
 
 template <int D, bool INTER>
