@@ -497,8 +497,8 @@ int fa2_kv4_gather(const void* cache, long long page_stride, const int* block_ta
  * outside [0, num_pages) leaves its keys out and sets 5.
  * workspace: 256-byte aligned, fa2_kv4_attn_workspace_bytes(...) bytes for the
  * same sizes (max_seqlen_k not above the table's room), whatever it holds; NULL
- * where that is 0: small calls (few key/value heads and rows of short
- * requests) need none and take one launch, others two.  (It is 0 for invalid
+ * where that is 0: calls of short requests (max_seqlen_k up to 1024 or 2048,
+ * for many rows or few) need none and take one launch, others two.  (It is 0 for invalid
  * sizes as well.)  Results do not vary from run to run.  total_q = 0 is
  * allowed and does nothing.
  */

@@ -121,12 +121,15 @@ def test_attention_refusals(lib):
         assert attn(lib, **bad) == 4, bad
     for bad in (dict(o=A), dict(o=2 * A), dict(lse=6 * A), dict(lse=4 * A)):
         assert attn(lib, **bad) == 9, bad
-    # tables of more than 2048 keys, or more than 152 units: two launches and a workspace
+    # tables of more than 2048 keys: two launches and a workspace
     need = lib.fa2_kv4_attn_workspace_bytes(2, 4, 2, 4, 129 * 16, 64)
     assert need > 0 and attn(lib, W=129, ws=None) == 8 and attn(lib, W=129, ws=8 * A + 16) == 8
     assert attn(lib, W=129, wsb=need - 1) == 8 and attn(lib, W=129, ws=A) == 9 and attn(lib, W=129, ws=2 * A) == 9
     ws = lib.fa2_kv4_attn_workspace_bytes
-    assert ws(77, 4, 2, 4, 32, 64) > 0 and ws(76, 4, 2, 4, 32, 64) == 0 and ws(1, 4, 2, 4, 2048, 64) == 0
+    assert ws(76, 4, 2, 4, 32, 64) == 0 and ws(1, 4, 2, 4, 2048, 64) == 0
+    assert ws(77, 4, 2, 4, 2048, 64) == 0 and ws(77, 4, 2, 4, 2049, 64) > 0  # more units than SMs
+    assert ws(77, 4, 2, 8, 1024, 64) == 0 and ws(77, 4, 2, 8, 1025, 64) > 0  # of 16 rows
+    assert ws(609, 4, 2, 4, 128, 64) == 0 and ws(609, 4, 2, 4, 127, 64) > 0 and ws(608, 4, 2, 4, 1, 64) == 0
     assert ws(76, 4, 2, 4, 54 * 152, 64) == 0 and ws(76, 4, 2, 4, 54 * 152 + 1, 64) > 0
     assert attn(lib, W=129, mk=2048, ws=None, o=A) == 9  # (a tight bound: no workspace asked for)
     for bad in ((0, 4, 2, 1, 99, 64), (1, 4, 3, 1, 99, 64), (1, 4, 2, 0, 99, 64), (1, 4, 2, 1, 0, 64), (1, 4, 2, 1, 99999, 60)):
@@ -653,3 +656,44 @@ def test_cache_past_32_bits():
     got, want = fa2.fa2_kv4_attn(q[:4], cache, far, i32([T])), fa2.fa2_kv4_attn(q[:4], near, close, i32([T]))
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
     assert fa2.fa2_device_status() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("B,n,H,Hkv,nq,d,P", [(90, 350, 4, 2, 1, 128, 16), (23, 800, 16, 8, 1, 64, 64), (40, 70, 16, 4, 5, 32, 32),
+                                              (17, 1000, 30, 10, 7, 128, 128), (160, 40, 1, 1, 2, 16, 16)])
+def test_attention_more_units_than_sms(B, n, H, Hkv, nq, d, P):
+    """Many units of short requests: a small CTA each, or (by the bound on the lengths alone) many units in a span."""
+    rng = np.random.default_rng(n)
+    lens = [n, 0, 1, 31, 33] + [int(x) for x in rng.integers(0, n, B - 5)]
+    nqs = [nq] * (B - 3) + [0, 1, nq]
+    cache, table, kv = filled(rng, lens, Hkv, P, d, width=4096 // P)
+    cu = np.r_[0, np.cumsum(nqs)]
+    total = int(cu[-1])
+    q = torch.from_numpy(rng.standard_normal((total, H, d))).to(torch.bfloat16).cuda()
+    rows = [(int(cu[b]), int(cu[b + 1])) for b in range(B)]
+    fa2.fa2_device_status(reset=True)
+    for bound in (n, None):
+        assert (fa2.fa2_kv4_attn_workspace_bytes(B, H, Hkv, nq, bound or table.shape[1] * P, d) > 0) == (bound is None)
+        for causal in (True, False):
+            o, lse = fa2.fa2_kv4_attn(q, cache, i32(table), i32(lens), i32(cu), nq, max_seqlen_k=bound, causal=causal)
+            check_attention(o, lse, rows, q.double().cpu().numpy(), kv, 1 / math.sqrt(d), causal, H)
+            again = fa2.fa2_kv4_attn(q, cache, i32(table), i32(lens), i32(cu), nq, max_seqlen_k=bound, causal=causal)
+            assert torch.equal(again[0], o) and torch.equal(again[1], lse)
+    assert fa2.fa2_device_status() == 0
+    # a length past the bound and a page that does not exist: reported, the other requests as before
+    at = lens.index(max(lens[5:-3]), 5)
+    o, lse = fa2.fa2_kv4_attn(q, cache, i32(table), i32(lens), i32(cu), nq, max_seqlen_k=n)
+    bad = list(lens)
+    bad[at] = n + 1
+    o2, lse2 = torch.full_like(o, 9.0), torch.full_like(lse, 9.0)
+    fa2.fa2_kv4_attn(q, cache, i32(table), i32(bad), i32(cu), nq, max_seqlen_k=n, o=o2, lse=lse2)
+    assert fa2.fa2_device_status(reset=True) == 3
+    mine = torch.zeros(total, dtype=torch.bool, device="cuda")
+    mine[rows[at][0]:rows[at][1]] = True
+    assert torch.all(o2[mine] == 9) and torch.all(lse2[:, mine] == 9)
+    assert torch.equal(o2[~mine], o[~mine]) and torch.equal(lse2[:, ~mine], lse[:, ~mine])
+    missing = table.copy()
+    missing[at, 0] = cache.shape[0]
+    o3, lse3 = fa2.fa2_kv4_attn(q, cache, i32(missing), i32(lens), i32(cu), nq, max_seqlen_k=n)
+    assert fa2.fa2_device_status(reset=True) == 5
+    assert torch.equal(o3[~mine], o[~mine]) and torch.equal(lse3[:, ~mine], lse[:, ~mine])

@@ -17,9 +17,9 @@
 // A unit inside one span is finished by its warp; one that spans share leaves
 // a partial result per span (unnormalised O, running maximum and sum), which
 // the combine kernel joins in span order.  Warps share nothing, so there are
-// no barriers, and the result does not depend on the order they run in.  Few
-// units of short requests take one CTA each instead, whose warps share the
-// unit's keys and join in shared memory.
+// no barriers, and the result does not depend on the order they run in.  Units
+// of short requests take one CTA each instead, whose warps share the unit's
+// keys and join in shared memory.
 //
 // Operands (lane (g, c) = (lane / 4, lane % 4)).  The first product is
 // S^T = K Q^T: a tile's 16 keys are the rows of the instruction and the 8
@@ -74,6 +74,7 @@ template <int NT>
 constexpr int kWarps = NT == 1 ? 16 : 12;
 template <int NT>
 constexpr int kSpans = 152 * kWarps<NT>;  // one wave
+constexpr int kFew = 4;  // warps of a CTA that takes one of many short units
 constexpr float kNoMax = -1.7e38f;  // running maximum of a row that has seen no key (finite: no inf - inf)
 constexpr float kLift = 11.f;   // weights are held 2^11 up
 constexpr float kLag = 4.f;     // a score may pass the running maximum by 2^4
@@ -858,11 +859,11 @@ __global__ void __launch_bounds__(256) fa2_kv4_combine_kernel(const Attn4Problem
   write_row<D>(p, rq, h, r, o, l, top, lane);
 }
 
-// Short requests: one CTA per unit, whose warps take equal parts of its keys
-// and join their partial results in shared memory, in the order of the keys:
-// one launch, no line to lay out first, no workspace.
-template <int D, int NT>
-__global__ void __launch_bounds__(kWarps<NT> * 32, 1) fa2_kv4_attn_unit_kernel(const Attn4Problem p, int max_row_tiles) {
+// Short requests: one CTA of W warps per unit, which take equal parts of its
+// keys and join their partial results in shared memory, in the order of the
+// keys: one launch, no line to lay out first, no workspace.
+template <int D, int NT, int W>
+__global__ void __launch_bounds__(W * 32, kWarps<NT> / W) fa2_kv4_attn_unit_kernel(const Attn4Problem p, int max_row_tiles) {
   constexpr int kRows = 8 * NT, kCols = D >= 32 ? D / 32 : 1;
   extern __shared__ __align__(128) char smem[];
   WarpSmem<D, NT>* const all = reinterpret_cast<WarpSmem<D, NT>*>(smem);
@@ -882,15 +883,15 @@ __global__ void __launch_bounds__(kWarps<NT> * 32, 1) fa2_kv4_attn_unit_kernel(c
     return;
   }
   if (row0 >= rows) return;
-  const int np = key_pairs(rq), each = (np + kWarps<NT> - 1) / kWarps<NT>;
+  const int np = key_pairs(rq), each = (np + W - 1) / W;
   const int first = warp * each, n = min(each, np - first);
-  // (a warp whose copy did not come leaves its part out, with the status
-  // word set: the others must not wait for it)
+  // (a warp whose copy did not come leaves the unit's rows wrong, with the
+  // status word set: the others must not wait for it)
   if (n > 0 && run_pairs<D, NT>(s, ring, p, rq, b, h, row0, first, n, lane))
     end_unit<D, NT>(s, p, rq, h, row0, reinterpret_cast<float*>(ws->tiles), ws->ml, lane);
   __syncthreads();
   const int parts = each > 0 ? (np + each - 1) / each : 0;
-  for (int local = warp; local < kRows && row0 + local < rows; local += kWarps<NT>) {
+  for (int local = warp; local < kRows && row0 + local < rows; local += W) {
     const float2 ml = lane < parts ? all[lane].ml[local] : make_float2(kNoMax, 0.f);
     float top = ml.x;
 #pragma unroll
@@ -921,19 +922,30 @@ inline long long max_units(int B, int H_kv, long long max_rows) {
   return static_cast<long long>(B) * H_kv * ((max_rows + rows - 1) / rows);
 }
 
-// One CTA per unit where every unit finds an SM and the longest request is
-// short for the number of units.  Measured, lengths from a quarter of the
-// longest to it, 128 columns, 8 rows a unit, one CTA per unit / the line in us:
-//   8 units    1024 keys  7.6 / 8.5   2048 10.7 / 8.7   4096 16.9 / 9.0
-//   64 units   1024 keys  7.9 / 11.7  2048 11.1 / 12.4  4096 17.2 / 15.4
-//   152 units  1024 keys  8.1 / 15.2  4096 17.7 / 22.8  8192 32.2 / 33.3
-//   304 units  1024 keys 14.3 / 15.8  2048 19.6 / 19.0
+// Warps of a CTA where each unit takes a CTA, 0 where the line is cut instead.
+// One unit a SM: a full CTA, where the longest request is short for the number
+// of units.  More units than SMs: kFew warps, of which three or four CTAs share
+// an SM, where the longest request is short.  Measured, lengths from a quarter
+// of the longest to it, 128 columns, a full CTA / kFew warps / the line in us:
+//   8 rows a unit:
+//   8 units     1024 keys   7.8 / 9.4 / 8.6     2048  11.0 / 15.3 / 8.9   4096  17.1 / 26.8 / 9.3
+//   64 units    1024 keys   8.1 / 9.8 / 11.7    2048  11.3 / 15.7 / 12.3  4096  17.5 / 27.4 / 15.4
+//   152 units   1024 keys   8.4 / 10.1 / 15.3   4096  19.7 / 28.3 / 24.0  8192  32.6 / 52.0 / 32.0
+//   304 units    128 keys   9.5 / 5.6 / 11.3    2048  23.4 / 20.2 / 21.9  4096  35.7 / 34.8 / 30.3
+//   2432 units   128 keys  66.5 / 22.1 / 28.0   2048 147.1 / 91.4 / 93.2  4096 213.7 / 158.9 / 153.4
+//   16 rows a unit:
+//   304 units    128 keys  14.8 / 10.2 / 16.4   1024  23.5 / 21.2 / 24.4  2048  35.5 / 35.3 / 32.1
+//   760 units    128 keys  34.7 / 18.5 / 22.6   1024  53.5 / 37.7 / 40.6  2048  71.6 / 55.1 / 53.1
+//   3040 units    32 keys 116.5 / 50.0 / 31.7    128 126.3 / 59.8 / 59.8  1024 212.9 / 118.2 / 123.6
 // (the line spreads the bytes over all SMs but has its layout, its partial
 // results and a second launch to pay for: the few units' bound is set where
-// that launch's host time is still saved).
-inline bool one_cta_units(int B, int H_kv, long long max_rows, long long max_keys) {
+// that launch's host time is still saved.  Very many units of a few keys leave
+// most of a CTA's warps without any.)
+inline int unit_warps(int B, int H_kv, long long max_rows, long long max_keys) {
   const long long units = max_units(B, H_kv, max_rows);
-  return units <= 152 && max_keys <= (54 * units > 2048 ? 54 * units : 2048);
+  const bool wide = wide_rows(max_rows);
+  if (units <= 152) return max_keys <= (54 * units > 2048 ? 54 * units : 2048) ? (wide ? kWarps<2> : kWarps<1>) : 0;
+  return max_keys <= (wide ? 1024 : 2048) && (units <= 152 * 8 || max_keys >= 128) ? kFew : 0;
 }
 
 template <int D, int NT>
@@ -941,10 +953,11 @@ int launch_attn_d(Attn4Problem p, long long max_rows, cudaStream_t st) {
   constexpr int kRows = 8 * NT, kSmem = kWarps<NT> * sizeof(WarpSmem<D, NT>);
   const int row_tiles = static_cast<int>((max_rows + kRows - 1) / kRows);
   const long long units = max_units(p.B, p.cache.heads, max_rows);
-  if (one_cta_units(p.B, p.cache.heads, max_rows, p.max_k)) {
-    if (int e = ensure_max_smem(reinterpret_cast<const void*>(fa2_kv4_attn_unit_kernel<D, NT>), kSmem)) return e;
-    return launch_pdl(fa2_kv4_attn_unit_kernel<D, NT>, dim3(static_cast<unsigned>(units)), dim3(kWarps<NT> * 32), kSmem, st, p,
-                      row_tiles);
+  if (const int w = unit_warps(p.B, p.cache.heads, max_rows, p.max_k)) {
+    const auto kernel = w == kFew ? fa2_kv4_attn_unit_kernel<D, NT, kFew> : fa2_kv4_attn_unit_kernel<D, NT, kWarps<NT>>;
+    const int smem = w * static_cast<int>(sizeof(WarpSmem<D, NT>));
+    if (int e = ensure_max_smem(reinterpret_cast<const void*>(kernel), smem)) return e;
+    return launch_pdl(kernel, dim3(static_cast<unsigned>(units)), dim3(w * 32), smem, st, p, row_tiles);
   }
   if (int e = ensure_max_smem(reinterpret_cast<const void*>(fa2_kv4_attn_kernel<D, NT>), kSmem)) return e;
   if (int e = launch_pdl(fa2_kv4_attn_kernel<D, NT>, dim3(152), dim3(kWarps<NT> * 32), kSmem, st, p)) return e;
@@ -998,7 +1011,7 @@ size_t fa2_kv4_attn_workspace_bytes(int B, int H, int H_kv, int max_seqlen_q, in
   if (max_seqlen_k > kMaxKeys) max_seqlen_k = kMaxKeys;
   if (max_seqlen_q < 1 || max_seqlen_k < 1 || check_attn_sizes(B, H, H_kv, max_seqlen_q, max_seqlen_q, d) != FA2_OK) return 0;
   const long long max_rows = static_cast<long long>(H / H_kv) * max_seqlen_q;
-  if (one_cta_units(B, H_kv, max_rows, max_seqlen_k)) return 0;
+  if (unit_warps(B, H_kv, max_rows, max_seqlen_k)) return 0;
   const size_t rows = attn_slots(wide_rows(max_rows));
   return round_up(rows * d * sizeof(float)) + round_up(rows * sizeof(float2)) +
          round_up((static_cast<size_t>(B) + 1) * sizeof(long long));
