@@ -354,3 +354,13 @@ def test_forward_many_tokens(case):
     a, b = q.clone() if q.is_contiguous() else q, k.clone() if k.is_contiguous() else k
     fa2.fa2_qk_norm_rope(a, b, wq, wk, rope, pos, eps=1e-5, q_out=a, k_out=b)  # in place
     assert torch.equal(a, qo) and torch.equal(b, ko) and fa2.fa2_device_status() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("case", [(1, 4, 1, 3001, 32, 32, False, "bf16", "packed"), (2, 2, 2, 1500, 128, 96, True, "fp32", "fused"),
+                                  (3, 2, 1, 700, 64, 32, False, "fp32", "bhnd"), (1, 5, 1, 9001, 16, 16, True, "bf16", "packed"),
+                                  (1, 1, 1, 9000, 128, 128, False, "bf16", "packed")], ids=str)
+def test_few_heads(case):
+    """Groups of two heads, and groups with rows missing, over many tokens."""
+    test_forward(case)
+    test_backward(case)

@@ -418,24 +418,35 @@ __global__ void __launch_bounds__(1024) fa2_qk_norm_dw_kernel(const float* __res
 
 
 constexpr int kBwdCtas = 152 * kBwdPerSm;  // one wave
-// From this many lane groups of four heads on, four heads a group fill the
-// GPU (152 SMs, 512 threads each); below, one head a group gives shorter
-// chains of loads.
-inline bool many(long long tokens, int heads, int d) {
-  return tokens * ((heads + 3) / 4) * (d / 8) >= 152LL * 512;
-}
+// Rows of q and k that lane groups of `rows` heads have room for, per token.
+inline long long room(int hq, int hk, int rows) { return rows * ((hq + rows - 1LL) / rows + (hk + rows - 1) / rows); }
 
-// Heads a lane group of the forward pass takes.  With eight the angles and
-// the addresses are made half as often: of half-split pairs, 128 columns, 53.9
-// against 57.0 us for 16384 tokens x 40 heads, 15.9 / 16.8 for 4096, 9.7 / 9.6
-// for 2048 (1.4 rounds of CTAs: so from two rounds on, and where at most one
-// head in nine of the groups is missing); interleaved pairs, whose angles are
-// half the bytes, gain nothing (54.6 / 54.4), rows of 16 columns neither.
+// Heads a lane group of the forward pass takes: one where the call is small
+// (shorter chains of loads: 0.3 million elements 2.1 us against 2.5 with four,
+// 1 million 3.3 / 2.7) or nearly all rows of a group would be missing, else
+// four.  With eight the angles and the addresses are made half as often: of
+// half-split pairs, 128 columns, 53.9 against 57.0 us for 16384 tokens x 40
+// heads, 15.9 / 16.8 for 4096, 9.7 / 9.6 for 2048 (1.4 rounds of CTAs: so from
+// two rounds on, and where at most one row in nine is missing); interleaved
+// pairs, whose angles are half the bytes, gain nothing (54.6 / 54.4), rows of
+// 16 columns neither.
 template <int D, bool INTER>
 int forward_rows(long long tokens, int hq, int hk) {
-  if (!many(tokens, hq + hk, D)) return 1;
-  const long long groups = (hq + 7) / 8 + (hk + 7) / 8;
-  return !INTER && D >= 32 && 9 * (hq + hk) >= 64 * groups && tokens * groups * (D / 8) >= 152LL * 3 * 256 * 2 ? 8 : 4;
+  const int n = hq + hk;
+  if (tokens * n * D < 152 * 4096 || room(hq, hk, 4) >= 3 * n) return 1;
+  return !INTER && D >= 32 && 8 * room(hq, hk, 8) <= 9 * n && tokens * room(hq, hk, 8) * D >= 152LL * 3 * 256 * 2 * 64 ? 8 : 4;
+}
+
+// The same for the gradient.  Measured, 128 columns, one / two / four heads a
+// group in us: 0.1 million elements of 32 + 8 heads 4.0 / 3.7 / 3.8, 0.3
+// million 5.0 / 4.6 / 4.3, 40 million 66.7 / 50.4 / 45.3; 40 million of 4 + 1
+// heads 70.2 / 59.1 / 60.9, 2 + 2 69.4 / 53.6 / 72.4, 2 + 1 69.9 / 64.6 / 93.9:
+// with four the missing rows cost the most.
+inline int backward_rows(long long tokens, int hq, int hk, int d) {
+  const int n = hq + hk;
+  if (tokens * n * d < 152 * 1024) return 1;
+  if (5 * room(hq, hk, 4) <= 6 * room(hq, hk, 2)) return 4;
+  return 2 * room(hq, hk, 2) < 3 * n ? 2 : 1;
 }
 
 // Items of `rows` heads, and the CTAs they fill.
@@ -464,9 +475,9 @@ int launch_fwd_d(NormProblem p, long long tokens, cudaStream_t st) {
 
 template <int D, bool INTER>
 int launch_bwd_d(NormProblem p, long long tokens, float* dwq, float* dwk, cudaStream_t st) {
-  const bool big = many(tokens, p.heads[0] + p.heads[1], D);
+  const int rows = backward_rows(tokens, p.heads[0], p.heads[1], D);
   unsigned ctas[2];
-  divide(&p, tokens, big ? 4 : 1, D, kBwdThreads, ctas);
+  divide(&p, tokens, rows, D, kBwdThreads, ctas);
   if (ctas[0] + ctas[1] > kBwdCtas) {  // q's and k's shares of the persistent CTAs
     const unsigned q = static_cast<unsigned>(static_cast<unsigned long long>(kBwdCtas) * p.items[0] /
                                              (static_cast<unsigned long long>(p.items[0]) + p.items[1]));
@@ -475,8 +486,10 @@ int launch_bwd_d(NormProblem p, long long tokens, float* dwq, float* dwk, cudaSt
   }
   p.ctas_q = ctas[0];
   const unsigned grid = ctas[0] + ctas[1];
-  int e = big ? launch_pdl(fa2_qk_norm_rope_bwd_kernel<D, INTER, 4>, dim3(grid), dim3(kBwdThreads), 0, st, p)
-              : launch_pdl(fa2_qk_norm_rope_bwd_kernel<D, INTER, 1>, dim3(grid), dim3(kBwdThreads), 0, st, p);
+  const auto kernel = rows == 4   ? fa2_qk_norm_rope_bwd_kernel<D, INTER, 4>
+                      : rows == 2 ? fa2_qk_norm_rope_bwd_kernel<D, INTER, 2>
+                                  : fa2_qk_norm_rope_bwd_kernel<D, INTER, 1>;
+  const int e = launch_pdl(kernel, dim3(grid), dim3(kBwdThreads), 0, st, p);
   if (e || !p.partial) return e;
   return launch_pdl(fa2_qk_norm_dw_kernel, dim3((D + 31) / 32, 2), dim3(1024), 0, st, static_cast<const float*>(p.partial),
                     static_cast<int>(ctas[0]), static_cast<int>(grid), D, dwq, dwk);
