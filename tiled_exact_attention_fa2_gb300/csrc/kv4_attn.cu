@@ -229,10 +229,11 @@ __device__ __forceinline__ void start_unit(Rows<D, NT>& s, const Attn4Problem& p
   const int g = lane >> 2, c = lane & 3;
   const int rows = p.G * rq.Lq;
   s.min_vis = rq.Lk;
+  uint32_t raw[NT][kPer / 2];
 #pragma unroll
-  for (int j = 0; j < NT; ++j) {
+  for (int j = 0; j < NT; ++j) {  // (all rows' loads at once)
     const int r = row0 + 8 * j + g;
-    uint32_t w[kPer / 2];
+    uint32_t (&w)[kPer / 2] = raw[j];
 #pragma unroll
     for (int i = 0; i < kPer / 2; ++i) w[i] = 0;
     if (r < rows) {
@@ -250,6 +251,10 @@ __device__ __forceinline__ void start_unit(Rows<D, NT>& s, const Attn4Problem& p
         w[0] = u.x, w[1] = u.y;
       }
     }
+  }
+#pragma unroll
+  for (int j = 0; j < NT; ++j) {
+    uint32_t (&w)[kPer / 2] = raw[j];
     // the power of two at or below the row's largest magnitude (1 for a row
     // of zeros, infinities or NaN)
     float mx = 0.f;
