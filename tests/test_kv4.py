@@ -697,3 +697,26 @@ def test_attention_more_units_than_sms(B, n, H, Hkv, nq, d, P):
     o3, lse3 = fa2.fa2_kv4_attn(q, cache, i32(missing), i32(lens), i32(cu), nq, max_seqlen_k=n)
     assert fa2.fa2_device_status(reset=True) == 5
     assert torch.equal(o3[~mine], o[~mine]) and torch.equal(lse3[:, ~mine], lse[:, ~mine])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("B", [512, 513, 4096, 4097, 16384])
+def test_plan_at_the_sizes_where_its_layout_changes(B):
+    test_plan(B, 16, 40, 3)
+    rng = np.random.default_rng(B)
+    cached, new = rng.integers(0, 40, B), rng.integers(0, 4, B)
+    bad = rng.choice(B, 7, replace=False)
+    odd = cached.copy()
+    odd[bad] = [-1, -2 ** 31, 2 ** 31 - 1, 65, 64, -5, 1000]
+    cached[bad] = 0
+    fewer, more = new.copy(), new.copy()
+    fewer[bad], more[bad] = 0, 1
+    free = i32(np.arange(4 * B))
+    T = int(fewer.sum())
+    fa2.fa2_device_status(reset=True)
+    tables = [torch.full((B, 4), -7, dtype=torch.int32, device="cuda") for _ in range(2)]
+    want = fa2.fa2_page_plan(i32(cached), i32(fewer), free, tables[0], 16, T)
+    assert fa2.fa2_device_status() == 0
+    got = fa2.fa2_page_plan(i32(odd), i32(more), free, tables[1], 16, T)
+    assert fa2.fa2_device_status(reset=True) == 3
+    assert all(torch.equal(a, b) for a, b in zip(got, want)) and torch.equal(*tables)
