@@ -13,6 +13,7 @@ from __future__ import annotations
 import ctypes
 import math
 import os
+import struct
 from typing import NamedTuple, Optional, Tuple
 
 import torch
@@ -37,7 +38,6 @@ _i = ctypes.c_int
 _f = ctypes.c_float
 _sz = ctypes.c_size_t
 _ll = ctypes.c_longlong
-_llp = ctypes.POINTER(_ll)
 
 _SIGNATURES = {
     "fa2_fwd": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _f, _i, _vp]),
@@ -77,13 +77,13 @@ _SIGNATURES = {
     "fa2_bwd_varlen_workspace_bytes": (_sz, [_i, _i, _i]),
     "fa2_bwd_varlen": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _i,
                             _f, _i, _vp, _sz, _vp]),
-    "fa2_qk_norm_rope": (_i, [_vp, _vp, _vp, _vp, _i, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _i, _f, _llp, _vp]),
+    "fa2_qk_norm_rope": (_i, [_vp, _vp, _vp, _vp, _i, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _i, _f, _vp, _vp]),
     "fa2_qk_norm_rope_bwd_workspace_bytes": (_sz, [_i]),
     "fa2_qk_norm_rope_bwd": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _i, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i,
-                                  _i, _i, _f, _llp, _vp, _sz, _vp]),
+                                  _i, _i, _f, _vp, _vp, _sz, _vp]),
     "fa2_page_plan": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _ll, _i, _i, _vp]),
     "fa2_kv4_page_bytes": (_sz, [_i, _i, _i]),
-    "fa2_kv4_append": (_i, [_vp, _vp, _llp, _vp, _ll, _vp, _vp, _vp, _i, _i, _i, _i, _i, _f, _f, _vp]),
+    "fa2_kv4_append": (_i, [_vp, _vp, _vp, _vp, _ll, _vp, _vp, _vp, _i, _i, _i, _i, _i, _f, _f, _vp]),
     "fa2_kv4_gather": (_i, [_vp, _ll, _vp, _ll, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _f, _f, _vp]),
     "fa2_kv4_attn_workspace_bytes": (_sz, [_i, _i, _i, _i, _i, _i]),
     "fa2_kv4_attn": (_i, [_vp, _vp, _ll, _vp, _ll, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _i, _i, _i, _f, _f, _f,
@@ -593,7 +593,8 @@ def fa2_step_from_host(host: dict, causal: bool = True, scale: Optional[float] =
 # stream handle comes from torch without a Stream object.
 _raw_stream = torch._C._cuda_getCurrentRawStream
 _current_device = torch._C._cuda_getDevice
-_LL4, _LL12, _LL18 = _ll * 4, _ll * 12, _ll * 18
+# A host array of strides, as the bytes of C's long longs (made in a third of the time of a ctypes array).
+_pack4, _pack12, _pack18 = (struct.Struct(f"{n}q").pack for n in (4, 12, 18))
 
 
 class _on:
@@ -722,7 +723,7 @@ def fa2_qk_norm_rope(q, k, q_weight=None, k_weight=None, rope=None, positions=No
     k_out, sk = _norm_out(k, k_out, "k_out", dev)
     rc = load_library().fa2_qk_norm_rope(
         q.data_ptr(), k.data_ptr(), _dp(q_weight), _dp(k_weight), w32, _dp(rope), _dp(positions), q_out.data_ptr(),
-        k_out.data_ptr(), *dims, eps, _LL12(*strides, *sq, *sk), _raw_stream(dev))
+        k_out.data_ptr(), *dims, eps, _pack12(*strides, *sq, *sk), _raw_stream(dev))
     if rc != FA2_OK:
         raise FA2Error("fa2_qk_norm_rope", rc)
     return q_out, k_out
@@ -758,7 +759,7 @@ def fa2_qk_norm_rope_bwd(dq_out, dk_out, q, k, q_weight=None, k_weight=None, rop
         workspace = torch.empty(max(1, lib.fa2_qk_norm_rope_bwd_workspace_bytes(d)), dtype=torch.uint8, device=q.device)
     rc = lib.fa2_qk_norm_rope_bwd(
         dq_out.data_ptr(), dk_out.data_ptr(), q.data_ptr(), k.data_ptr(), _dp(q_weight), _dp(k_weight), w32, _dp(rope),
-        _dp(positions), dq.data_ptr(), dk.data_ptr(), _dp(dwq), _dp(dwk), *dims, eps, _LL18(*grads, *strides, *sq, *sk),
+        _dp(positions), dq.data_ptr(), dk.data_ptr(), _dp(dwq), _dp(dwk), *dims, eps, _pack18(*grads, *strides, *sq, *sk),
         _dp(workspace), 0 if workspace is None else workspace.numel() * workspace.element_size(), _raw_stream(dev))
     if rc != FA2_OK:
         raise FA2Error("fa2_qk_norm_rope_bwd", rc)
@@ -854,7 +855,7 @@ def fa2_kv4_append(k, v, cache, slots, k_scale: float = 1.0, v_scale: float = 1.
     if T == 0:
         return
     rc = load_library().fa2_kv4_append(
-        k.data_ptr(), v.data_ptr(), _LL4(kt, kh, vt, vh), cache.data_ptr(), page_stride, slots.data_ptr(), _dp(k_out),
+        k.data_ptr(), v.data_ptr(), _pack4(kt, kh, vt, vh), cache.data_ptr(), page_stride, slots.data_ptr(), _dp(k_out),
         _dp(v_out), T, heads, pages, page_size, d, k_scale, v_scale, _raw_stream(dev))
     if rc != FA2_OK:
         raise FA2Error("fa2_kv4_append", rc)
