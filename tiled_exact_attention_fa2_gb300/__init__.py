@@ -792,10 +792,10 @@ def fa2_page_plan(cached_lens, new_lens, free_pages, block_table, page_size: int
     if max_tokens < 0:
         raise ValueError("max_tokens must be at least 0")
     if plan is None:
-        lens, cu_new, cu_total, positions, needed = torch.empty(
-            3 * B + 3 + max_tokens, dtype=torch.int32, device=cached_lens.device).split_with_sizes((B, B + 1, B + 1, max_tokens, 1))
-        plan = PagePlan(lens, cu_new, cu_total, torch.empty(max_tokens, dtype=torch.int64, device=cached_lens.device),
-                        positions, needed)
+        at = cached_lens.device  # (six allocations take less time than two and the views of their parts)
+        plan = PagePlan(torch.empty(B, dtype=torch.int32, device=at), torch.empty(B + 1, dtype=torch.int32, device=at),
+                        torch.empty(B + 1, dtype=torch.int32, device=at), torch.empty(max_tokens, dtype=torch.int64, device=at),
+                        torch.empty(max_tokens, dtype=torch.int32, device=at), torch.empty(1, dtype=torch.int32, device=at))
     else:
         for t, name, n in zip(plan, PagePlan._fields, (B, B + 1, B + 1, max_tokens, max_tokens, 1)):
             _ints(t, "plan." + name, dev, n, torch.int64 if name == "slots" else torch.int32)
