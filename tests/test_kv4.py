@@ -720,3 +720,52 @@ def test_plan_at_the_sizes_where_its_layout_changes(B):
     got = fa2.fa2_page_plan(i32(odd), i32(more), free, tables[1], 16, T)
     assert fa2.fa2_device_status(reset=True) == 3
     assert all(torch.equal(a, b) for a, b in zip(got, want)) and torch.equal(*tables)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("B,most,H,Hkv,d", [(40, 300, 4, 1, 128), (33, 77, 6, 2, 64), (70, 90, 3, 3, 16), (1100, 200, 2, 1, 32)])
+def test_attention_ragged_queries(B, most, H, Hkv, d):
+    """A few requests have most of the queries; offsets that do not begin at 0; a request that is left out."""
+    rng = np.random.default_rng(B)
+    nqs = rng.integers(0, 3, B)
+    nqs[[0, B // 2, B - 1]] = [most // 2, most, 5]
+    lens = rng.integers(0, 40 if B < 1000 else 5, B)
+    lens[[0, B // 2, B - 1]] = [most, most + 100, 3]
+    cache, table, kv = filled(rng, [int(x) for x in lens], Hkv, 16, d, width=64)
+    cu = 4 + np.r_[0, np.cumsum(nqs)]
+    total = int(cu[-1]) + 6
+    q = torch.from_numpy(rng.standard_normal((total, H, d))).to(torch.bfloat16).cuda()
+    rows = [(int(cu[b]), int(cu[b + 1])) for b in range(B)]
+    fa2.fa2_device_status(reset=True)
+    left = torch.ones(total, dtype=torch.bool, device="cuda")
+    left[int(cu[0]):int(cu[-1])] = False
+    for bound in (most + 100, 1 << 20):
+        o, lse = torch.full_like(q, 9.0), torch.full((H, total), 9.0, device="cuda")
+        tab = i32(table) if bound < 1 << 20 else torch.cat([i32(table), torch.zeros((B, 100), dtype=torch.int32, device="cuda")], 1)
+        fa2.fa2_kv4_attn(q, cache, tab, i32(lens), i32(cu), most, max_seqlen_k=bound, o=o, lse=lse)
+        assert (fa2.fa2_kv4_attn_workspace_bytes(B, H, Hkv, most, min(bound, tab.shape[1] * 16), d) > 0) == (bound == 1 << 20)
+        assert fa2.fa2_device_status() == 0
+        check_attention(o, lse, rows, q.double().cpu().numpy(), kv, 1 / math.sqrt(d), True, H)
+        assert torch.all(o[left] == 9) and torch.all(lse[:, left] == 9)
+        for at, bad_len in ((B // 2, -1), (1, 1 << 24)):
+            bad = lens.copy()
+            bad[at] = bad_len
+            o2, lse2 = torch.full_like(q, 9.0), torch.full_like(lse, 9.0)
+            fa2.fa2_kv4_attn(q, cache, tab, i32(bad), i32(cu), most, max_seqlen_k=bound, o=o2, lse=lse2)
+            assert fa2.fa2_device_status(reset=True) == 3
+            mine = left.clone()
+            mine[rows[at][0]:rows[at][1]] = True
+            assert torch.all(o2[mine] == 9)
+            if bound < 1 << 20:
+                assert torch.equal(o2[~mine], o[~mine]) and torch.equal(lse2[:, ~mine], lse[:, ~mine])
+            else:  # (the line is cut elsewhere: sums in another order)
+                others = [r if i != at else (0, 0) for i, r in enumerate(rows)]
+                check_attention(o2, lse2, others, q.double().cpu().numpy(), kv, 1 / math.sqrt(d), True, H)
+    # offsets that go down, and past the queries: nothing out of range is read or written
+    for at, x in ((B // 3, total + 1000), (B // 2, -5)):
+        wrong = cu.copy()
+        wrong[at] = x
+        o2, lse2 = torch.full_like(q, 9.0), torch.full_like(lse, 9.0)
+        fa2.fa2_kv4_attn(q, cache, i32(table), i32(lens), i32(wrong), most, max_seqlen_k=most + 100, o=o2, lse=lse2)
+        assert fa2.fa2_device_status(reset=True) == 3
+        assert torch.all(o2[left] == 9)
