@@ -769,3 +769,9 @@ def test_attention_ragged_queries(B, most, H, Hkv, d):
         fa2.fa2_kv4_attn(q, cache, i32(table), i32(lens), i32(wrong), most, max_seqlen_k=most + 100, o=o2, lse=lse2)
         assert fa2.fa2_device_status(reset=True) == 3
         assert torch.all(o2[left] == 9)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,Hkv,d", [(300, 12, 16), (100, 5, 16), (77, 33, 128), (65, 9, 32), (40, 20, 64), (1, 1, 16), (3001, 16, 32)])
+def test_append_head_counts_that_do_not_fill_a_block(T, Hkv, d):
+    test_append_many_tokens_and_back(T, Hkv, d)

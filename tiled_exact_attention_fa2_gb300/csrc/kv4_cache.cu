@@ -5,7 +5,7 @@
 // bits (and 2 bytes more where the caller wants the stored values), the
 // gather reads 4.5 bits and writes 2 bytes.  Measured on a GB300 (device
 // time): append of 16385 tokens x 8 heads of 128 columns with the stored
-// values 25.6 us (6.0 TB/s, 88 % of a copy's rate), gather of 20000 tokens of
+// values 25.5 us (6.0 TB/s, 88 % of a copy's rate), gather of 20000 tokens of
 // the same 21.4 us (5.4 TB/s; 1258 CTAs in 2.8 waves).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -29,7 +29,7 @@ struct AppendProblem {
   float k_scale, v_scale;
   const long long* slots;
   PagedCache cache;
-  int tokens, row_threads, block_tokens;  // threads of a token (H_kv d / 8), tokens of a CTA
+  int tokens, block_heads, block_tokens;  // K/V heads and tokens of a CTA
 };
 
 // The values of four code bytes as bf16 (exact: 6 significant bits).
@@ -92,12 +92,15 @@ __global__ void __launch_bounds__(256, 5) fa2_kv4_append_kernel(const AppendProb
   using L = Kv4<D>;
   griddep_wait();
   griddep_launch_dependents();
-  // thread -> (token, head, columns); a pair of lanes stays together, since
-  // row_threads is even
-  const int local = threadIdx.x / p.row_threads;
-  const int r = threadIdx.x - local * p.row_threads + blockIdx.y * 256;
-  const bool fits = r < p.row_threads && local < p.block_tokens;
-  const int h = r / (D / 8), c8 = r % (D / 8), grp = c8 >> 1;
+  // thread -> (token, head, columns), a group's pair of lanes together.  Rows
+  // of 16 and 32 columns go through the tokens before the heads: a byte store
+  // of a warp then falls into a few sectors of a tile, not into one of every
+  // head (39000 tokens of 16 heads of 32 columns 44 us else).
+  const int c8 = threadIdx.x % (D / 8), grp = c8 >> 1, at = threadIdx.x / (D / 8);
+  const int slow = at / (D <= 32 ? p.block_tokens : p.block_heads), fast = at - slow * (D <= 32 ? p.block_tokens : p.block_heads);
+  const int local = D <= 32 ? fast : slow, head = D <= 32 ? slow : fast;
+  const int h = blockIdx.y * p.block_heads + head;
+  const bool fits = local < p.block_tokens && head < p.block_heads && h < p.cache.heads;
   uint4 k[TOKENS], v[TOKENS];
   long long slot[TOKENS];
 #pragma unroll
@@ -260,11 +263,12 @@ __global__ void __launch_bounds__(256) fa2_kv4_gather_kernel(const GatherProblem
 
 template <int D>
 int launch_append_d(AppendProblem p, cudaStream_t st) {
-  // whole tokens to a CTA; a token of more than 256 threads spreads over
-  // blockIdx.y
-  p.row_threads = p.cache.heads * (D / 8);
-  p.block_tokens = p.row_threads >= 256 ? 1 : 256 / p.row_threads;
-  const unsigned parts = (p.row_threads + 255) / 256;
+  // (token, head) pairs of a CTA: whole tokens where they fit (16 of them for
+  // short rows), else equal parts of the heads over blockIdx.y
+  constexpr int kPairs = 256 / (D / 8), kHeads = D <= 32 ? kPairs / 16 : kPairs;
+  const unsigned parts = (p.cache.heads + kHeads - 1) / kHeads;
+  p.block_heads = (p.cache.heads + parts - 1) / parts;
+  p.block_tokens = kPairs / p.block_heads;
   // Many tokens: two to a thread, for twice the loads in flight.
   const long long ctas = (p.tokens + p.block_tokens - 1LL) / p.block_tokens;
   if (ctas * parts >= 152 * 16)
