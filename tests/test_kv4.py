@@ -775,3 +775,44 @@ def test_attention_ragged_queries(B, most, H, Hkv, d):
 @pytest.mark.parametrize("T,Hkv,d", [(300, 12, 16), (100, 5, 16), (77, 33, 128), (65, 9, 32), (40, 20, 64), (1, 1, 16), (3001, 16, 32)])
 def test_append_head_counts_that_do_not_fill_a_block(T, Hkv, d):
     test_append_many_tokens_and_back(T, Hkv, d)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("lens,H,Hkv,nq,d", [([2048] * 19, 8, 8, 1, 64),    # every unit is one CTA's part of the line
+                                             ([4096] * 19, 8, 4, 1, 32),    # two CTAs'
+                                             ([2048] * 19, 128, 8, 1, 16),  # the same with 16 rows: parts that straddle
+                                             ([60000], 4, 1, 1, 16), ([60000], 4, 1, 3, 16),
+                                             ([30011, 5, 20000, 0, 9000], 2, 2, 1, 32),
+                                             # few units, whose CTAs join their warps: all ends at CTAs' ends
+                                             ([12288] * 19, 4, 1, 1, 16), ([9216] * 19, 16, 1, 1, 16),
+                                             # a unit that is the share of one CTA of seven warps, behind a long one
+                                             ([60032, 448], 2, 1, 1, 16), ([60032, 448], 16, 1, 1, 16),
+                                             ([60000, 448, 0, 3], 1, 1, 1, 64), ([131072], 8, 1, 1, 128),
+                                             ([20000, 130000], 24, 2, 1, 32)],
+                         ids=lambda x: f"{len(x)}x{max(x)}" if isinstance(x, list) else str(x))
+def test_attention_units_of_whole_ctas(lens, H, Hkv, nq, d):
+    """Units that are long against a CTA's part of the line, whose warps join their results before the combine."""
+    P, g = 128, torch.Generator(device="cuda").manual_seed(len(lens))
+    counts = [-(-x // P) for x in lens]
+    table, at = np.zeros((len(lens), max(max(counts), 16384 // P)), np.int64), 0
+    cache = fa2.fa2_kv4_cache(sum(counts), Hkv, P, d)
+    kv = []
+    for b, x in enumerate(lens):
+        table[b, :counts[b]] = np.arange(at, at + counts[b])
+        at += counts[b]
+        ramp = torch.linspace(0.2, 2.0, x, device="cuda")[:, None, None]
+        k = (torch.randn(x, Hkv, d, generator=g, device="cuda") * ramp).to(torch.bfloat16)
+        v = torch.randn(x, Hkv, d, generator=g, device="cuda").to(torch.bfloat16)
+        ko, vo = torch.empty_like(k), torch.empty_like(v)
+        pos = torch.arange(x, device="cuda")
+        fa2.fa2_kv4_append(k, v, cache, i32(table[b]).long()[pos // P] * P + pos % P, k_out=ko, v_out=vo)
+        kv.append([t.double().cpu().numpy().transpose(1, 0, 2) for t in (ko, vo)])
+    q = torch.randn(len(lens) * nq, H, d, generator=g, device="cuda").to(torch.bfloat16)
+    fa2.fa2_device_status(reset=True)
+    assert fa2.fa2_kv4_attn_workspace_bytes(len(lens), H, Hkv, nq, table.shape[1] * P, d) > 0
+    o, lse = fa2.fa2_kv4_attn(q, cache, i32(table), i32(lens))
+    assert fa2.fa2_device_status() == 0
+    rows = [(b * nq, (b + 1) * nq) for b in range(len(lens))]
+    check_attention(o, lse, rows, q.double().cpu().numpy(), kv, 1 / math.sqrt(d), True, H)
+    again = fa2.fa2_kv4_attn(q, cache, i32(table), i32(lens))
+    assert torch.equal(again[0], o) and torch.equal(again[1], lse)

@@ -16,8 +16,9 @@
 // warp: every warp reads as many bytes as any other, whatever the lengths.
 // A unit inside one span is finished by its warp; one that spans share leaves
 // a partial result per span (unnormalised O, running maximum and sum), which
-// the combine kernel joins in span order.  Warps share nothing, so there are
-// no barriers, and the result does not depend on the order they run in.  Units
+// the combine kernel joins in span order (where very many share a unit, each
+// CTA's warps first).  Warps share nothing on the way, and the result does not
+// depend on the order they run in.  Units
 // of short requests take one CTA each instead, whose warps share the unit's
 // keys and join in shared memory.
 //
@@ -72,8 +73,16 @@ __device__ int g_attn4_status;
 // rows allow.
 template <int NT>
 constexpr int kWarps = NT == 1 ? 16 : 12;
+constexpr int kCtas = 152;  // one wave
+// From this many spans of a unit on its CTAs join theirs before the combine
+// kernel, whose time else grows with them.  Measured, 128 columns, joined /
+// not, in us: one unit of 131072 keys 15.6 / 36, 8 of up to 131072 (304 spans)
+// 34.5 / 38.0, 24 of 40000 (101) 30.2 / 30.9, 32 of 32768 (76) 27.0 / 27.2, 64
+// of 16384 (38) 30.0 / 29.5; 16 rows a unit, 8 of 65536 (228) 30.5 / 32.0, 64
+// of 8192 (28) 34.1 / 31.3.
+constexpr int kJoinSpans = 96;
 template <int NT>
-constexpr int kSpans = 152 * kWarps<NT>;  // one wave
+constexpr int kSpans = kCtas * kWarps<NT>;
 constexpr int kFew = 4;  // warps of a CTA that takes one of many short units
 constexpr float kNoMax = -1.7e38f;  // running maximum of a row that has seen no key (finite: no inf - inf)
 constexpr float kLift = 11.f;   // weights are held 2^11 up
@@ -158,17 +167,23 @@ __device__ __forceinline__ long long pairs_of(const Attn4Problem& p, const Reque
   return r.ok ? static_cast<long long>(p.cache.heads) * row_tiles<ROWS>(p, r) * key_pairs(r) : 0;
 }
 
-// The line of all units' pairs cut into equal spans.
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+  return (a | b) >> 32 ? a / b : static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+}
+
+// The line of all units' pairs cut into equal spans, of which a CTA's `warps`
+// take consecutive ones: all of a CTA's on a long line, few on a short one, so
+// that it spreads over the SMs.  With JOIN a CTA whose spans lie in one unit
+// joins them to one partial result, in the place of its first span's.
 template <int NT>
 struct Line {
+  int warps;
   long long len;
-  __device__ __forceinline__ explicit Line(long long total) {
-    len = total >> 32 ? (total + kSpans<NT> - 1) / kSpans<NT> : (static_cast<uint32_t>(total) + (kSpans<NT> - 1LL)) / kSpans<NT>;
-    if (len < kMinPairs) len = kMinPairs;
-  }
-  __device__ __forceinline__ int span_of(long long pair) const {
-    return static_cast<int>(pair >> 32 ? pair / len : static_cast<uint32_t>(pair) / static_cast<uint32_t>(len));
-  }
+  __device__ __forceinline__ explicit Line(long long total)
+      : warps(static_cast<int>(min(static_cast<long long>(kWarps<NT>), quotient(total + kCtas * kMinPairs - 1, kCtas * kMinPairs)))),
+        len(max(quotient(total + kSpans<NT> - 1, kSpans<NT>), static_cast<long long>(kMinPairs))) {}
+  __device__ __forceinline__ long long share() const { return len * warps; }  // of a CTA
+  __device__ __forceinline__ int span_of(long long pair) const { return static_cast<int>(quotient(pair, len)); }
 };
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -704,7 +719,32 @@ __device__ __forceinline__ void write_row(const Attn4Problem& p, const Request& 
   if (lane == 0) p.lse[static_cast<long long>(head) * p.total_q + tok] = l == 0.f ? -INFINITY : row_lse(top, l);
 }
 
+// A row of the partial results that `parts` <= 32 warps of the CTA left in
+// shared memory: the lane's columns, sum and maximum.
 template <int D, int NT>
+__device__ __forceinline__ void join_row(const WarpSmem<D, NT>* all, int parts, int local, float* o, float& l, float& top,
+                                         int lane) {
+  constexpr int kCols = D >= 32 ? D / 32 : 1;
+  const float2 ml = lane < parts ? all[lane].ml[local] : make_float2(kNoMax, 0.f);
+  top = ml.x;
+#pragma unroll
+  for (int sh = 16; sh > 0; sh >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, sh));
+  const float w = ex2_approx(ml.x - top);
+  l = w * ml.y;
+#pragma unroll
+  for (int sh = 16; sh > 0; sh >>= 1) l += __shfl_xor_sync(0xffffffffu, l, sh);
+#pragma unroll
+  for (int k = 0; k < kCols; ++k) o[k] = 0.f;
+  for (int i = 0; i < parts; ++i) {
+    const float wi = __shfl_sync(0xffffffffu, w, i);
+    const float* row = reinterpret_cast<const float*>(all[i].tiles) + local * D + lane * kCols;
+#pragma unroll
+    for (int k = 0; k < kCols; ++k)
+      if (lane * kCols < D) o[k] = fmaf(wi, row[k], o[k]);
+  }
+}
+
+template <int D, int NT, bool JOIN>
 __global__ void __launch_bounds__(kWarps<NT> * 32, 1) fa2_kv4_attn_kernel(const Attn4Problem p) {
   constexpr int kRows = 8 * NT;
   extern __shared__ __align__(128) char smem[];
@@ -751,9 +791,8 @@ __global__ void __launch_bounds__(kWarps<NT> * 32, 1) fa2_kv4_attn_kernel(const 
     if (!fine) atomicCAS(&g_attn4_status, kDevOk, kDevBadSeqlens);
   }
   const Line<NT> line(total);
-  // A short line spreads over the SMs, a long one gives an SM consecutive
-  // spans (whose units share queries and pages).
-  const int span = line.len == kMinPairs ? warp * gridDim.x + blockIdx.x : blockIdx.x * kWarps<NT> + warp;
+  if (warp >= line.warps) return;
+  const int span = blockIdx.x * line.warps + warp;
   const long long begin = span * line.len, end = min(begin + line.len, total);
   long long at = begin;
   if (at >= end) return;
@@ -775,10 +814,34 @@ __global__ void __launch_bounds__(kWarps<NT> * 32, 1) fa2_kv4_attn_kernel(const 
     // (a request's units are at most H_kv times its row tiles: 32 bits, as its
     // pairs are; their product may not be)
     const long long rel = at - base;
-    const int unit = rel >> 32 ? static_cast<int>(rel / np) : static_cast<int>(static_cast<uint32_t>(rel) / static_cast<uint32_t>(np));
+    const int unit = static_cast<int>(quotient(rel, np));
     const int first = static_cast<int>(rel - static_cast<long long>(unit) * np);
     const int h = unit / rt, row0 = (unit - h * rt) * kRows;
     const int n = static_cast<int>(min(static_cast<long long>(np - first), end - at));
+    // (the same for all warps of the CTA: it is about all their spans)
+    const long long cta = blockIdx.x * line.share(), start = at - first;
+    if (JOIN && start <= cta && cta + line.share() <= start + np) {
+      // (a warp whose copy did not come leaves the rows wrong, with the status
+      // word set: the others must not wait for it)
+      if (run_pairs<D, NT>(s, ring, p, rq, b, h, row0, first, n, lane))
+        end_unit<D, NT>(s, p, rq, h, row0, reinterpret_cast<float*>(ws->tiles), ws->ml, lane);
+      asm volatile("bar.sync 1, %0;" ::"r"(line.warps * 32) : "memory");
+      constexpr int kCols = D >= 32 ? D / 32 : 1;
+      const long long slot = 2LL * blockIdx.x * line.warps * kRows;
+      for (int local = warp; local < kRows && row0 + local < p.G * rq.Lq; local += line.warps) {
+        float o[kCols], l, top;
+        join_row<D, NT>(reinterpret_cast<const WarpSmem<D, NT>*>(smem), line.warps, local, o, l, top, lane);
+        if (np == line.share()) {
+          write_row<D>(p, rq, h, row0 + local, o, l, top, lane);
+          continue;
+        }
+#pragma unroll
+        for (int k = 0; k < kCols; ++k)
+          if (lane * kCols < D) p.part[(slot + local) * D + lane * kCols + k] = o[k];
+        if (lane == 0) p.part_ml[slot + local] = make_float2(top, l);
+      }
+      return;
+    }
     if (!run_pairs<D, NT>(s, ring, p, rq, b, h, row0, first, n, lane)) return;
     // A unit that is whole goes out; else slot 0 of the span if the part
     // began at the span's start, slot 1 if within it.
@@ -794,7 +857,7 @@ __global__ void __launch_bounds__(kWarps<NT> * 32, 1) fa2_kv4_attn_kernel(const 
 // after the other (where the unit's spans are, their maxima and sums, their
 // rows), so each of the three is one round of loads: a lane per span for the
 // maxima, then the rows of kBatch spans at once.
-template <int D, int ROWS, int WPR>
+template <int D, int ROWS, int WPR, bool JOIN>
 __global__ void __launch_bounds__(256) fa2_kv4_combine_kernel(const Attn4Problem p, int max_row_tiles) {
   constexpr int kCols = D >= 32 ? D / 32 : 1, kRowsCta = 8 / WPR, kBatch = 8;
   __shared__ float s_o[WPR > 1 ? 8 : 1][D];
@@ -814,24 +877,39 @@ __global__ void __launch_bounds__(256) fa2_kv4_combine_kernel(const Attn4Problem
   const bool live = rq.ok && row < p.G * rq.Lq;
   const int r = static_cast<int>(row);
   const int np = key_pairs(rq);
-  int count = 0, s0 = 0;  // spans that share the unit, the first of them
+  // The unit's partial results: `head` spans from s0 on, `mid` CTAs from span
+  // s1 on that joined theirs, spans from s2 on.
+  int count = 0, s0 = 0, head = 0, mid = 0, s1 = 0, s2 = 0, warps = 0;
   long long slot0 = 0;
   if (live && np > 0) {
     const Line<ROWS / 8> line(total);
     const long long first = start + (static_cast<long long>(h) * row_tiles<ROWS>(p, rq) + rt) * np;
+    warps = line.warps;
     s0 = line.span_of(first);
-    count = line.span_of(first + np - 1) - s0 + 1;
+    const int last = line.span_of(first + np - 1);
+    // the CTAs of the whole spans: from, to
+    const int lo = (s0 + (first != s0 * line.len ? 1 : 0) + warps - 1) / warps;
+    const int hi = (last + (first + np == (last + 1) * line.len ? 1 : 0)) / warps;
+    count = head = last - s0 + 1;
+    if (JOIN && hi > lo) {
+      s1 = lo * warps, s2 = hi * warps;
+      head = s1 - s0, mid = hi - lo;
+      count = head + mid + last - s2 + 1;
+    }
     // slot 0 of a span, but slot 1 where the unit begins within it
     slot0 = (2LL * s0 + (first != s0 * line.len ? 1 : 0)) * ROWS + local;
   }
   // (the same for all warps of a row; rows of one warp need no barrier)
   if (WPR == 1 && (!live || count == 1)) return;
-  auto at = [&](int i) { return i == 0 ? slot0 : 2LL * (s0 + i) * ROWS + local; };
+  auto at = [&](int i) {
+    const int span = i < head ? s0 + i : i < head + mid ? s1 + (i - head) * warps : s2 + i - head - mid;
+    return i == 0 ? slot0 : 2LL * span * ROWS + local;
+  };
   float l = 0.f, top = kNoMax, o[kCols];
 #pragma unroll
   for (int k = 0; k < kCols; ++k) o[k] = 0.f;
   const bool active = lane * kCols < D;
-  // warp `part` takes spans part, part + WPR, ..., 32 at a time
+  // warp `part` takes results part, part + WPR, ..., 32 at a time
   for (int i0 = part; count > 1 && i0 < count; i0 += WPR * 32) {
     float2 ml = make_float2(kNoMax, 0.f);
     if (i0 + lane * WPR < count) ml = p.part_ml[at(i0 + lane * WPR)];
@@ -927,23 +1005,8 @@ __global__ void __launch_bounds__(W * 32, kWarps<NT> / W) fa2_kv4_attn_unit_kern
   __syncthreads();
   const int parts = each > 0 ? (np + each - 1) / each : 0;
   for (int local = warp; local < kRows && row0 + local < rows; local += W) {
-    const float2 ml = lane < parts ? all[lane].ml[local] : make_float2(kNoMax, 0.f);
-    float top = ml.x;
-#pragma unroll
-    for (int sh = 16; sh > 0; sh >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, sh));
-    const float w = ex2_approx(ml.x - top);
-    float l = w * ml.y, o[kCols];
-#pragma unroll
-    for (int sh = 16; sh > 0; sh >>= 1) l += __shfl_xor_sync(0xffffffffu, l, sh);
-#pragma unroll
-    for (int k = 0; k < kCols; ++k) o[k] = 0.f;
-    for (int i = 0; i < parts; ++i) {
-      const float wi = __shfl_sync(0xffffffffu, w, i);
-      const float* row = reinterpret_cast<const float*>(all[i].tiles) + local * D + lane * kCols;
-#pragma unroll
-      for (int k = 0; k < kCols; ++k)
-        if (lane * kCols < D) o[k] = fmaf(wi, row[k], o[k]);
-    }
+    float o[kCols], l, top;
+    join_row<D, NT>(all, parts, local, o, l, top, lane);
     write_row<D>(p, rq, h, row0 + local, o, l, top, lane);
   }
 }
@@ -1002,15 +1065,19 @@ int launch_attn_d(Attn4Problem p, long long max_rows, cudaStream_t st) {
     if (int e = ensure_max_smem(reinterpret_cast<const void*>(kernel), smem)) return e;
     return launch_pdl(kernel, dim3(static_cast<unsigned>(units)), dim3(w * 32), smem, st, p, row_tiles);
   }
-  if (int e = ensure_max_smem(reinterpret_cast<const void*>(fa2_kv4_attn_kernel<D, NT>), kSmem)) return e;
-  if (int e = launch_pdl(fa2_kv4_attn_kernel<D, NT>, dim3(152), dim3(kWarps<NT> * 32), kSmem, st, p)) return e;
-  // Spans of a unit, were all requests of one length: with few, a warp joins
-  // a row alone; with many, a CTA's eight do.
-  if (kSpans<NT> / units < 16)
-    return launch_pdl(fa2_kv4_combine_kernel<D, kRows, 1>, dim3(static_cast<unsigned>(units * (kRows / 8))), dim3(256), 0, st, p,
+  // Spans of a unit, were all requests of one length: with few, a warp of the
+  // combine kernel joins a row alone; with more a CTA's eight do; with many the
+  // CTAs of the first kernel join theirs before.
+  const long long spans = kSpans<NT> / units;
+  const bool join = spans >= kJoinSpans;
+  const auto kernel = join ? fa2_kv4_attn_kernel<D, NT, true> : fa2_kv4_attn_kernel<D, NT, false>;
+  if (int e = ensure_max_smem(reinterpret_cast<const void*>(kernel), kSmem)) return e;
+  if (int e = launch_pdl(kernel, dim3(kCtas), dim3(kWarps<NT> * 32), kSmem, st, p)) return e;
+  if (spans < 16)
+    return launch_pdl(fa2_kv4_combine_kernel<D, kRows, 1, false>, dim3(static_cast<unsigned>(units * (kRows / 8))), dim3(256), 0, st, p,
                       row_tiles);
-  return launch_pdl(fa2_kv4_combine_kernel<D, kRows, 8>, dim3(static_cast<unsigned>(units * kRows)), dim3(256), 0, st, p,
-                    row_tiles);
+  return launch_pdl(join ? fa2_kv4_combine_kernel<D, kRows, 8, true> : fa2_kv4_combine_kernel<D, kRows, 8, false>,
+                    dim3(static_cast<unsigned>(units * kRows)), dim3(256), 0, st, p, row_tiles);
 }
 
 template <int D>
