@@ -38,7 +38,7 @@
 // TB/s of cache; between two lengths the marginal rate is 6.9 TB/s, a copy's:
 // the rest is 6 us until the first tiles arrive, about 4 us for the combine
 // kernel and as much between the first and the last warp's end); two requests
-// of 131072 keys, four queries and 4 heads a group (16 rows), 46.7 us, bound
+// of 131072 keys, four queries and 4 heads a group (16 rows), 45.4 us, bound
 // by instruction issue: an mma.m16n8k16 takes about 8 issue slots of its
 // scheduler, and 32 of them with the 64 decodes and 64 scalings of a tile at
 // least 107 cycles of an SM against 98 for the tile's bytes; one request of
@@ -820,14 +820,22 @@ __global__ void __launch_bounds__(kWarps<NT> * 32, 1) fa2_kv4_attn_kernel(const 
     const int n = static_cast<int>(min(static_cast<long long>(np - first), end - at));
     // (the same for all warps of the CTA: it is about all their spans)
     const long long cta = blockIdx.x * line.share(), start = at - first;
-    if (JOIN && start <= cta && cta + line.share() <= start + np) {
+    const bool whole = JOIN && start <= cta && cta + line.share() <= start + np;
+    if (run_pairs<D, NT>(s, ring, p, rq, b, h, row0, first, n, lane)) {
+      // A unit that is whole goes out; else slot 0 of the span if the part
+      // began at the span's start, slot 1 if within it.
+      const long long slot = (2LL * span + (at == begin ? 0 : 1)) * kRows;
+      float* const part = whole ? reinterpret_cast<float*>(ws->tiles) : n == np ? nullptr : p.part + slot * D;
+      end_unit<D, NT>(s, p, rq, h, row0, part, whole ? ws->ml : p.part_ml + slot, lane);
+    } else if (!whole) {
+      return;
+    }
+    if (whole) {
       // (a warp whose copy did not come leaves the rows wrong, with the status
       // word set: the others must not wait for it)
-      if (run_pairs<D, NT>(s, ring, p, rq, b, h, row0, first, n, lane))
-        end_unit<D, NT>(s, p, rq, h, row0, reinterpret_cast<float*>(ws->tiles), ws->ml, lane);
       asm volatile("bar.sync 1, %0;" ::"r"(line.warps * 32) : "memory");
       constexpr int kCols = D >= 32 ? D / 32 : 1;
-      const long long slot = 2LL * blockIdx.x * line.warps * kRows;
+      const long long to = 2LL * blockIdx.x * line.warps * kRows;
       for (int local = warp; local < kRows && row0 + local < p.G * rq.Lq; local += line.warps) {
         float o[kCols], l, top;
         join_row<D, NT>(reinterpret_cast<const WarpSmem<D, NT>*>(smem), line.warps, local, o, l, top, lane);
@@ -837,16 +845,11 @@ __global__ void __launch_bounds__(kWarps<NT> * 32, 1) fa2_kv4_attn_kernel(const 
         }
 #pragma unroll
         for (int k = 0; k < kCols; ++k)
-          if (lane * kCols < D) p.part[(slot + local) * D + lane * kCols + k] = o[k];
-        if (lane == 0) p.part_ml[slot + local] = make_float2(top, l);
+          if (lane * kCols < D) p.part[(to + local) * D + lane * kCols + k] = o[k];
+        if (lane == 0) p.part_ml[to + local] = make_float2(top, l);
       }
       return;
     }
-    if (!run_pairs<D, NT>(s, ring, p, rq, b, h, row0, first, n, lane)) return;
-    // A unit that is whole goes out; else slot 0 of the span if the part
-    // began at the span's start, slot 1 if within it.
-    const long long slot = (2LL * span + (at == begin ? 0 : 1)) * kRows;
-    end_unit<D, NT>(s, p, rq, h, row0, n == np ? nullptr : p.part + slot * D, p.part_ml + slot, lane);
     at += n;
   }
 }
