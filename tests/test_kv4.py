@@ -816,3 +816,34 @@ def test_attention_units_of_whole_ctas(lens, H, Hkv, nq, d):
     check_attention(o, lse, rows, q.double().cpu().numpy(), kv, 1 / math.sqrt(d), True, H)
     again = fa2.fa2_kv4_attn(q, cache, i32(table), i32(lens))
     assert torch.equal(again[0], o) and torch.equal(again[1], lse)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("B,H,Hkv,nq,d,lens", [(1, 8, 1, 1, 128, [2048]), (1, 32, 8, 1, 64, [1100]), (3, 4, 2, 2, 32, [1500, 0, 33]),
+                                               (4, 8, 8, 1, 16, [1, 31, 2047, 1025]), (2, 16, 1, 1, 128, [600, 2000]),
+                                               (20, 4, 1, 3, 16, [1030] + list(range(0, 190, 10))),
+                                               (8, 10, 5, 1, 32, [2000, 64, 0, 1, 500, 96, 7, 1999]),
+                                               (6, 24, 2, 3, 64, [800, 700, 0, 5, 769, 32])])
+def test_attention_units_of_clusters(B, H, Hkv, nq, d, lens):
+    """Few units of one to two thousand keys: eight, four or two CTAs each, some with no key."""
+    rng = np.random.default_rng(B)
+    cache, table, kv = filled(rng, lens, Hkv, 32, d)
+    q = torch.from_numpy(rng.standard_normal((B * nq, H, d)) * 2).to(torch.bfloat16).cuda()
+    rows = [(b * nq, (b + 1) * nq) for b in range(B)]
+    bound = max(max(lens), 769 if B == 6 else 1025)
+    fa2.fa2_device_status(reset=True)
+    assert fa2.fa2_kv4_attn_workspace_bytes(B, H, Hkv, nq, bound, d) == 0
+    tab = torch.cat([i32(table), torch.zeros((B, 2), dtype=torch.int32, device="cuda")], 1)
+    for causal in (True, False):
+        o, lse = fa2.fa2_kv4_attn(q, cache, tab, i32(lens), max_seqlen_k=bound, causal=causal)
+        check_attention(o, lse, rows, q.double().cpu().numpy(), kv, 1 / math.sqrt(d), causal, H)
+        again = fa2.fa2_kv4_attn(q, cache, tab, i32(lens), max_seqlen_k=bound, causal=causal)
+        assert torch.equal(again[0], o) and torch.equal(again[1], lse)
+    assert fa2.fa2_device_status() == 0
+    bad = list(lens)
+    bad[-1] = -1
+    o2, lse2 = torch.full_like(o, 9.0), torch.full_like(lse, 9.0)
+    fa2.fa2_kv4_attn(q, cache, tab, i32(bad), max_seqlen_k=bound, causal=False, o=o2, lse=lse2)
+    assert fa2.fa2_device_status(reset=True) == 3
+    at = rows[-1][0]
+    assert torch.all(o2[at:] == 9) and torch.equal(o2[:at], o[:at]) and torch.equal(lse2[:, :at], lse[:, :at])

@@ -976,9 +976,12 @@ __global__ void __launch_bounds__(256) fa2_kv4_combine_kernel(const Attn4Problem
 
 // Short requests: one CTA of W warps per unit, which take equal parts of its
 // keys and join their partial results in shared memory, in the order of the
-// keys: one launch, no line to lay out first, no workspace.
-template <int D, int NT, int W>
-__global__ void __launch_bounds__(W * 32, kWarps<NT> / W) fa2_kv4_attn_unit_kernel(const Attn4Problem p, int max_row_tiles) {
+// keys: one launch, no line to lay out first, no workspace.  CLUSTER: `ctas`
+// CTAs per unit, which take equal parts of its keys and join what their warps
+// joined through distributed shared memory.
+template <int D, int NT, int W, bool CLUSTER>
+__global__ void __launch_bounds__(W * 32, kWarps<NT> / W) fa2_kv4_attn_unit_kernel(const Attn4Problem p, int max_row_tiles,
+                                                                                   int ctas) {
   constexpr int kRows = 8 * NT, kCols = D >= 32 ? D / 32 : 1;
   extern __shared__ __align__(128) char smem[];
   WarpSmem<D, NT>* const all = reinterpret_cast<WarpSmem<D, NT>*>(smem);
@@ -989,28 +992,67 @@ __global__ void __launch_bounds__(W * 32, kWarps<NT> / W) fa2_kv4_attn_unit_kern
   start_warp(ws, s, ring, lane);
   griddep_wait();
   griddep_launch_dependents();
-  const int h = blockIdx.x % p.cache.heads;
+  const int unit = CLUSTER ? blockIdx.x / ctas : blockIdx.x, rank = CLUSTER ? static_cast<int>(cluster_rank()) : 0;
+  const int h = unit % p.cache.heads;
   {  // (a request that is left out may have no CTA: all are looked at)
     const long long i = static_cast<long long>(blockIdx.x) * (W * 32) + threadIdx.x;
     if (i < p.B && !request(p, static_cast<int>(i)).ok) atomicCAS(&g_attn4_status, kDevOk, kDevBadSeqlens);
   }
   int b, rt;
-  if (!find_tile<kRows>(p, max_row_tiles, blockIdx.x / p.cache.heads, lane, b, rt)) return;
+  if (!find_tile<kRows>(p, max_row_tiles, unit / p.cache.heads, lane, b, rt)) return;
   const Request rq = request(p, b);
   if (!rq.ok || static_cast<long long>(rt) * kRows >= p.G * rq.Lq) return;
   const int row0 = rt * kRows, rows = p.G * rq.Lq;
-  const int np = key_pairs(rq), each = (np + W - 1) / W;
-  const int first = warp * each, n = min(each, np - first);
+  const int np = key_pairs(rq);
+  // the CTA's pairs, and each warp's
+  const int from = CLUSTER ? static_cast<int>(static_cast<long long>(np) * rank / ctas) : 0;
+  const int size = CLUSTER ? static_cast<int>(static_cast<long long>(np) * (rank + 1) / ctas) - from : np;
+  const int each = (size + W - 1) / W, n = min(each, size - warp * each);
   // (a warp whose copy did not come leaves the unit's rows wrong, with the
   // status word set: the others must not wait for it)
-  if (n > 0 && run_pairs<D, NT>(s, ring, p, rq, b, h, row0, first, n, lane))
+  if (n > 0 && run_pairs<D, NT>(s, ring, p, rq, b, h, row0, from + warp * each, n, lane))
     end_unit<D, NT>(s, p, rq, h, row0, reinterpret_cast<float*>(ws->tiles), ws->ml, lane);
   __syncthreads();
-  const int parts = each > 0 ? (np + each - 1) / each : 0;
+  const int parts = each > 0 ? (size + each - 1) / each : 0;
+  // (a row joined in the CTA goes where the queries were, its maximum and sum behind it)
+  auto joined = [&](int local) { return reinterpret_cast<float*>(all[local % W].q) + local / W * (D + 2); };
+  static_assert((kRows + W - 1) / W * (D + 2) * sizeof(float) <= sizeof(ws->q), "rows fit");
   for (int local = warp; local < kRows && row0 + local < rows; local += W) {
     float o[kCols], l, top;
     join_row<D, NT>(all, parts, local, o, l, top, lane);
-    write_row<D>(p, rq, h, row0 + local, o, l, top, lane);
+    if constexpr (!CLUSTER) {
+      write_row<D>(p, rq, h, row0 + local, o, l, top, lane);
+    } else {
+      float* const row = joined(local);
+#pragma unroll
+      for (int k = 0; k < kCols; ++k)
+        if (lane * kCols < D) row[lane * kCols + k] = o[k];
+      if (lane == 0) row[D] = top, row[D + 1] = l;
+    }
+  }
+  if constexpr (CLUSTER) {
+    cluster_sync();
+    for (int local = rank + ctas * warp; local < kRows && row0 + local < rows; local += ctas * W) {
+      const uint32_t row = smem_u32(joined(local));
+      const float m = lane < ctas ? load_cluster_f32(row + D * 4, lane) : kNoMax;
+      float l = lane < ctas ? load_cluster_f32(row + D * 4 + 4, lane) : 0.f, top = m, o[kCols];
+#pragma unroll
+      for (int sh = 16; sh > 0; sh >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, sh));
+      const float w = ex2_approx(m - top);
+      l *= w;
+#pragma unroll
+      for (int sh = 16; sh > 0; sh >>= 1) l += __shfl_xor_sync(0xffffffffu, l, sh);
+#pragma unroll
+      for (int k = 0; k < kCols; ++k) o[k] = 0.f;
+      for (int i = 0; i < ctas; ++i) {
+        const float wi = __shfl_sync(0xffffffffu, w, i);
+#pragma unroll
+        for (int k = 0; k < kCols; ++k)
+          if (lane * kCols < D) o[k] = fmaf(wi, load_cluster_f32(row + (lane * kCols + k) * 4, i), o[k]);
+      }
+      write_row<D>(p, rq, h, row0 + local, o, l, top, lane);
+    }
+    cluster_sync();  // (no CTA leaves while another reads its rows)
   }
 }
 
@@ -1049,6 +1091,22 @@ inline int unit_warps(int B, int H_kv, long long max_rows, long long max_keys) {
   return max_keys <= (wide ? 1024 : 2048) && (units <= 152 * 8 || max_keys >= 128) ? kFew : 0;
 }
 
+// CTAs of a unit: a cluster of them where the keys are enough to make up for
+// what the cluster costs (about 2 us) and its CTAs find SMs side by side
+// (not 16 clusters of 8).  Measured as above, one CTA / two / four / eight:
+//   8 units    512 keys   6.2 / 6.9 / 6.7 / 6.9   1000   8.1 / 8.3 / 7.4 / 7.1   2048  11.1 / 9.9 / 8.5 / 7.4
+//   16 units  1000 keys   8.2 / 8.3 / 7.5 / 13.1  2048  11.4 / 9.8 / 8.5 / 13.4
+//   32 units  1000 keys   8.3 / 8.3 / 7.5         2048  11.4 / 9.9 / 8.6
+//   64 units  1000 keys   8.3 / 8.4               2048  11.4 / 10.1              4096  17.7 / 13.3
+//   16 rows a unit, 4 units 512 keys 9.0 / 9.7 / 9.0 / 9.0, 1000 12.2 / 11.0 / 10.4 / 9.5, 2048 17.2 / 14.0 / 11.7 / 10.7
+//   64 units   512 keys   9.6 / 10.3              1000  12.4 / 11.5              2048  17.5 / 14.4
+// (max_keys is a bound: the thresholds leave room for shorter requests).
+inline int unit_ctas(long long units, bool wide, int max_keys) {
+  if (max_keys <= (wide ? 512 : 1024) || units > 64) return 1;
+  if (units > 32) return max_keys > (wide ? 768 : 1536) ? 2 : 1;
+  return units > 8 ? 4 : 8;
+}
+
 template <int D, int NT>
 int launch_attn_d(Attn4Problem p, long long max_rows, cudaStream_t st) {
   constexpr int kRows = 8 * NT, kSmem = kWarps<NT> * sizeof(WarpSmem<D, NT>);
@@ -1063,10 +1121,15 @@ int launch_attn_d(Attn4Problem p, long long max_rows, cudaStream_t st) {
     units = tiles * p.cache.heads;
   }
   if (const int w = unit_warps(p.B, p.cache.heads, max_rows, p.max_k)) {
-    const auto kernel = w == kFew ? fa2_kv4_attn_unit_kernel<D, NT, kFew> : fa2_kv4_attn_unit_kernel<D, NT, kWarps<NT>>;
     const int smem = w * static_cast<int>(sizeof(WarpSmem<D, NT>));
+    const int ctas = w == kFew ? 1 : unit_ctas(units, NT == 2, p.max_k);
+    const auto kernel = w == kFew  ? fa2_kv4_attn_unit_kernel<D, NT, kFew, false>
+                        : ctas > 1 ? fa2_kv4_attn_unit_kernel<D, NT, kWarps<NT>, true>
+                                   : fa2_kv4_attn_unit_kernel<D, NT, kWarps<NT>, false>;
     if (int e = ensure_max_smem(reinterpret_cast<const void*>(kernel), smem)) return e;
-    return launch_pdl(kernel, dim3(static_cast<unsigned>(units)), dim3(w * 32), smem, st, p, row_tiles);
+    const dim3 grid(static_cast<unsigned>(units * ctas)), block(w * 32);
+    return ctas > 1 ? launch_pdl_cluster(kernel, grid, block, smem, st, ctas, p, row_tiles, ctas)
+                    : launch_pdl(kernel, grid, block, smem, st, p, row_tiles, ctas);
   }
   // Spans of a unit, were all requests of one length: with few, a warp of the
   // combine kernel joins a row alone; with more a CTA's eight do; with many the
