@@ -531,6 +531,13 @@ const char* fa2_last_error_detail(void);
  * every wait in the attention kernels does after 2 s).  Faults nothing. */
 int fa2_check_wait_timeout(int timeout_us, int* status_out);
 
+/* The same for waits that a warp makes together: a phase that completes after
+ * late_us (100 .. 1e6) microseconds, which is in time for the odd lanes'
+ * limits and too late for the even ones', then one that is in time for all.
+ * lanes_out[0 .. 1]: the lanes that were told "in time", which have to be none
+ * and all 32 (lanes of one warp must not part). */
+int fa2_check_warp_wait(int late_us, unsigned* lanes_out);
+
 /* ABI version of this header (major * 100 + minor). */
 int fa2_abi_version(void);
 

@@ -36,6 +36,14 @@ def test_bounded_wait_reports_timeout_and_context_survives():
     check_lse(to_np(lse), ref_l)
 
 
+def test_lanes_of_a_warp_give_up_together():
+    """A phase that completes between the lanes' limits: no lane goes on while another has given up."""
+    lanes = (ctypes.c_uint * 2)(7, 7)
+    assert fa2.load_library().fa2_check_warp_wait(4000, lanes) == 0
+    assert list(lanes) == [0, 0xFFFFFFFF]
+    assert fa2.load_library().fa2_check_warp_wait(50, lanes) == 2 and fa2.load_library().fa2_check_warp_wait(1000, None) == 1
+
+
 def test_bounded_wait_argument_checks():
     lib = fa2.load_library()
     st = ctypes.c_int(0)

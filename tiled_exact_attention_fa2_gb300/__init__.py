@@ -70,6 +70,7 @@ _SIGNATURES = {
     "fa2_bwd_gqa_ws": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _f, _i, _vp, _sz,
                             _vp]),
     "fa2_check_wait_timeout": (_i, [_i, ctypes.POINTER(_i)]),
+    "fa2_check_warp_wait": (_i, [_i, ctypes.POINTER(ctypes.c_uint)]),
     "fa2_fwd_splitkv_workspace_bytes": (_sz, [_i, _i, _i, _i, _i, _i]),
     "fa2_fwd_splitkv_suggest_splits": (_i, [_i, _i, _i, _i, _i, _i]),
     "fa2_fwd_splitkv": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _f, _i, _i, _vp, _sz, _vp]),

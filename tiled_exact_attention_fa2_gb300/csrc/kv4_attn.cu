@@ -684,9 +684,9 @@ __device__ __forceinline__ bool run_pairs(Rows<D, NT>& s, Ring& ring, const Attn
   start_unit<D, NT>(s, p, rq, h, row0, lane);
   const int whole = s.min_vis / kPairKeys;  // every row sees all keys of the pairs below
   for (int pair = first; pair < first + n; ++pair) {
-    if (!mbar_wait(&ring.full[ring.slot], ring.phase, &g_attn4_status)) {
+    if (!mbar_wait_warp(&ring.full[ring.slot], ring.phase, &g_attn4_status)) {
       // a copy that never came: wait (as long again) for the other, then give up
-      if (pair + 1 < first + n) mbar_wait(&ring.full[ring.slot ^ 1], ring.phase ^ ring.slot, &g_attn4_status);
+      if (pair + 1 < first + n) mbar_wait_warp(&ring.full[ring.slot ^ 1], ring.phase ^ ring.slot, &g_attn4_status);
       return false;
     }
     const uint32_t tiles = ring.tiles + ring.slot * (kPair * Kv4<D>::kTileBytes);

@@ -128,6 +128,15 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, int* s
   }
 }
 
+// The same for a warp whose lanes go on together: one answer for all of them,
+// true where every lane saw the phase complete in time.  (A phase that
+// completes as the limit runs out may be in time for some lanes only; lanes
+// that went separate ways would miss each other's votes and barriers.)
+__device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, int* status,
+                                               uint64_t timeout_ns = FA2_WAIT_TIMEOUT_NS) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, status, timeout_ns));
+}
+
 // Sleeping variant for long, non-critical waits.
 __device__ __forceinline__ bool mbar_wait_sleep(uint64_t* bar, uint32_t parity, int* status) {
   return mbar_wait<true>(bar, parity, status);
