@@ -1,0 +1,62 @@
+"""The 4-bit paged cache where its calls meet what a caller gets wrong or leaves empty."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import tiled_exact_attention_fa2_gb300 as fa2
+from test_kv4 import check_attention, filled, i32
+
+
+# ---------------------------------------------------------------- GPU
+@pytest.mark.gpu
+@pytest.mark.parametrize("B,most,H,Hkv,d", [(40, 300, 4, 1, 128), (70, 90, 3, 3, 16), (1100, 200, 2, 1, 32)])
+def test_a_wrong_query_offset_costs_only_its_own_requests(B, most, H, Hkv, d):
+    """Ragged queries: an offset far too small or too large takes the two requests it belongs to, and no other, in both
+    forms of the kernel."""
+    rng = np.random.default_rng(B)
+    nqs = rng.integers(1, 3, B)
+    nqs[[0, B // 2, B - 1]] = [most // 2, most, 5]
+    lens = rng.integers(0, 40 if B < 1000 else 5, B)
+    lens[[0, B // 2, B - 1]] = [most, most + 100, 3]
+    cache, table, kv = filled(rng, [int(x) for x in lens], Hkv, 16, d, width=64)
+    cu = np.r_[0, np.cumsum(nqs)]
+    total = int(cu[-1])
+    q = torch.from_numpy(rng.standard_normal((total, H, d))).to(torch.bfloat16).cuda()
+    q64 = q.double().cpu().numpy()
+    fa2.fa2_device_status(reset=True)
+    for bound in (most + 100, 1 << 20):
+        tab = i32(table) if bound < 1 << 20 else torch.cat([i32(table), torch.zeros((B, 100), dtype=torch.int32, device="cuda")], 1)
+        # (the second request, one in the middle of the long ones', where a search would look first, the last but one)
+        for at in (1, B // 3, B // 2 + 1, 8 * (B // 16), B - 1):
+            for x in (-7, total + 1000):
+                wrong = cu.copy()
+                wrong[at] = x
+                o, lse = torch.full_like(q, 9.0), torch.full((H, total), 9.0, device="cuda")
+                fa2.fa2_kv4_attn(q, cache, tab, i32(lens), i32(wrong), most, max_seqlen_k=bound, o=o, lse=lse)
+                assert fa2.fa2_device_status(reset=True) == 3
+                gone = slice(int(cu[at - 1]), int(cu[at + 1]))
+                assert torch.all(o[gone] == 9) and torch.all(lse[:, gone] == 9)
+                rows = [(int(cu[b]), int(cu[b + 1])) if b not in (at - 1, at) else (0, 0) for b in range(B)]
+                check_attention(o, lse, rows, q64, kv, 1 / math.sqrt(d), True, H)
+
+
+@pytest.mark.gpu
+def test_query_offsets_that_overlap():
+    """Offsets that go up and down give the same rows to several requests, and a tile's number to several tiles: every
+    request whose own offsets are in range is computed (here they all have the same keys, so it does not show which
+    wrote a row last)."""
+    rng = np.random.default_rng(3)
+    B, H, Hkv, d, most = 48, 4, 1, 64, 64
+    cache, table, kv = filled(rng, [90], Hkv, 16, d, width=64)
+    cu = np.zeros(B + 1, np.int64)
+    cu[1::2] = most  # requests 0, 2, ...: all 64 rows; 1, 3, ...: backwards
+    q = torch.from_numpy(rng.standard_normal((most, H, d))).to(torch.bfloat16).cuda()
+    fa2.fa2_device_status(reset=True)
+    for width in (0, 100):
+        tab = torch.cat([i32(table), torch.zeros((1, width), dtype=torch.int32, device="cuda")], 1).expand(B, -1).contiguous()
+        o, lse = torch.full_like(q, 9.0), torch.full((H, most), 9.0, device="cuda")
+        fa2.fa2_kv4_attn(q, cache, tab, i32([90] * B), i32(cu), most, o=o, lse=lse)
+        assert fa2.fa2_device_status(reset=True) == 3
+        check_attention(o, lse, [(0, most)], q.double().cpu().numpy(), kv, 1 / math.sqrt(d), True, H)

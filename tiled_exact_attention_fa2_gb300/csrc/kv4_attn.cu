@@ -57,6 +57,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <climits>
 #include <cmath>
 
 #include "args.h"
@@ -102,10 +103,11 @@ struct Attn4Problem {
   const int* cu_q;    // or NULL: every request has uniform_q queries
   float* part;        // [2 * spans][rows][d] unnormalised O
   float2* part_ml;    // [2 * spans][rows] maximum (log2), sum
-  long long* start;   // [B + 1] first tile pair of each request on the line
+  long long* start;   // [B + 1] first tile pair of each request on the line; then, for the search, whether offsets are out of order
   int B, H, G, total_q, uniform_q, max_q, max_k;
   float scale_log2, v_scale;
   int causal;
+  int ragged;         // the grids count row tiles (below) instead of requests times the most of one
 };
 
 struct Request {
@@ -113,18 +115,30 @@ struct Request {
   bool ok;
 };
 
+// The query rows of request b; false where they are out of range.
+__device__ __forceinline__ bool queries(const Attn4Problem& p, int b, int& q0, int& Lq) {
+  if (p.cu_q) {
+    q0 = __ldg(p.cu_q + b);
+    Lq = __ldg(p.cu_q + b + 1) - q0;
+  } else {
+    q0 = b * p.uniform_q;
+    Lq = p.uniform_q;
+  }
+  return q0 >= 0 && Lq >= 0 && Lq <= p.max_q && q0 <= p.total_q - Lq;
+}
+
+// Whether the offsets go down at request b or begin below 0; if they do at
+// none, all are in order.
+__device__ __forceinline__ bool out_of_order(const Attn4Problem& p, int b) {
+  const int q0 = __ldg(p.cu_q + b);
+  return q0 < 0 || __ldg(p.cu_q + b + 1) < q0;
+}
+
 // A request with impossible lengths is left out (its rows are not written).
 __device__ __forceinline__ Request request(const Attn4Problem& p, int b) {
   Request r;
   r.Lk = __ldg(p.lens + b);
-  if (p.cu_q) {
-    r.q0 = __ldg(p.cu_q + b);
-    r.Lq = __ldg(p.cu_q + b + 1) - r.q0;
-  } else {
-    r.q0 = b * p.uniform_q;
-    r.Lq = p.uniform_q;
-  }
-  r.ok = r.Lk >= 0 && r.Lk <= p.max_k && r.q0 >= 0 && r.Lq >= 0 && r.Lq <= p.max_q && r.q0 <= p.total_q - r.Lq;
+  r.ok = queries(p, b, r.q0, r.Lq) && r.Lk >= 0 && r.Lk <= p.max_k;
   return r;
 }
 
@@ -134,20 +148,23 @@ __device__ __forceinline__ int row_tiles(const Attn4Problem& p, const Request& r
 }
 __device__ __forceinline__ int key_pairs(const Request& r) { return (r.Lk + kPairKeys - 1) / kPairKeys; }
 
-// The request and row tile that number t of a K/V head's grid stands for.
-// max_row_tiles > 0: that many for every request.  0: where a few requests
-// have most of the queries, room for as many tiles as total_q and B allow:
-// request b's tiles are numbers G cu_q[b] / ROWS + b on, which is past those
-// of the one before (its G Lq rows touch at most that many tiles); b is found
-// by a search 32 wide.  False where no tile has the number.
+// Row tiles of a K/V head's grid are numbered.  Where the grid has
+// `max_row_tiles` for every request, t is tile t mod max_row_tiles of request
+// t / max_row_tiles.  Where a few requests have most of the queries it has as
+// many as total_q and B allow, and request b's are numbers G cu_q[b] / ROWS + b
+// on: past those of the one before if the offsets are in order, since its
+// G Lq rows touch at most that many tiles.
 template <int ROWS>
-__device__ __forceinline__ bool find_tile(const Attn4Problem& p, int max_row_tiles, int t, int lane, int& b, int& rt) {
-  if (max_row_tiles > 0) {
-    b = t / max_row_tiles;
-    rt = t - b * max_row_tiles;
-    return true;
-  }
-  auto number = [&](int i) { return static_cast<long long>(p.G) * __ldg(p.cu_q + i) / ROWS + i; };
+__device__ __forceinline__ long long first_tile(const Attn4Problem& p, int q0, int b) {
+  return static_cast<long long>(p.G) * q0 / ROWS + b;
+}
+
+// The request and the tile of it that number t stands for, found by a search
+// 32 wide; right where the offsets are in order.  False where no request has
+// it.
+template <int ROWS>
+__device__ __forceinline__ bool search_tile(const Attn4Problem& p, int t, int lane, int& b, int& rt) {
+  auto number = [&](int i) { return first_tile<ROWS>(p, __ldg(p.cu_q + i), i); };
   b = 0;
   for (int n = p.B; n > 0;) {
     const int step = (n + 31) / 32, i = lane * step;
@@ -162,9 +179,45 @@ __device__ __forceinline__ bool find_tile(const Attn4Problem& p, int max_row_til
   return true;
 }
 
+// The same by asking every request from `from` on, a lane each, whether the
+// number is one of its own: right whatever the offsets are, so that a wrong one
+// costs no request but those it belongs to.  (Offsets out of order can give a
+// number to several requests: `more`.)
+template <int ROWS>
+__device__ __forceinline__ bool scan_tile(const Attn4Problem& p, int t, int from, int lane, int& b, int& rt, bool& more) {
+  int mine = INT_MAX, tile = 0, count = 0;
+#pragma unroll 4
+  for (int i = from + lane; i < p.B; i += 32) {  // (unrolled: the loads of four requests at once)
+    int q0, Lq;
+    const bool there = queries(p, i, q0, Lq);
+    const long long rel = t - first_tile<ROWS>(p, q0, i);
+    if (there && rel >= 0 && rel * ROWS < static_cast<long long>(p.G) * Lq && count++ == 0)
+      mine = i, tile = static_cast<int>(rel);
+  }
+  b = __reduce_min_sync(0xffffffffu, mine);
+  rt = __shfl_sync(0xffffffffu, tile, (b - from) & 31);
+  more = __reduce_add_sync(0xffffffffu, count) > 1;
+  return b < INT_MAX;
+}
+
 template <int ROWS>
 __device__ __forceinline__ long long pairs_of(const Attn4Problem& p, const Request& r) {
   return r.ok ? static_cast<long long>(p.cache.heads) * row_tiles<ROWS>(p, r) * key_pairs(r) : 0;
+}
+
+// The next unit, from unit k of request b on (k: its row tile times H_kv plus
+// its head), whose number the search takes for another's.
+template <int ROWS>
+__device__ __forceinline__ bool next_lost(const Attn4Problem& p, int& b, int& k, int lane) {
+  for (; b < p.B; ++b, k = 0) {
+    const Request r = request(p, b);
+    for (const int units = r.ok ? row_tiles<ROWS>(p, r) * p.cache.heads : 0; k < units; ++k) {
+      const int t = static_cast<int>(first_tile<ROWS>(p, r.q0, b)) + k / p.cache.heads;
+      int found, rt;
+      if (!search_tile<ROWS>(p, t, lane, found, rt) || found != b) return true;
+    }
+  }
+  return false;
 }
 
 __device__ __forceinline__ long long quotient(long long a, long long b) {
@@ -790,6 +843,13 @@ __global__ void __launch_bounds__(kWarps<NT> * 32, 1) fa2_kv4_attn_kernel(const 
     if (lane == 31) p.start[p.B] = total;
     if (!fine) atomicCAS(&g_attn4_status, kDevOk, kDevBadSeqlens);
   }
+  if (!JOIN && p.ragged && blockIdx.x == kCtas - 1 && warp == kWarps<NT> - 1) {  // (the warp with the least to do)
+    bool mixed = false;
+#pragma unroll 4
+    for (int b = lane; b < p.B; b += 32) mixed |= out_of_order(p, b);
+    mixed = __any_sync(0xffffffffu, mixed);
+    if (lane == 0) p.start[p.B + 1] = mixed;
+  }
   const Line<NT> line(total);
   if (warp >= line.warps) return;
   const int span = blockIdx.x * line.warps + warp;
@@ -854,26 +914,11 @@ __global__ void __launch_bounds__(kWarps<NT> * 32, 1) fa2_kv4_attn_kernel(const 
   }
 }
 
-// Join the partial results of the units that several spans share, in span
-// order, and write the rows that see no key.  A CTA of 8 warps takes 8 / WPR
-// rows of a unit, WPR warps each.  Bound by the latency of what it reads one
-// after the other (where the unit's spans are, their maxima and sums, their
-// rows), so each of the three is one round of loads: a lane per span for the
-// maxima, then the rows of kBatch spans at once.
+// One row of a unit in the combine kernel below, for warp `part` of its WPR.
 template <int D, int ROWS, int WPR, bool JOIN>
-__global__ void __launch_bounds__(256) fa2_kv4_combine_kernel(const Attn4Problem p, int max_row_tiles) {
-  constexpr int kCols = D >= 32 ? D / 32 : 1, kRowsCta = 8 / WPR, kBatch = 8;
-  __shared__ float s_o[WPR > 1 ? 8 : 1][D];
-  __shared__ float s_m[8], s_l[8];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int id = blockIdx.x;
-  const int local = (id % (ROWS / kRowsCta)) * kRowsCta + warp / WPR, part = warp % WPR;
-  id /= ROWS / kRowsCta;
-  const int h = id % p.cache.heads;
-  griddep_wait();
-  griddep_launch_dependents();
-  int b, rt;
-  if (!find_tile<ROWS>(p, max_row_tiles, id / p.cache.heads, lane, b, rt)) return;
+__device__ __forceinline__ void combine_row(const Attn4Problem& p, int b, int h, int rt, int local, int part,
+                                            float (*s_o)[D], float* s_m, float* s_l, int lane, int warp) {
+  constexpr int kCols = D >= 32 ? D / 32 : 1, kBatch = 8;
   const long long start = p.start[b], total = p.start[p.B];
   const Request rq = request(p, b);
   const long long row = static_cast<long long>(rt) * ROWS + local;
@@ -974,34 +1019,51 @@ __global__ void __launch_bounds__(256) fa2_kv4_combine_kernel(const Attn4Problem
   write_row<D>(p, rq, h, r, o, l, top, lane);
 }
 
-// Short requests: one CTA of W warps per unit, which take equal parts of its
-// keys and join their partial results in shared memory, in the order of the
-// keys: one launch, no line to lay out first, no workspace.  CLUSTER: `ctas`
-// CTAs per unit, which take equal parts of its keys and join what their warps
-// joined through distributed shared memory.
-template <int D, int NT, int W, bool CLUSTER>
-__global__ void __launch_bounds__(W * 32, kWarps<NT> / W) fa2_kv4_attn_unit_kernel(const Attn4Problem p, int max_row_tiles,
-                                                                                   int ctas) {
-  constexpr int kRows = 8 * NT, kCols = D >= 32 ? D / 32 : 1;
-  extern __shared__ __align__(128) char smem[];
-  WarpSmem<D, NT>* const all = reinterpret_cast<WarpSmem<D, NT>*>(smem);
+// Join the partial results of the units that several spans share, in span
+// order, and write the rows that see no key.  A CTA of 8 warps takes 8 / WPR
+// rows of a unit, WPR warps each.  Bound by the latency of what it reads one
+// after the other (where the unit's spans are, their maxima and sums, their
+// rows), so each of the three is one round of loads: a lane per span for the
+// maxima, then the rows of kBatch spans at once.
+template <int D, int ROWS, int WPR, bool JOIN>
+__global__ void __launch_bounds__(256) fa2_kv4_combine_kernel(const Attn4Problem p, int max_row_tiles) {
+  constexpr int kRowsCta = 8 / WPR;
+  __shared__ float s_o[WPR > 1 ? 8 : 1][D];
+  __shared__ float s_m[8], s_l[8];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  WarpSmem<D, NT>* const ws = all + warp;
-  Rows<D, NT> s;
-  Ring ring;
-  start_warp(ws, s, ring, lane);
+  int id = blockIdx.x;
+  const int local = (id % (ROWS / kRowsCta)) * kRowsCta + warp / WPR, part = warp % WPR;
+  id /= ROWS / kRowsCta;
+  const int h = id % p.cache.heads;
   griddep_wait();
   griddep_launch_dependents();
-  const int unit = CLUSTER ? blockIdx.x / ctas : blockIdx.x, rank = CLUSTER ? static_cast<int>(cluster_rank()) : 0;
-  const int h = unit % p.cache.heads;
-  {  // (a request that is left out may have no CTA: all are looked at)
-    const long long i = static_cast<long long>(blockIdx.x) * (W * 32) + threadIdx.x;
-    if (i < p.B && !request(p, static_cast<int>(i)).ok) atomicCAS(&g_attn4_status, kDevOk, kDevBadSeqlens);
+  const int t = id / p.cache.heads;
+  int b = t, rt = 0;
+  bool there = true, more = false;
+  if (max_row_tiles > 0) {
+    b = t / max_row_tiles;
+    rt = t - b * max_row_tiles;
+  } else if (WPR == 1) {  // (many units)
+    const long long mixed = p.start[p.B + 1];
+    there = search_tile<ROWS>(p, t, lane, b, rt);
+    if (mixed) there = scan_tile<ROWS>(p, t, 0, lane, b, rt, more);
+  } else {
+    there = scan_tile<ROWS>(p, t, 0, lane, b, rt, more);
   }
-  int b, rt;
-  if (!find_tile<kRows>(p, max_row_tiles, unit / p.cache.heads, lane, b, rt)) return;
-  const Request rq = request(p, b);
-  if (!rq.ok || static_cast<long long>(rt) * kRows >= p.G * rq.Lq) return;
+  while (there) {  // (of a call as it should be: once)
+    combine_row<D, ROWS, WPR, JOIN>(p, b, h, rt, local, part, s_o, s_m, s_l, lane, warp);
+    if (!more) return;
+    if (WPR > 1) __syncthreads();  // (what the row's warps left has been read)
+    there = scan_tile<ROWS>(p, t, b + 1, lane, b, rt, more);
+  }
+}
+
+// A unit in the kernel below.  `fine`: the warp's copies have all come.
+template <int D, int NT, int W, bool CLUSTER>
+__device__ __forceinline__ void run_unit(Rows<D, NT>& s, Ring& ring, bool& fine, WarpSmem<D, NT>* all, const Attn4Problem& p,
+                                         const Request& rq, int b, int h, int rt, int rank, int ctas, int lane, int warp) {
+  constexpr int kRows = 8 * NT, kCols = D >= 32 ? D / 32 : 1;
+  WarpSmem<D, NT>* const ws = all + warp;
   const int row0 = rt * kRows, rows = p.G * rq.Lq;
   const int np = key_pairs(rq);
   // the CTA's pairs, and each warp's
@@ -1010,8 +1072,10 @@ __global__ void __launch_bounds__(W * 32, kWarps<NT> / W) fa2_kv4_attn_unit_kern
   const int each = (size + W - 1) / W, n = min(each, size - warp * each);
   // (a warp whose copy did not come leaves the unit's rows wrong, with the
   // status word set: the others must not wait for it)
-  if (n > 0 && run_pairs<D, NT>(s, ring, p, rq, b, h, row0, from + warp * each, n, lane))
-    end_unit<D, NT>(s, p, rq, h, row0, reinterpret_cast<float*>(ws->tiles), ws->ml, lane);
+  if (n > 0 && fine) {
+    fine = run_pairs<D, NT>(s, ring, p, rq, b, h, row0, from + warp * each, n, lane);
+    if (fine) end_unit<D, NT>(s, p, rq, h, row0, reinterpret_cast<float*>(ws->tiles), ws->ml, lane);
+  }
   __syncthreads();
   const int parts = each > 0 ? (size + each - 1) / each : 0;
   // (a row joined in the CTA goes where the queries were, its maximum and sum behind it)
@@ -1053,6 +1117,65 @@ __global__ void __launch_bounds__(W * 32, kWarps<NT> / W) fa2_kv4_attn_unit_kern
       write_row<D>(p, rq, h, row0 + local, o, l, top, lane);
     }
     cluster_sync();  // (no CTA leaves while another reads its rows)
+  }
+}
+
+// Short requests: one CTA of W warps per unit, which take equal parts of its
+// keys and join their partial results in shared memory, in the order of the
+// keys: one launch, no line to lay out first, no workspace.  CLUSTER: `ctas`
+// CTAs per unit, which take equal parts of its keys and join what their warps
+// joined through distributed shared memory.
+template <int D, int NT, int W, bool CLUSTER>
+__global__ void __launch_bounds__(W * 32, kWarps<NT> / W) fa2_kv4_attn_unit_kernel(const Attn4Problem p, int max_row_tiles,
+                                                                                   int ctas) {
+  constexpr int kRows = 8 * NT;
+  extern __shared__ __align__(128) char smem[];
+  WarpSmem<D, NT>* const all = reinterpret_cast<WarpSmem<D, NT>*>(smem);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  Rows<D, NT> s;
+  Ring ring;
+  start_warp(all + warp, s, ring, lane);
+  griddep_wait();
+  griddep_launch_dependents();
+  const int unit = CLUSTER ? blockIdx.x / ctas : blockIdx.x, rank = CLUSTER ? static_cast<int>(cluster_rank()) : 0;
+  // (a request that is left out may have no CTA: all are looked at)
+  const long long first = static_cast<long long>(blockIdx.x) * (W * 32), mine = first + threadIdx.x;
+  bool mixed = false;
+  if (mine < p.B) {
+    if (!request(p, static_cast<int>(mine)).ok) atomicCAS(&g_attn4_status, kDevOk, kDevBadSeqlens);
+    mixed = max_row_tiles == 0 && out_of_order(p, static_cast<int>(mine));
+  }
+  // Which unit this is.  With a full CTA for each, requests are few (one an SM
+  // at most) and all asked.  Else the number is searched for, and a CTA that
+  // has found offsets out of order takes the units that no search finds too.
+  constexpr bool kSearch = W == kFew;
+  const int t = unit / p.cache.heads;
+  int h = unit % p.cache.heads, b = t, rt = 0;
+  bool there = true, more = false, fine = true;
+  if (max_row_tiles > 0) {
+    b = t / max_row_tiles;
+    rt = t - b * max_row_tiles;
+  } else {
+    there = kSearch ? search_tile<kRows>(p, t, lane, b, rt) : scan_tile<kRows>(p, t, 0, lane, b, rt, more);
+    if (kSearch && first < p.B) more = __syncthreads_or(mixed);
+  }
+  for (int lost = 0;;) {  // (of a call as it should be: once)
+    if (there) {
+      const Request rq = request(p, b);
+      if (rq.ok && static_cast<long long>(rt) * kRows < p.G * rq.Lq)
+        run_unit<D, NT, W, CLUSTER>(s, ring, fine, all, p, rq, b, h, rt, rank, ctas, lane, warp);
+    }
+    if (!more) return;
+    __syncthreads();  // (what the unit's warps left has been read)
+    if (kSearch) {
+      if (lost == 0) b = 0;  // from the first request's first unit on
+      more = there = next_lost<kRows>(p, b, lost, lane);
+      rt = lost / p.cache.heads;
+      h = lost % p.cache.heads;
+      ++lost;
+    } else {
+      there = scan_tile<kRows>(p, t, b + 1, lane, b, rt, more);
+    }
   }
 }
 
@@ -1119,6 +1242,7 @@ int launch_attn_d(Attn4Problem p, long long max_rows, cudaStream_t st) {
   if (p.cu_q && tiles < static_cast<long long>(p.B) * row_tiles / 2) {
     row_tiles = 0;
     units = tiles * p.cache.heads;
+    p.ragged = 1;
   }
   if (const int w = unit_warps(p.B, p.cache.heads, max_rows, p.max_k)) {
     const int smem = w * static_cast<int>(sizeof(WarpSmem<D, NT>));
@@ -1190,7 +1314,7 @@ size_t fa2_kv4_attn_workspace_bytes(int B, int H, int H_kv, int max_seqlen_q, in
   if (unit_warps(B, H_kv, max_rows, max_seqlen_k)) return 0;
   const size_t rows = attn_slots(wide_rows(max_rows));
   return round_up(rows * d * sizeof(float)) + round_up(rows * sizeof(float2)) +
-         round_up((static_cast<size_t>(B) + 1) * sizeof(long long));
+         round_up((static_cast<size_t>(B) + 2) * sizeof(long long));
 }
 
 int fa2_kv4_attn(const void* q, const void* cache, long long page_stride, const int* block_table, long long table_stride,
