@@ -481,8 +481,9 @@ int fa2_kv4_gather(const void* cache, long long page_stride, const int* block_ta
  * Attention of new query tokens over the 4-bit cache.  q, o: packed
  * [total_q, H, d] bf16, lse: fp32 [H, total_q], as in fa2_fwd_varlen; request
  * b owns the query rows cu_seqlens_q[b] .. cu_seqlens_q[b+1] - 1 (DEVICE
- * int32 [B + 1], at most max_seqlen_q each; or NULL: every request has
- * max_seqlen_q rows, total_q = B * max_seqlen_q) and the first lens[b] tokens
+ * int32 [B + 1], at most max_seqlen_q each, 1 <= max_seqlen_q <= total_q; or
+ * NULL: every request has max_seqlen_q rows, total_q = B * max_seqlen_q) and
+ * the first lens[b] tokens
  * of its pages, block_table [B, table_width] (DEVICE int32, row stride
  * table_stride).  Query head h reads key/value head h / (H / H_kv).  With
  * causal != 0 a request's Lq queries are its last positions: query i sees key
@@ -500,7 +501,7 @@ int fa2_kv4_gather(const void* cache, long long page_stride, const int* block_ta
  * where that is 0: calls of short requests (max_seqlen_k up to 1024 or 2048,
  * for many rows or few) need none and take one launch, others two.  (It is 0 for invalid
  * sizes as well.)  Results do not vary from run to run.  total_q = 0 is
- * allowed and does nothing.
+ * allowed, with any max_seqlen_q >= 0, and does nothing.
  */
 size_t fa2_kv4_attn_workspace_bytes(int B, int H, int H_kv, int max_seqlen_q, int max_seqlen_k, int d);
 int fa2_kv4_attn(const void* q, const void* cache, long long page_stride, const int* block_table, long long table_stride,

@@ -6,10 +6,44 @@ import pytest
 import torch
 
 import tiled_exact_attention_fa2_gb300 as fa2
-from test_kv4 import check_attention, filled, i32
+from test_kv4 import A, attn, check_attention, filled, i32
+
+
+# ---------------------------------------------------------------- CPU
+@pytest.fixture(scope="module")
+def lib():
+    from tiled_exact_attention_fa2_gb300 import _build
+    _build.build()
+    return fa2.load_library()
+
+
+def test_no_queries_under_any_bound(lib):
+    for cu in (5 * A, None):
+        for mq in (0, 1, 7, 2 ** 31 - 1):
+            assert attn(lib, tq=0, mq=mq, cu=cu) == 0
+    assert attn(lib, tq=0, mq=-1) == 2 and attn(lib, tq=0, mq=1, B=0) == 2 and attn(lib, tq=0, mq=1, cache=None) == 1
 
 
 # ---------------------------------------------------------------- GPU
+@pytest.mark.gpu
+def test_query_bounds_above_the_rows_there_are():
+    """A step's rounded-up max_seqlen_q over fewer rows, and a step without any."""
+    rng = np.random.default_rng(4)
+    cache, table, kv = filled(rng, [40, 70], 2, 16, 64)
+    t, lens = i32(table), i32([40, 70])
+    q = torch.from_numpy(rng.standard_normal((5, 4, 64))).to(torch.bfloat16).cuda()
+    fa2.fa2_device_status(reset=True)
+    want = fa2.fa2_kv4_attn(q, cache, t, lens, i32([0, 2, 5]), 5)
+    check_attention(*want, [(0, 2), (2, 5)], q.double().cpu().numpy(), kv, 0.125, True, 4)
+    for bound in (8, 2 ** 31 - 1, 2 ** 40):
+        got = fa2.fa2_kv4_attn(q, cache, t, lens, i32([0, 2, 5]), bound)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    for bound in (0, 1, 8):
+        o, lse = fa2.fa2_kv4_attn(q[:0], cache, t, lens, i32([0, 0, 0]), bound)
+        assert o.shape == (0, 4, 64) and lse.shape == (4, 0)
+    assert fa2.fa2_device_status() == 0
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("B,most,H,Hkv,d", [(40, 300, 4, 1, 128), (70, 90, 3, 3, 16), (1100, 200, 2, 1, 32)])
 def test_a_wrong_query_offset_costs_only_its_own_requests(B, most, H, Hkv, d):

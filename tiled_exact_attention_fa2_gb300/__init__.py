@@ -902,8 +902,8 @@ def fa2_kv4_attn(q, cache, block_table, lens, cu_seqlens_q=None, max_seqlen_q: O
     (int32 [B, width]); its queries are rows cu_seqlens_q[b] .. of q, its last
     positions where ``causal``.  Without cu_seqlens_q every request has
     ``max_seqlen_q`` queries (default: total_q / B).  With cu_seqlens_q and no
-    max_seqlen_q the maximum is read from the offsets (a device sync).
-    ``max_seqlen_k`` bounds lens (default: what block_table has room for); a
+    max_seqlen_q the maximum is read from the offsets (a device sync); a bound
+    may be larger than any request's queries.  ``max_seqlen_k`` bounds lens (default: what block_table has room for); a
     tight bound lets short requests take a single launch without workspace.
     """
     dev = _gpu(cache, "cache")
@@ -919,7 +919,7 @@ def fa2_kv4_attn(q, cache, block_table, lens, cu_seqlens_q=None, max_seqlen_q: O
     _ints(lens, "lens", dev, B)
     if cu_seqlens_q is not None:
         _ints(cu_seqlens_q, "cu_seqlens_q", dev, B + 1)
-        mq = _max_len(cu_seqlens_q, max_seqlen_q)
+        mq = min(_max_len(cu_seqlens_q, max_seqlen_q), tq)
     else:
         mq = tq // max(B, 1) if max_seqlen_q is None else int(max_seqlen_q)
         if mq * B != tq:

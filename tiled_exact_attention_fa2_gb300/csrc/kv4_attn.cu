@@ -1280,8 +1280,9 @@ size_t attn_slots(bool wide) { return wide ? static_cast<size_t>(kSpans<2>) * 2 
 constexpr int kMaxKeys = 1 << 30;  // of a request: positions, rounded up, in 32 bits
 
 int check_attn_sizes(int B, int H, int H_kv, int total_q, int max_q, int d) {
-  if (B < 1 || H < 1 || total_q < 0 || max_q < 0 || total_q > (1 << 30) || max_q > total_q || (total_q > 0 && max_q < 1))
-    return FA2_ERR_SHAPE;
+  if (B < 1 || H < 1 || total_q < 0 || max_q < 0 || total_q > (1 << 30)) return FA2_ERR_SHAPE;
+  if (total_q == 0) max_q = 0;  // (a step without queries, whatever the bound)
+  if (max_q > total_q || (total_q > 0 && max_q < 1)) return FA2_ERR_SHAPE;
   if (!head_dim_ok(d)) return FA2_ERR_HEADDIM;
   if (int rc = check_heads(H, H_kv)) return rc;
   // combine grid: a CTA per row, rounded up to whole units
@@ -1327,7 +1328,7 @@ int fa2_kv4_attn(const void* q, const void* cache, long long page_stride, const 
   if (max_seqlen_k < 1) return FA2_ERR_SHAPE;
   if (max_seqlen_k > kMaxKeys) max_seqlen_k = kMaxKeys;
   if (static_cast<long long>(table_width) * page_size < max_seqlen_k) max_seqlen_k = table_width * page_size;
-  if (!cu_seqlens_q && total_q != 0 && static_cast<long long>(B) * max_seqlen_q != total_q) return FA2_ERR_SHAPE;
+  if (!cu_seqlens_q && total_q > 0 && static_cast<long long>(B) * max_seqlen_q != total_q) return FA2_ERR_SHAPE;
   if (check_scale(scale) || !power_of_two(k_scale) || !power_of_two(v_scale) || check_scale(scale * k_scale))
     return FA2_ERR_SCALE;
   if (total_q == 0) return FA2_OK;
