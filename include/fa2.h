@@ -468,10 +468,11 @@ int fa2_kv4_append(const void* k, const void* v, const long long* strides, void*
  * rows of a key/value head (queries times H / H_kv), 16 at a time, and from
  * some hundred rows on fa2_fwd_varlen on the gathered cache is faster (GB300,
  * 16 requests of up to 8192 keys, 8 key/value heads of 128 columns: 44 us for
- * 16 rows, 371 for 256; gather and fa2_fwd_varlen 345 for any of them).  Rows outside every sequence are not
- * written; rows of a sequence that its table row has no room for (status word
- * 3) or whose page id is outside [0, num_pages) (status word 5) neither.  One
- * launch.
+ * 16 rows, 371 for 256; gather and fa2_fwd_varlen 345 for any of them).  Rows
+ * outside every sequence (before the first, behind the last) are not written,
+ * nor are those past total; rows of a sequence that its table row has no room
+ * for (status word 3) or whose page id is outside [0, num_pages) (status word
+ * 5) neither.  One launch.
  */
 int fa2_kv4_gather(const void* cache, long long page_stride, const int* block_table, long long table_stride,
                    const int* cu_seqlens, void* k, void* v, int B, int H_kv, int total, int num_pages, int page_size,

@@ -94,3 +94,22 @@ def test_query_offsets_that_overlap():
         fa2.fa2_kv4_attn(q, cache, tab, i32([90] * B), i32(cu), most, o=o, lse=lse)
         assert fa2.fa2_device_status(reset=True) == 3
         check_attention(o, lse, [(0, most)], q.double().cpu().numpy(), kv, 1 / math.sqrt(d), True, H)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d,Hkv", [(16, 3), (128, 2)])
+def test_gather_behind_a_gap(d, Hkv):
+    """Rows before the first sequence and behind the last keep what they hold, and are no error; nor is a smaller total."""
+    rng = np.random.default_rng(d)
+    lens = [0, 33, 0, 20]
+    cache, table, kv = filled(rng, lens, Hkv, 16, d)
+    cu = 37 + np.r_[0, np.cumsum(lens)]
+    fa2.fa2_device_status(reset=True)
+    for total in (int(cu[-1]) + 9, int(cu[-1]) - 5, 37, 20):
+        k, v = (torch.full((total, Hkv, d), 9.0, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+        fa2.fa2_kv4_gather(cache, i32(table), i32(cu), total, k=k, v=v)
+        assert fa2.fa2_device_status(reset=True) == 0
+        for got, i in ((k, 0), (v, 1)):
+            want = np.full((max(total, int(cu[-1])), Hkv, d), 9.0)
+            want[37:int(cu[-1])] = np.concatenate([x[i].transpose(1, 0, 2) for x in kv])
+            assert np.array_equal(got.double().cpu().numpy(), want[:total])

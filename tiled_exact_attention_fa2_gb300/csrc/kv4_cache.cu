@@ -179,11 +179,11 @@ __device__ __forceinline__ const char* find_row(const GatherProblem& p, int t, i
       hi = mid;
   }
   const int a = __ldg(p.cu + lo), e = __ldg(p.cu + lo + 1);
-  if (a < 0 || a > t || e < a) {
+  if (a < 0 || e < a) {
     atomicCAS(&g_cache_status, kDevOk, kDevBadSeqlens);
     return nullptr;
   }
-  if (t >= e) return nullptr;  // behind the last sequence
+  if (t < a || t >= e) return nullptr;  // before the first sequence, behind the last
   const int pos = t - a, pg = pos >> p.cache.shift, off = pos & ((1 << p.cache.shift) - 1);
   if (pg >= p.width) {
     atomicCAS(&g_cache_status, kDevOk, kDevBadSeqlens);
