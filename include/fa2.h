@@ -472,7 +472,8 @@ int fa2_kv4_append(const void* k, const void* v, const long long* strides, void*
  * outside every sequence (before the first, behind the last) are not written,
  * nor are those past total; rows of a sequence that its table row has no room
  * for (status word 3) or whose page id is outside [0, num_pages) (status word
- * 5) neither.  One launch.
+ * 5) neither.  Offsets that begin below 0 or go down set the status word to 3;
+ * rows may then hold another sequence's.  One launch.
  */
 int fa2_kv4_gather(const void* cache, long long page_stride, const int* block_table, long long table_stride,
                    const int* cu_seqlens, void* k, void* v, int B, int H_kv, int total, int num_pages, int page_size,

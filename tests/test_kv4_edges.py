@@ -113,3 +113,21 @@ def test_gather_behind_a_gap(d, Hkv):
             want = np.full((max(total, int(cu[-1])), Hkv, d), 9.0)
             want[37:int(cu[-1])] = np.concatenate([x[i].transpose(1, 0, 2) for x in kv])
             assert np.array_equal(got.double().cpu().numpy(), want[:total])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("B", [4, 700])
+def test_gather_reports_offsets_out_of_order(B):
+    """Wherever they are: rows can fall to a sequence whose own offsets are right and whose table row has room for them."""
+    lens = [20] * B
+    cache = fa2.fa2_kv4_cache(2 * B, 1, 16, 16)
+    table = i32(np.arange(2 * B))[None].expand(B, -1).contiguous()
+    cu = np.r_[0, np.cumsum(lens)]
+    fa2.fa2_device_status(reset=True)
+    fa2.fa2_kv4_gather(cache, table, i32(cu), int(cu[-1]))
+    assert fa2.fa2_device_status(reset=True) == 0
+    for at, x in ((0, -1), (1, 45), (B // 2, 10 ** 9), (B - 1, -2 ** 31), (B, 0), (B, -1), (2, int(cu[1]) - 1)):
+        wrong = cu.copy()
+        wrong[at] = x
+        fa2.fa2_kv4_gather(cache, table, i32(wrong), int(cu[-1]))
+        assert fa2.fa2_device_status(reset=True) == 3, (at, x)

@@ -179,11 +179,7 @@ __device__ __forceinline__ const char* find_row(const GatherProblem& p, int t, i
       hi = mid;
   }
   const int a = __ldg(p.cu + lo), e = __ldg(p.cu + lo + 1);
-  if (a < 0 || e < a) {
-    atomicCAS(&g_cache_status, kDevOk, kDevBadSeqlens);
-    return nullptr;
-  }
-  if (t < a || t >= e) return nullptr;  // before the first sequence, behind the last
+  if (a < 0 || t < a || t >= e) return nullptr;  // (before the first sequence, behind the last)
   const int pos = t - a, pg = pos >> p.cache.shift, off = pos & ((1 << p.cache.shift) - 1);
   if (pg >= p.width) {
     atomicCAS(&g_cache_status, kDevOk, kDevBadSeqlens);
@@ -217,6 +213,13 @@ __global__ void __launch_bounds__(256) fa2_kv4_gather_kernel(const GatherProblem
     s_tile[threadIdx.x] = find_row(p, t0 + threadIdx.x, L::kTileBytes, key);
     s_key[threadIdx.x] = key;
   }
+  // Offsets out of order would give rows to the wrong sequences unnoticed: the
+  // last CTA, which has the fewest rows, looks at all of them.
+  if (blockIdx.x == gridDim.x - 1)
+    for (int b = threadIdx.x; b < p.B; b += 256) {
+      const int a = __ldg(p.cu + b);
+      if (a < 0 || __ldg(p.cu + b + 1) < a) atomicCAS(&g_cache_status, kDevOk, kDevBadSeqlens);
+    }
   __syncthreads();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int group = warp / p.head_warps;
