@@ -519,7 +519,8 @@ const char* fa2_status_string(int status);
  * 2 = shared memory base misaligned, 3 = invalid cu_seqlens or request
  * lengths (varlen and paged-cache calls), 5 = a page id, cache slot or
  * rotation position out of range (paged-cache calls, fa2_qk_norm_rope).
- * Synchronous with respect to the device. Returns an fa2_status. */
+ * Synchronous with respect to the device (about 10 us for each source of
+ * kernels that the process has called). Returns an fa2_status. */
 int fa2_device_status(int* value, int reset);
 
 /* Text describing the last CUDA failure (FA2_ERR_CUDA / FA2_ERR_ALLOC) an

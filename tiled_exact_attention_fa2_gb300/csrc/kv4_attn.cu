@@ -57,6 +57,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <climits>
 #include <cmath>
 
@@ -69,6 +70,7 @@ namespace fa2 {
 namespace {
 
 __device__ int g_attn4_status;
+std::atomic<bool> g_launched{false};  // some call of this process has: the word may be set
 
 // Warps of a CTA (one CTA per SM): as many as the registers of 8 and of 16
 // rows allow.
@@ -1294,6 +1296,10 @@ int check_attn_sizes(int B, int H, int H_kv, int total_q, int max_q, int d) {
 }  // namespace
 
 int read_attn4_status(int* value, bool reset) {
+  if (!g_launched.load()) {
+    *value = 0;
+    return 0;
+  }
   if (cudaError_t e = cudaMemcpyFromSymbol(value, g_attn4_status, sizeof(int))) return static_cast<int>(e);
   if (reset) {
     const int zero = 0;
@@ -1380,6 +1386,7 @@ int fa2_kv4_attn(const void* q, const void* cache, long long page_stride, const 
   p.v_scale = v_scale;
   p.causal = causal != 0;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  g_launched = true;
   const int e = d == 16    ? launch_attn<16>(p, max_rows, st)
                 : d == 32  ? launch_attn<32>(p, max_rows, st)
                 : d == 64  ? launch_attn<64>(p, max_rows, st)

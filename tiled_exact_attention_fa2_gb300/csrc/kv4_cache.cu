@@ -10,6 +10,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cmath>
 
 #include "args.h"
@@ -21,6 +22,7 @@ namespace fa2 {
 namespace {
 
 __device__ int g_cache_status;
+std::atomic<bool> g_launched{false};  // some call of this process has: the word may be set
 
 struct AppendProblem {
   const __nv_bfloat16 *k, *v;  // [T, H_kv, d]
@@ -320,6 +322,10 @@ size_t cache_span(long long page_stride, int num_pages, int page_size, int H_kv,
 }
 
 int read_cache_status(int* value, bool reset) {
+  if (!g_launched.load()) {
+    *value = 0;
+    return 0;
+  }
   if (cudaError_t e = cudaMemcpyFromSymbol(value, g_cache_status, sizeof(int))) return static_cast<int>(e);
   if (reset) {
     const int zero = 0;
@@ -380,6 +386,7 @@ int fa2_kv4_append(const void* k, const void* v, const long long* strides, void*
   p.slots = slots;
   p.cache = paged_cache(cache, page_stride, num_pages, page_size, H_kv);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  g_launched = true;
   const int e = d == 16    ? launch_append_d<16>(p, st)
                 : d == 32  ? launch_append_d<32>(p, st)
                 : d == 64  ? launch_append_d<64>(p, st)
@@ -409,6 +416,7 @@ int fa2_kv4_gather(const void* cache, long long page_stride, const int* block_ta
   const GatherProblem p{paged_cache(cache, page_stride, num_pages, page_size, H_kv), block_table, table_stride, table_width,
                         cu_seqlens, B, total, static_cast<__nv_bfloat16*>(k), static_cast<__nv_bfloat16*>(v), k_scale, v_scale, 0};
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  g_launched = true;
   const int e = d == 16    ? launch_gather_d<16>(p, st)
                 : d == 32  ? launch_gather_d<32>(p, st)
                 : d == 64  ? launch_gather_d<64>(p, st)

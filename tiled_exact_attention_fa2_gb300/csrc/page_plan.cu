@@ -19,6 +19,7 @@
 // us, 333 requests with 132 thousand new tokens 4.9 us.
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <climits>
 
 #include "args.h"
@@ -30,6 +31,7 @@ namespace fa2 {
 namespace {
 
 __device__ int g_plan_status;
+std::atomic<bool> g_launched{false};  // some call of this process has: the word may be set
 
 constexpr int kThreads = 512;
 // From here on a thread's lengths no longer stay in L1 between its reads: 4000
@@ -218,6 +220,10 @@ __global__ void __launch_bounds__(kThreads) fa2_page_plan_kernel(const PlanProbl
 }  // namespace
 
 int read_plan_status(int* value, bool reset) {
+  if (!g_launched.load()) {
+    *value = 0;
+    return 0;
+  }
   if (cudaError_t e = cudaMemcpyFromSymbol(value, g_plan_status, sizeof(int))) return static_cast<int>(e);
   if (reset) {
     const int zero = 0;
@@ -268,6 +274,7 @@ extern "C" int fa2_page_plan(const int* cached_lens, const int* new_lens, const 
   // 113 with 8439 5.9 / 4.8 / 3.9; with two CTAs per SM 5.2 / 3.9).
   long long grid = (static_cast<long long>(max_tokens) + kThreads - 1) / kThreads;
   grid = grid < 1 ? 1 : (grid > 152 ? 152 : grid);
+  g_launched = true;
   if (int e = launch_pdl(kernel, dim3(static_cast<unsigned>(grid)), dim3(kThreads), smem,
                          static_cast<cudaStream_t>(stream), p))
     return record_cuda_failure(e, "page plan launch");

@@ -37,6 +37,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cmath>
 #include <utility>
 
@@ -49,6 +50,7 @@ namespace fa2 {
 namespace {
 
 __device__ int g_norm_status;
+std::atomic<bool> g_launched{false};  // some call of this process has: the word may be set
 
 struct View {  // [B, heads, N, d] with the last dimension contiguous; strides in elements
   char* p;
@@ -623,6 +625,10 @@ NormProblem problem_of(const NormArgs& a) {
 }  // namespace
 
 int read_norm_status(int* value, bool reset) {
+  if (!g_launched.load()) {
+    *value = 0;
+    return 0;
+  }
   if (cudaError_t e = cudaMemcpyFromSymbol(value, g_norm_status, sizeof(int))) return static_cast<int>(e);
   if (reset) {
     const int zero = 0;
@@ -655,6 +661,7 @@ int fa2_qk_norm_rope(const void* q, const void* k, const void* q_weight, const v
   if (int rc = validate_norm(a, t, 4, 2, strides)) return rc;
   if (N == 0) return FA2_OK;
   NormProblem p = problem_of(a);
+  g_launched = true;
   for (int i = 0; i < 2; ++i) {
     p.x[i] = view_of(t[i]);
     p.y[i] = view_of(t[2 + i]);
@@ -712,6 +719,7 @@ int fa2_qk_norm_rope_bwd(const void* dq_out, const void* dk_out, const void* q, 
     }
   }
   NormProblem p = problem_of(a);
+  g_launched = true;
   for (int i = 0; i < 2; ++i) {
     p.g[i] = view_of(t[i]);
     p.x[i] = view_of(t[2 + i]);
