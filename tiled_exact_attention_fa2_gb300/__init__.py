@@ -11,6 +11,8 @@ Build the library with ``python -c "import __graft_entry__ as g; g.build()"``
 from __future__ import annotations
 
 import ctypes
+import functools
+import inspect
 import math
 import os
 import struct
@@ -156,14 +158,56 @@ def _stream(stream, device) -> int:
     if stream is None:
         return torch.cuda.current_stream(device).cuda_stream
     if isinstance(stream, torch.cuda.Stream):
+        if device.index is not None and stream.device_index != device.index:
+            raise ValueError(f"the stream belongs to cuda:{stream.device_index}, the tensors to {device}")
         return stream.cuda_stream
     return int(stream)
+
+
+class _on:
+    """`device` current, and the given stream torch's current one, so that what a call allocates belongs to the stream
+    that uses it."""
+
+    def __init__(self, device, stream):
+        if isinstance(stream, torch.cuda.Stream) and stream.device_index != device:
+            raise ValueError(f"the stream belongs to cuda:{stream.device_index}, the tensors to cuda:{device}")
+        self.guards = [torch.cuda.device(device)]
+        if stream is not None:
+            if not isinstance(stream, torch.cuda.Stream):
+                stream = torch.cuda.ExternalStream(int(stream), device=device)
+            self.guards.append(torch.cuda.stream(stream))
+
+    def __enter__(self):
+        for g in self.guards:
+            g.__enter__()
+
+    def __exit__(self, *exc):
+        for g in reversed(self.guards):
+            g.__exit__(*exc)
+
+
+def _made_on_stream(fn):
+    """The call made on the `stream` that it is given: what it allocates (outputs, scratch that is freed when it returns)
+    belongs to that stream, so no other stream's work is given the memory while this call's is under way."""
+    at = list(inspect.signature(fn).parameters).index("stream")
+
+    @functools.wraps(fn)
+    def call(*args, **kwargs):
+        stream = args[at] if len(args) > at else kwargs.get("stream")
+        q = args[0] if args else kwargs.get("q")
+        if stream is None or not q.is_cuda:
+            return fn(*args, **kwargs)
+        with _on(q.get_device(), stream):
+            return fn(*args, **kwargs)
+
+    return call
 
 
 def _scale(scale, d):
     return 1.0 / math.sqrt(d) if scale is None else float(scale)
 
 
+@_made_on_stream
 def fa2_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: Optional[torch.Tensor] = None,
             lse: Optional[torch.Tensor] = None, scale: Optional[float] = None, causal: bool = True,
             stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
@@ -190,6 +234,7 @@ def fa2_fwd_workspace_bytes(B: int, H_kv: int, N: int, d: int) -> int:
     return load_library().fa2_fwd_workspace_bytes(B, H_kv, N, d)
 
 
+@_made_on_stream
 def fa2_fwd_ws(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, workspace: torch.Tensor,
                o: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None, scale: Optional[float] = None,
                causal: bool = True, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
@@ -226,6 +271,7 @@ def _bwd_common(q, k, v, o, dO, lse, dq, dk, dv):
     return (B, H, N, d), dq, dk, dv
 
 
+@_made_on_stream
 def fa2_bwd(q, k, v, o, dO, lse, dq=None, dk=None, dv=None, scale: Optional[float] = None,
             causal: bool = True, stream=None):
     """dQ, dK, dV (bf16) of L with dL/dO = dO; scratch is allocated stream-ordered inside the library."""
@@ -239,6 +285,7 @@ def fa2_bwd(q, k, v, o, dO, lse, dq=None, dk=None, dv=None, scale: Optional[floa
     return dq, dk, dv
 
 
+@_made_on_stream
 def fa2_bwd_ws(q, k, v, o, dO, lse, workspace: torch.Tensor, dq=None, dk=None, dv=None,
                scale: Optional[float] = None, causal: bool = True, stream=None):
     """fa2_bwd with caller-owned scratch (a CUDA byte tensor of fa2_bwd_workspace_bytes bytes)."""
@@ -299,6 +346,7 @@ def _gqa_shapes(q, k, v):
     return B, H, Hkv, N, d
 
 
+@_made_on_stream
 def fa2_fwd_gqa(q, k, v, o=None, lse=None, scale: Optional[float] = None, causal: bool = True, stream=None):
     """Grouped-query forward: q [B,H,N,d], k/v [B,H_kv,N,d]; query head h reads K/V head h // (H // H_kv)."""
     lib = load_library()
@@ -315,6 +363,7 @@ def fa2_fwd_gqa(q, k, v, o=None, lse=None, scale: Optional[float] = None, causal
     return o, lse
 
 
+@_made_on_stream
 def fa2_bwd_gqa(q, k, v, o, dO, lse, dq=None, dk=None, dv=None, scale: Optional[float] = None,
                 causal: bool = True, stream=None):
     """Grouped-query backward: dk/dv [B,H_kv,N,d] are sums over each group of query heads."""
@@ -336,6 +385,7 @@ def fa2_bwd_gqa(q, k, v, o, dO, lse, dq=None, dk=None, dv=None, scale: Optional[
     return dq, dk, dv
 
 
+@_made_on_stream
 def fa2_fwd_splitkv(q, k, v, num_splits: Optional[int] = None, o=None, lse=None, workspace=None,
                     scale: Optional[float] = None, causal: bool = True, stream=None):
     """Split-KV forward for Nq <= Nk (decoding): q [B,H,Nq,d], k/v [B,H_kv,Nk,d].
@@ -401,6 +451,7 @@ def _max_len(cu, given):
     return int((cu[1:] - cu[:-1]).max().item()) if cu.numel() > 1 else 0
 
 
+@_made_on_stream
 def fa2_fwd_varlen(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q: Optional[int] = None,
                    max_seqlen_k: Optional[int] = None, o=None, lse=None, scale: Optional[float] = None,
                    causal: bool = True, stream=None):
@@ -424,6 +475,7 @@ def fa2_fwd_varlen(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q: Optional[i
     return o, lse
 
 
+@_made_on_stream
 def fa2_bwd_varlen(q, k, v, o, dO, lse, cu_seqlens_q, cu_seqlens_k, max_seqlen_q: Optional[int] = None,
                    max_seqlen_k: Optional[int] = None, dq=None, dk=None, dv=None, workspace=None,
                    scale: Optional[float] = None, causal: bool = True, stream=None):
@@ -452,6 +504,7 @@ def fa2_bwd_varlen(q, k, v, o, dO, lse, cu_seqlens_q, cu_seqlens_k, max_seqlen_q
     return dq, dk, dv
 
 
+@_made_on_stream
 def fa2_bwd_noalloc(q, k, v, o, dO, lse, dq=None, dk=None, dv=None, scale: Optional[float] = None,
                     causal: bool = True, stream=None):
     """fa2_bwd for callers that cannot allocate device memory: the library's
@@ -470,6 +523,7 @@ def fa2_bwd_noalloc(q, k, v, o, dO, lse, dq=None, dk=None, dv=None, scale: Optio
 FA2_DQ_REDUCE, FA2_DQ_ATOMIC, FA2_DQ_SPLIT = 0, 1, 2
 
 
+@_made_on_stream
 def fa2_bwd_deterministic(q, k, v, o, dO, lse, dq=None, dk=None, dv=None, workspace=None,
                           scale: Optional[float] = None, causal: bool = True, stream=None):
     """Bitwise-reproducible backward (d = 128): dQ summed over key tiles in a
@@ -577,7 +631,9 @@ def fa2_step_from_host(host: dict, causal: bool = True, scale: Optional[float] =
     if need == 0:
         raise FA2Error("fa2_step_from_host_workspace_bytes", 2)
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=torch.cuda.current_device())
+        dev = stream.device_index if isinstance(stream, torch.cuda.Stream) else torch.cuda.current_device()
+        with _on(dev, stream):
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
     st = _stream(stream, workspace.device)
     rc = lib.fa2_step_from_host(q.data_ptr(), host["k"].data_ptr(), host["v"].data_ptr(), host["dO"].data_ptr(),
                                 host["o"].data_ptr(), lse.data_ptr(), host["dq"].data_ptr(), host["dk"].data_ptr(),
@@ -596,28 +652,6 @@ _raw_stream = torch._C._cuda_getCurrentRawStream
 _current_device = torch._C._cuda_getDevice
 # A host array of strides, as the bytes of C's long longs (made in a third of the time of a ctypes array).
 _pack4, _pack12, _pack18 = (struct.Struct(f"{n}q").pack for n in (4, 12, 18))
-
-
-class _on:
-    """`device` current, and the given stream torch's current one, so that what a call allocates belongs to the stream
-    that uses it."""
-
-    def __init__(self, device, stream):
-        if isinstance(stream, torch.cuda.Stream) and stream.device_index != device:
-            raise ValueError(f"the stream belongs to cuda:{stream.device_index}, the tensors to cuda:{device}")
-        self.guards = [torch.cuda.device(device)]
-        if stream is not None:
-            if not isinstance(stream, torch.cuda.Stream):
-                stream = torch.cuda.ExternalStream(int(stream), device=device)
-            self.guards.append(torch.cuda.stream(stream))
-
-    def __enter__(self):
-        for g in self.guards:
-            g.__enter__()
-
-    def __exit__(self, *exc):
-        for g in reversed(self.guards):
-            g.__exit__(*exc)
 
 
 # (devices are compared by index: -1 is the CPU)
