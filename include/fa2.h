@@ -500,9 +500,14 @@ int fa2_kv4_gather(const void* cache, long long page_stride, const int* block_ta
  * outside [0, num_pages) leaves its keys out and sets 5.
  * workspace: 256-byte aligned, fa2_kv4_attn_workspace_bytes(...) bytes for the
  * same sizes (max_seqlen_k not above the table's room), whatever it holds; NULL
- * where that is 0: calls of short requests (max_seqlen_k up to 1024 or 2048,
- * for many rows or few) need none and take one launch, others two.  (It is 0 for invalid
- * sizes as well.)  Results do not vary from run to run.  total_q = 0 is
+ * where that is 0.  It is 0, and the call one launch, for short requests: with U
+ * = B * H_kv * ceil(rows / 8) units (16 in place of 8 above 8 rows; rows =
+ * max_seqlen_q * H / H_kv), up to 152 of them and max_seqlen_k at most 2048 or
+ * 54 U, whichever is more; or more of them and max_seqlen_k at most 2048 (1024
+ * above 8 rows), but at least 128 where U is above 1216.  So a shorter bound can
+ * need a workspace where a longer one needs none: ask for each call's sizes, or
+ * with max_seqlen_k = 2^30 for what is enough under any bound.  (It is 0 for
+ * invalid sizes as well.)  Results do not vary from run to run.  total_q = 0 is
  * allowed, with any max_seqlen_q >= 0, and does nothing.
  */
 size_t fa2_kv4_attn_workspace_bytes(int B, int H, int H_kv, int max_seqlen_q, int max_seqlen_k, int d);

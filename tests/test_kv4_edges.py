@@ -24,6 +24,27 @@ def test_no_queries_under_any_bound(lib):
     assert attn(lib, tq=0, mq=-1) == 2 and attn(lib, tq=0, mq=1, B=0) == 2 and attn(lib, tq=0, mq=1, cache=None) == 1
 
 
+def test_workspace_rule_as_documented(lib):
+    """Which bounds need a workspace, which is not monotone in the bound, and one that is enough for all of them."""
+    ws = lib.fa2_kv4_attn_workspace_bytes
+    rng = np.random.default_rng(6)
+    for _ in range(2000):
+        B, Hkv, G, nq = (int(x) for x in np.exp(rng.uniform(0, np.log([400, 16, 16, 20]))))
+        rows = G * nq
+        units = B * Hkv * -(-rows // (16 if rows > 8 else 8))
+        bound = int(np.exp(rng.uniform(0, np.log(20000))))
+        if units <= 152:
+            none = bound <= max(2048, 54 * units)
+        else:
+            none = bound <= (1024 if rows > 8 else 2048) and (units <= 1216 or bound >= 128)
+        most = ws(B, G * Hkv, Hkv, nq, 1 << 30, 64)
+        assert most > 0 and ws(B, G * Hkv, Hkv, nq, bound, 64) == (0 if none else most)
+    # 2048 units: none needed under a bound of 2048 keys, but under one of 100
+    long, short = dict(B=256, H=32, Hkv=8, tq=256, mq=1, W=128, mk=2048), dict(B=256, H=32, Hkv=8, tq=256, mq=1, W=128, mk=100)
+    assert attn(lib, ws=None, o=A, **long) == 9 and attn(lib, ws=None, o=A, **short) == 8
+    assert attn(lib, o=A, wsb=ws(256, 32, 8, 1, 1 << 30, 64), **short) == 9
+
+
 # ---------------------------------------------------------------- GPU
 @pytest.mark.gpu
 def test_query_bounds_above_the_rows_there_are():

@@ -922,7 +922,11 @@ def fa2_kv4_gather(cache, block_table, cu_seqlens, total: int, k_scale: float = 
 
 
 def fa2_kv4_attn_workspace_bytes(B: int, H: int, H_kv: int, max_seqlen_q: int, max_seqlen_k: int, d: int) -> int:
-    """Scratch of fa2_kv4_attn (0: none); max_seqlen_k at most width * page_size of the block table."""
+    """Scratch of fa2_kv4_attn for these sizes (0: none); max_seqlen_k at most width * page_size of the block table.
+
+    A call with a shorter bound can need more (include/fa2.h has the rule); with
+    max_seqlen_k = 2**30 it is what is enough under any bound.
+    """
     return load_library().fa2_kv4_attn_workspace_bytes(B, H, H_kv, max_seqlen_q, max_seqlen_k, d)
 
 
