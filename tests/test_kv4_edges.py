@@ -152,3 +152,18 @@ def test_gather_reports_offsets_out_of_order(B):
         wrong[at] = x
         fa2.fa2_kv4_gather(cache, table, i32(wrong), int(cu[-1]))
         assert fa2.fa2_device_status(reset=True) == 3, (at, x)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("P", [16, 64])
+def test_gather_stops_at_the_table_rows_end(P):
+    """A sequence of one token more than its row's only (valid) page holds: its last row is left out, with status 3."""
+    rng = np.random.default_rng(P)
+    cache, table, kv = filled(rng, [P, P], 2, P, 32, spare=0)
+    beyond = torch.cat([i32(table[:1]), i32(table[1:])], 1)  # (what lies behind the row is a valid page as well)
+    fa2.fa2_device_status(reset=True)
+    k, v = (torch.full((P + 1, 2, 32), 9.0, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    fa2.fa2_kv4_gather(cache, beyond[:, :1], i32([0, P + 1]), P + 1, k=k, v=v)
+    assert fa2.fa2_device_status(reset=True) == 3
+    for got, i in ((k, 0), (v, 1)):
+        assert np.array_equal(got[:P].double().cpu().numpy(), kv[0][i].transpose(1, 0, 2)) and torch.all(got[P] == 9)
