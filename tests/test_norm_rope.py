@@ -106,6 +106,26 @@ def bwd(lib, p=None, B=2, H=4, Hkv=2, N=16, d=64, ws=20 * A, wsb=1 << 24, eps=1e
                                     ws, wsb, None)
 
 
+def test_overlap_check_accepts_views_that_are_apart(lib):
+    """dq and dk as heads of one token-major buffer, reached through the refusal that follows the overlap check (8: no
+    workspace): apart only where dk's heads begin behind dq's and end with the token's row."""
+    B, H, Hkv, N, d = 2, 4, 2, 16, 64
+    row = (H + Hkv) * d
+    own = [[h * N * d, N * d, d] for h in (H, Hkv)]
+    view = [N * row, d, row]
+    for first, want in ((H * d, 8), ((H - 1) * d, 9), (H * d + 8, 9), (H * d - 8, 9), (0, 9), (row + H * d, 8)):
+        s = (ctypes.c_longlong * 18)(*(own[0] + own[1] + own[0] + own[1] + view + view))
+        p = [A * (i + 1) for i in range(12)]
+        gq, gk, q, k, wq, wk, rope, pos, dq, dk, dwq, dwk = p
+        assert lib.fa2_qk_norm_rope_bwd(gq, gk, q, k, wq, wk, 0, rope, pos, dq, dq + 2 * first, dwq, dwk, B, H, Hkv, N, d, 64, 0, 64,
+                                        1e-6, s, None, 0, None) == want, first
+    # the token's row of a padded buffer, [heads of q, 64 columns unused, heads of k]
+    wide = [N * (row + 64), d, row + 64]
+    s = (ctypes.c_longlong * 18)(*(own[0] + own[1] + own[0] + own[1] + wide + wide))
+    assert lib.fa2_qk_norm_rope_bwd(gq, gk, q, k, wq, wk, 0, rope, pos, dq, dq + 2 * (H * d + 64), dwq, dwk, B, H, Hkv, N, d, 64, 0, 64,
+                                    1e-6, s, None, 0, None) == 8
+
+
 def test_backward_refusals(lib):
     p = [A * (i + 1) for i in range(12)]
     for i in (0, 1, 2, 3, 6, 8, 9):
