@@ -6,9 +6,12 @@
 // and K/V head against 4 d flops for each query head of its group, far below
 // the balance of even the warp-level matrix instructions (1024 fp16
 // multiply-adds a clock and SM, measured), so the products are
-// mma.sync.m16n8k16 on operands decoded in registers: a tcgen05 operand would
-// have to be written to shared memory in 16 bits first, 3.6 times the bytes
-// that come in, for 128-row tiles of which a decoding step fills 1 to 16.
+// mma.sync.m16n8k16 on operands decoded in registers.  A tcgen05 operand in
+// shared memory would have to be written there in 16 bits first, 3.6 times the
+// bytes that come in; keys decoded into TMEM (as the A operand, 128 of them)
+// would not, but pay only where a K/V head has more rows than the 8 or 16 of a
+// unit here: a unit reads and decodes its keys for itself, so the time grows
+// with every 16 rows.
 //
 // Work.  A unit is (request, K/V head, 8 NT query rows), its keys pairs of
 // 16-key tiles; row r of a unit is query r / G, head r % G of the group.  All
@@ -34,15 +37,19 @@
 // registers by two 8x8 transposes (movmatrix).
 //
 // Measured on a GB300 (device time, 8 and 4 K/V heads of 128 columns): 48
-// requests of up to 8191 keys, one query and 4 heads a group, 55.5 us (5.15
+// requests of up to 8191 keys, one query and 4 heads a group, 55.6 us (5.14
 // TB/s of cache; between two lengths the marginal rate is 6.9 TB/s, a copy's:
 // the rest is 6 us until the first tiles arrive, about 4 us for the combine
 // kernel and as much between the first and the last warp's end); two requests
-// of 131072 keys, four queries and 4 heads a group (16 rows), 45.4 us, bound
-// by instruction issue: an mma.m16n8k16 takes about 8 issue slots of its
-// scheduler, and 32 of them with the 64 decodes and 64 scalings of a tile at
-// least 107 cycles of an SM against 98 for the tile's bytes; one request of
-// 1000 keys 7.7 us, bound by latency.
+// of 131072 keys, four queries and 4 heads a group (16 rows), 45.7 us, of which
+// about 14 do not depend on the length (262144 and 524288 keys: 79 and 142 us)
+// and the others are 72.5 ns, about 145 cycles, an SM and tile.  Of these its
+// bytes would take 100 cycles and its 32 matrix instructions, 64 decodes and 64
+// scalings 107 if nothing waited; with 12 warps an SM (168 registers) the
+// schedulers issue in half of the cycles, and their three warps wait most for
+// fixed latencies (1.8 of the 6 cycles between two instructions of a warp) and
+// for the matrix and ALU pipes (0.9): as much latency as issue.  One request of
+// 1000 keys 8.0 us, bound by latency.
 //
 // Precision.  Cache values are exact in fp16 (6 significant bits), Q (8 bits)
 // is divided by a power of two per row so that its largest value is in
@@ -1208,7 +1215,18 @@ inline long long max_units(int B, int H_kv, long long max_rows) {
 // (the line spreads the bytes over all SMs but has its layout, its partial
 // results and a second launch to pay for: the few units' bound is set where
 // that launch's host time is still saved.  Very many units of a few keys leave
-// most of a CTA's warps without any.)
+// most of a CTA's warps without any.  Up to 64 units of more than 1024 keys no
+// longer take one CTA each, as in the first two lines, but a cluster: below.)
+// The rule goes by the bound on the lengths, so one long request among short
+// ones keeps it to few SMs where the line would spread it.  8 rows a unit, 8
+// K/V heads, one request of the longest length and the others of 100 keys, this
+// rule's form / the line in us (even lengths in brackets):
+//   24 units    1024 keys   8.2 / 11.0 (8.2 / 10.3)     2048   8.5 / 10.9 (8.6 / 10.5)
+//   152 units   1024 keys   8.1 / 12.3 (8.7 / 15.6)     2048  11.5 / 12.3 (11.8 / 18.6)   8192  30.1 / 13.5 (32.6 / 32.4)
+//   304 units   1024 keys  10.5 / 10.3 (11.8 / 16.1)    2048  16.6 / 11.5 (19.9 / 20.8)
+//   760 units   1024 keys  11.7 / 13.5 (24.8 / 26.4)    2048  17.6 / 13.8 (37.4 / 37.3)
+// (a caller who knows of such a mix can give a longer bound, up to the table's
+// room, which takes the line.)
 inline int unit_warps(int B, int H_kv, long long max_rows, long long max_keys) {
   const long long units = max_units(B, H_kv, max_rows);
   const bool wide = wide_rows(max_rows);
