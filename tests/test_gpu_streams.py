@@ -68,3 +68,21 @@ def test_what_a_call_allocates_belongs_to_its_stream(monkeypatch):
 def test_a_stream_of_another_device_is_refused():
     with pytest.raises(ValueError):
         fa2._stream(torch.cuda.Stream(), torch.device("cuda", torch.cuda.current_device() + 1))
+
+
+def test_default_stream_by_its_handles():
+    """0 and cudaStreamLegacy (1) are torch's default stream; neither is one of torch's own numbers."""
+    dev, default = torch.cuda.current_device(), torch.cuda.default_stream()
+    q = torch.randn(1, 2, 64, 64, device="cuda").to(torch.bfloat16)
+    want = fa2.fa2_qk_norm_rope(q, q.clone())
+    with torch.cuda.stream(torch.cuda.Stream()):
+        for handle in (0, 1, default):
+            with fa2._on(dev, handle):
+                assert torch.cuda.current_stream() == default
+            torch.cuda.synchronize()
+            got = fa2.fa2_qk_norm_rope(q, q.clone(), stream=handle)
+            torch.cuda.synchronize()
+            assert torch.equal(got[0], want[0])
+    per_thread = fa2._on(dev, 2)
+    with per_thread:
+        assert torch.cuda.current_stream().cuda_stream == 2

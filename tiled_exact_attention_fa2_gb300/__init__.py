@@ -174,7 +174,9 @@ class _on:
         self.guards = [torch.cuda.device(device)]
         if stream is not None:
             if not isinstance(stream, torch.cuda.Stream):
-                stream = torch.cuda.ExternalStream(int(stream), device=device)
+                # (1 is cudaStreamLegacy, which torch would take for a number of its own)
+                handle = int(stream)
+                stream = torch.cuda.default_stream(device) if handle in (0, 1) else torch.cuda.ExternalStream(handle, device=device)
             self.guards.append(torch.cuda.stream(stream))
 
     def __enter__(self):
