@@ -98,6 +98,46 @@ def test_a_wrong_query_offset_costs_only_its_own_requests(B, most, H, Hkv, d):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("Hkv", [1, 4])
+def test_a_wrong_query_offset_among_few_requests(Hkv):
+    """The same where a unit has a full CTA, a cluster of them, or spans of the line that several warps join."""
+    rng = np.random.default_rng(Hkv)
+    B, H, d, most = 6, 2 * Hkv, 64, 40
+    nqs, lens = [1, 1, most, 1, 1, 5], [33, 250, 290, 1, 70, 17]
+    cache, table, kv = filled(rng, lens, Hkv, 16, d, width=8192 // 16)
+    cu = np.r_[0, np.cumsum(nqs)]
+    total = int(cu[-1])
+    q = torch.from_numpy(rng.standard_normal((total, H, d))).to(torch.bfloat16).cuda()
+    q64 = q.double().cpu().numpy()
+    fa2.fa2_device_status(reset=True)
+    for bound in (300, 900, 8192):
+        assert (fa2.fa2_kv4_attn_workspace_bytes(B, H, Hkv, most, bound, d) > 0) == (bound == 8192)
+        want = fa2.fa2_kv4_attn(q, cache, i32(table), i32(lens), i32(cu), most, max_seqlen_k=bound)
+        assert fa2.fa2_device_status() == 0
+        check_attention(*want, [(int(cu[b]), int(cu[b + 1])) for b in range(B)], q64, kv, 1 / math.sqrt(d), True, H)
+        for at in range(B + 1):
+            for x in (-7, total + 1000):
+                wrong = cu.copy()
+                wrong[at] = x
+                o, lse = torch.full_like(q, 9.0), torch.full((H, total), 9.0, device="cuda")
+                fa2.fa2_kv4_attn(q, cache, i32(table), i32(lens), i32(wrong), most, max_seqlen_k=bound, o=o, lse=lse)
+                assert fa2.fa2_device_status(reset=True) == 3
+                gone = slice(int(cu[max(at - 1, 0)]), int(cu[min(at + 1, B)]))
+                assert torch.all(o[gone] == 9) and torch.all(lse[:, gone] == 9)
+                rows = [(int(cu[b]), int(cu[b + 1])) if b not in (at - 1, at) else (0, 0) for b in range(B)]
+                check_attention(o, lse, rows, q64, kv, 1 / math.sqrt(d), True, H)
+        # requests 2 and 4 on the same rows (their keys differ: the rows hold the one's or the other's), 3 backwards
+        twice = np.r_[cu[:4], cu[2], cu[3], total]
+        o, lse = torch.full_like(q, 9.0), torch.full((H, total), 9.0, device="cuda")
+        fa2.fa2_kv4_attn(q, cache, i32(table), i32(lens), i32(twice), most, max_seqlen_k=bound, o=o, lse=lse)
+        assert fa2.fa2_device_status(reset=True) == 3
+        check_attention(o, lse, [(0, 1), (1, 2)], q64, kv[:2], 1 / math.sqrt(d), True, H)
+        check_attention(o, lse, [(int(cu[3]), total)], q64, kv[5:], 1 / math.sqrt(d), True, H)
+        both = lse[:, 2:int(cu[3])]
+        assert torch.all(torch.isfinite(both) & (both != 9))
+
+
+@pytest.mark.gpu
 def test_query_offsets_that_overlap():
     """Offsets that go up and down give the same rows to several requests, and a tile's number to several tiles: every
     request whose own offsets are in range is computed (here they all have the same keys, so it does not show which
