@@ -331,7 +331,7 @@ __device__ __forceinline__ void join_unit(Rows<D, NT>& s, Fixed<D, E, NT>& sm, c
             row[(16 * t + 8 + g) ^ turn] = b;
           }
         }
-        if (round == 0 && g == 0) sm.ml[warp][2 * c + u] = make_float2(kLift<E> - s.off[j][u], s.l[j][u]);
+        if (round == 0 && g == 0) sm.ml[warp][2 * c + u] = make_float2(-s.off[j][u], s.l[j][u]);
       }
       sync_warps();
       if (round == 0) {
@@ -391,7 +391,7 @@ __device__ __forceinline__ void join_unit(Rows<D, NT>& s, Fixed<D, E, NT>& sm, c
           if (part)
             ml[local] = make_float2(top, l);
           else
-            p.lse[static_cast<long long>(head) * p.total_q + tok] = l == 0.f ? -INFINITY : row_lse(top, l, kLift<E>);
+            p.lse[static_cast<long long>(head) * p.total_q + tok] = l == 0.f ? -INFINITY : row_lse(top, l);
         }
       }
     }
@@ -461,7 +461,7 @@ __device__ __forceinline__ void join_parts(const AttnProblem& p, const Unit& it,
       const int r = it.row0 + local, i = query_of(p, r), head = it.h * p.G + (r - i * p.G);
       const long long tok = it.q0 + i;
       if (active) write_columns<kCols>(p.o + (tok * p.H + head) * D + lane * kCols, o, l == 0.f ? 0.f : p.v_scale / l);
-      if (lane == 0) p.lse[static_cast<long long>(head) * p.total_q + tok] = l == 0.f ? -INFINITY : row_lse(top, l, kLift<E>);
+      if (lane == 0) p.lse[static_cast<long long>(head) * p.total_q + tok] = l == 0.f ? -INFINITY : row_lse(top, l);
     }
   }
 }
@@ -693,7 +693,7 @@ __device__ __forceinline__ void join_cluster(const AttnProblem& p, const Unit& i
     const int r = it.row0 + local, i0 = query_of(p, r), head = it.h * p.G + (r - i0 * p.G);
     const long long tok = it.q0 + i0;
     if (col < D) write_columns<kLane>(p.o + (tok * p.H + head) * D + col, o, l == 0.f ? 0.f : p.v_scale / l);
-    if (lane == 0) p.lse[static_cast<long long>(head) * p.total_q + tok] = l == 0.f ? -INFINITY : row_lse(top, l, kLift<E>);
+    if (lane == 0) p.lse[static_cast<long long>(head) * p.total_q + tok] = l == 0.f ? -INFINITY : row_lse(top, l);
   }
 }
 
@@ -844,7 +844,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool known = false;  // the next is described
     if (it.len > 0 || it.live) {
       const int first = it.first, len = it.len, Lk = it.Lk;
-      put_queries<D, E>(sm.f.q, sm.f.factor, queries, p.scale_log2, threadIdx.x);
+      put_queries<D, E>(sm.f.q, sm.f.factor, queries, p.scale_log2, Lk, threadIdx.x);
       start_rows<D, E, NT>(s, p, it.unit.Lq, Lk, it.unit.row0, lane);
       known = !it.end && __all_sync(0xffffffffu, mbar_test_wait(&sm.f.desc_full[(k + 1) % kDescs], ((k + 1) / kDescs) & 1));
       if (known) ask(next);

@@ -19,7 +19,7 @@
 // the largest keep all 11.  The running maximum is raised only when a score
 // passes it by kLag, which saves the tile's maximum and the rescaling of O for
 // nearly every tile.  Maximum, sum and O are fp32; the quotient removes the
-// common factor exactly.
+// common factor exactly.  Any finite V gives a finite O: see lift().
 #pragma once
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -51,7 +51,7 @@ struct AttnProblem {
   const int* cu_q;    // or NULL: every request has max_q queries
   size_t table_bytes, q_bytes;
   float* part;        // [kPlaces][rows][d] unnormalised O
-  float2* part_ml;    // [kPlaces][rows] maximum (log2), sum
+  float2* part_ml;    // [kPlaces][rows] maximum - lift (log2), sum
   unsigned long long* arrived;  // [2][kPlaces]: this call's number in the upper 48 bits, parts that are there in the lower
   unsigned long long* queue;    // its upper 32 bits, and items that have been taken
   unsigned long long call;      // that number, in the upper 48 bits
@@ -241,17 +241,20 @@ __device__ __forceinline__ void load_v(uint32_t (*a)[4], uint32_t half, int tile
 template <int D, int NT>
 struct Rows {
   float o[NT][D / 16][4];
-  float off[NT][2], l[NT][2];  // kLift - maximum, sum, of query rows 2c, 2c + 1
+  float off[NT][2], l[NT][2];  // lift - maximum, sum, of query rows 2c, 2c + 1: a weight is 2^(score + off)
   int vis[NT][2];              // keys they see
   int min_vis;                 // least of all the unit's rows
 };
 
-// Weights are held 2^kLift up, and a score may pass the maximum by 2^kLag (fp16
-// weights reach 2^15).
+// A score may pass the maximum by 2^kLag.  e4m3: weights are held 2^11 up (fp16 ones
+// reach 2^15).  bf16: they are held down by 2^kLag and the number of keys, so that
+// their sum is at most 1 and O stays within the largest value of V, whatever that is
+// (7 requests of up to 3527 keys, 40 rows a head, a lag of 2^4 / 2^8: 44.4 / 43.6 us).
+// That number's logarithm lies in shared memory: 32-row kernels have no register for it.
 template <int E>
-constexpr float kLift = E == 2 ? 0.f : 11.f;
+constexpr float kLag = E == 2 ? 8.f : 4.f;
 template <int E>
-constexpr float kLag = E == 2 ? 16.f : 4.f;
+__device__ __forceinline__ float lift(const float* factor) { return E == 1 ? 11.f : *factor; }
 
 template <int D, int E, int NT>
 __device__ __forceinline__ void start_rows(Rows<D, NT>& s, const AttnProblem& p, int Lq, int Lk, int row0, int lane) {
@@ -261,7 +264,7 @@ __device__ __forceinline__ void start_rows(Rows<D, NT>& s, const AttnProblem& p,
   for (int j = 0; j < NT; ++j) {
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      s.off[j][u] = kLift<E> - kNoMax;
+      s.off[j][u] = -kNoMax;
       s.l[j][u] = 0.f;
       const int r = row0 + 8 * j + 2 * c + u;
       int vis = Lk;
@@ -305,10 +308,11 @@ __device__ __forceinline__ void ask_queries(Queries<D, NT, THREADS>& s, const At
 }
 // The same as B operands in shared memory: lane (g, c)'s two words of row tile j
 // and step t at (j D / 16 + t) 256 + 8 lane.  e4m3: in fp16, each row divided by a
-// power of two, whose product with the scale goes to `factor`.
+// power of two, whose product with the scale goes to `factor`.  bf16: lift() goes there.
 template <int D, int E, int NT, int THREADS>
-__device__ __forceinline__ void put_queries(uint32_t* sq, float* factor, const Queries<D, NT, THREADS>& s, float scale, int thread) {
+__device__ __forceinline__ void put_queries(uint32_t* sq, float* factor, const Queries<D, NT, THREADS>& s, float scale, int Lk, int thread) {
   using Q = Queries<D, NT, THREADS>;
+  if (E == 2 && thread == 0) *factor = -kLag<E> - static_cast<float>(32 - __clz(Lk - 1));
 #pragma unroll
   for (int k = 0; k < Q::kPer; ++k) {
     const int i = k * THREADS + thread;
@@ -469,7 +473,7 @@ __device__ __forceinline__ void step(Rows<D, NT>& s, const uint32_t* sq, const f
       for (int u = 0; u < 4; ++u) y[i][j][u] = fmaf(x[i][j][u], cs[j][u & 1], s.off[j][u & 1]);
       top = fmax3(fmax3(top, y[i][j][0], y[i][j][1]), y[i][j][2], y[i][j][3]);
     }
-  if (__builtin_expect(__any_sync(0xffffffffu, top > kLift<E> + kLag<E>), 0)) {
+  if (__builtin_expect(__any_sync(0xffffffffu, top > lift<E>(factor) + kLag<E>), 0)) {
 #pragma unroll
     for (int j = 0; j < NT; ++j)
 #pragma unroll
@@ -480,9 +484,8 @@ __device__ __forceinline__ void step(Rows<D, NT>& s, const uint32_t* sq, const f
         mx *= cs[j][u];
 #pragma unroll
         for (int sh = 4; sh < 32; sh <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, sh));
-        const float old = kLift<E> - s.off[j][u], m = fmaxf(old, mx);
-        const float down = ex2_approx(old - m);
-        s.off[j][u] = kLift<E> - m;
+        const float off = fminf(s.off[j][u], lift<E>(factor) - mx), down = ex2_approx(off - s.off[j][u]);
+        s.off[j][u] = off;
         s.l[j][u] *= down;
 #pragma unroll
         for (int t = 0; t < kSteps; ++t) {
@@ -554,7 +557,8 @@ __device__ __forceinline__ void step(Rows<D, NT>& s, const uint32_t* sq, const f
   }
 }
 
-__device__ __forceinline__ float row_lse(float m, float l, float lift) { return (m - lift + log2f(l)) * 0.69314718055994531f; }
+// Of a sum of weights 2^(score - m).
+__device__ __forceinline__ float row_lse(float m, float l) { return (m + log2f(l)) * 0.69314718055994531f; }
 
 // Row tiles of a unit, 8 rows each: as many as the K/V head has rows, up to 4.
 inline int tiles_of(long long max_rows) { return max_rows <= 8 ? 1 : max_rows <= 16 ? 2 : 4; }

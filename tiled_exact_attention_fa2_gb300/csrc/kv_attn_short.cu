@@ -125,7 +125,7 @@ __device__ __forceinline__ void join_group(Rows<D, NT>& s, ShortSmem<D, E, NT>& 
 #pragma unroll
         for (int j = 0; j < NT; ++j)
 #pragma unroll
-          for (int u = 0; u < 2; ++u) sm.ml[warp][8 * j + 2 * c + u] = make_float2(kLift<E> - s.off[j][u], s.l[j][u]);
+          for (int u = 0; u < 2; ++u) sm.ml[warp][8 * j + 2 * c + u] = make_float2(-s.off[j][u], s.l[j][u]);
       }
     }
     sync_group(which, group);
@@ -135,12 +135,12 @@ __device__ __forceinline__ void join_group(Rows<D, NT>& s, ShortSmem<D, E, NT>& 
         for (int j = 0; j < NT; ++j)
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
-            const float m = kLift<E> - s.off[j][u];
+            const float m = -s.off[j][u];
             float top = m;
             for (int i = 1; i < group; ++i) top = fmaxf(top, sm.ml[warp + i][8 * j + 2 * c + u].x);
             w0[j][u] = ex2_approx(m - top);
             s.l[j][u] *= w0[j][u];
-            s.off[j][u] = kLift<E> - top;
+            s.off[j][u] = -top;
           }
       }
 #pragma unroll
@@ -156,7 +156,7 @@ __device__ __forceinline__ void join_group(Rows<D, NT>& s, ShortSmem<D, E, NT>& 
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
           const float2 a = sm.ml[warp + i][8 * j + 2 * c], b = sm.ml[warp + i][8 * j + 2 * c + 1];
-          const float wa = ex2_approx(a.x - (kLift<E> - s.off[j][0])), wb = ex2_approx(b.x - (kLift<E> - s.off[j][1]));
+          const float wa = ex2_approx(a.x + s.off[j][0]), wb = ex2_approx(b.x + s.off[j][1]);
           if (half == 0) {
             s.l[j][0] = fmaf(wa, a.y, s.l[j][0]);
             s.l[j][1] = fmaf(wb, b.y, s.l[j][1]);
@@ -189,7 +189,7 @@ __device__ __forceinline__ void write_rows(Rows<D, NT>& s, const AttnProblem& p,
       const int r = 8 * j + 2 * c + k;
       if (g == 0 && r < rows) {
         const int i = query_of(p, r), head = u.h * p.G + (r - i * p.G);
-        p.lse[static_cast<long long>(head) * p.total_q + u.q0 + i] = l == 0.f ? -INFINITY : row_lse(kLift<E> - s.off[j][k], l, kLift<E>);
+        p.lse[static_cast<long long>(head) * p.total_q + u.q0 + i] = l == 0.f ? -INFINITY : row_lse(-s.off[j][k], l);
       }
     }
     const int r = 8 * j + g, i = query_of(p, r), head = u.h * p.G + (r - i * p.G);
@@ -272,7 +272,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
   for (; unit < units; unit += stride) {
     if (now.Lq > 0) {
       ask_queries(queries, p, now.q0, now.Lq, now.h, 0, lane);
-      put_queries<D, E>(sm.q[warp], sm.factor[warp], queries, p.scale_log2, lane);
+      put_queries<D, E>(sm.q[warp], sm.factor[warp], queries, p.scale_log2, now.Lk, lane);
       start_rows<D, E, NT>(s, p, now.Lq, now.Lk, 0, lane);
       __syncwarp();
       for (int i = 0; alive && i < now.slots; ++i) {
