@@ -7,6 +7,7 @@ import torch
 
 import tiled_exact_attention_fa2_gb300 as fa2
 from test_kv import bits, check_attention, filled, i32
+from test_kv4 import check_attention as check4
 
 # B, H, H_kv, d, keys, bound on the keys: the line, clusters of 8 and 2 CTAs and single CTAs, four, two and one warps a unit
 FORMS = [(1, 4, 1, 128, 3000, None), (90, 4, 2, 64, 300, None), (1, 16, 1, 16, 20000, None), (1, 8, 1, 64, 2000, 2000), (20, 8, 2, 128, 1000, 1000),
@@ -51,3 +52,63 @@ def test_values_up_to_the_largest(form, scores):
     for b in some:
         check_attention(o[b:b + 1].double() / torch.from_numpy(top).cuda(), lse[:, b:b + 1], [(0, 1)], q[b:b + 1].double().cpu().numpy(),
                         [scaled[b]], 1.0, True, H, torch.bfloat16)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("form", [f for f in FORMS if f[0] in (1, 90, 350)], ids=str)
+@pytest.mark.parametrize("cache", ["bf16", "e4m3", "4 bit"])
+def test_infinite_queries(form, cache):
+    """Every key is positive in column 0 and of either sign elsewhere.  A query that is -inf there has no finite score,
+    however large its other values are (its scores are -inf, not NaN): zeros and -inf.  +inf, or a NaN: NaN.  Rows beside
+    them are right."""
+    B, H, Hkv, d, n, bound = form
+    rng = np.random.default_rng(n)
+    lens = [n] + [int(x) for x in rng.integers(n // 2, n + 1, B - 1)]
+    counts = [-(-m // 16) for m in lens]
+    table = np.full((B, 4096 if bound is None else max(counts)), -1)
+    order, at = rng.permutation(sum(counts)), 0
+    for b, c in enumerate(counts):
+        table[b, :c] = order[at:at + c]
+        at += c
+    k, v = (torch.from_numpy(rng.standard_normal((at * 16, Hkv, d))).to(torch.bfloat16).cuda() for _ in range(2))
+    k[..., 0] = 4 + k[..., 0].abs()
+    slots = torch.arange(at * 16, device="cuda")
+    if cache == "4 bit":
+        held = fa2.fa2_kv4_cache(at, Hkv, 16, d)
+        fa2.fa2_kv4_append(k, v, held, slots)
+        call = lambda q: fa2.fa2_kv4_attn(q, held, i32(table), i32(lens), max_seqlen_k=bound)  # noqa: E731
+    else:
+        held = fa2.fa2_kv_cache(at, Hkv, 16, d, dtype=torch.bfloat16 if cache == "bf16" else torch.float8_e4m3fn)
+        fa2.fa2_kv_append(k, v, *held, slots)
+        call = lambda q: fa2.fa2_kv_attn(q, *held, i32(table), i32(lens), max_seqlen_k=bound)  # noqa: E731
+    q = torch.from_numpy(rng.standard_normal((B, H, d))).to(torch.bfloat16).cuda()
+    want_o, want_lse = call(q)
+    odd = q.clone()
+    odd[:, 0, 1:] *= 1e6
+    odd[0, 0, 1:] = torch.where(odd[0, 0, 1:] < 0, -3e38, 3e38)
+    odd[:, 0, 0] = -math.inf
+    if H > 1:
+        odd[:, 1, 0] = math.inf
+    if H > 2:
+        odd[:, 2, 1], odd[:, 2, 2] = math.nan, 3e38
+    o, lse = call(odd)
+    # A bf16 cache's products are summed as they are: where those of the finite values pass fp32's range (sum |q| |k| >=
+    # 2^128, request 0 only: 1e6 times a normal number stays far below) their sum is an infinity itself, of either sign,
+    # and the score may be NaN.  The other caches' sums are of q divided by a power of two.
+    fits = torch.ones(B, dtype=torch.bool, device="cuda")
+    if cache == "bf16":
+        pages = torch.from_numpy(table[0, :counts[0]]).cuda()
+        sums = odd[0, 0, 1:].double().abs() @ held[0][pages, 0].reshape(-1, d)[:n, 1:].double().abs().T
+        fits[0] = bool(sums.max() < 2.0 ** 128)
+    assert torch.all(o[fits, 0] == 0) and torch.all(lse[0, fits] == -math.inf)
+    assert torch.all(torch.isnan(o[:, 1:3])) and torch.all(torch.isnan(lse[1:3]))
+    # (not to the bit: the running maxima of a unit's rows are raised together, when one of them is passed, and with them
+    # the weights' common factor; each of the two calls is held to the definition)
+    o[:, :3], lse[:3] = want_o[:, :3], want_lse[:3]
+    for b in (0, B - 1):
+        pages, cu = i32(table[b:b + 1]), i32([0, lens[b]])
+        got = fa2.fa2_kv4_gather(held, pages, cu, lens[b]) if cache == "4 bit" else fa2.fa2_kv_gather(*held, pages, cu, lens[b])
+        kv = [tuple(x.double().cpu().numpy().transpose(1, 0, 2) for x in got)]
+        for x, y in ((o, lse), (want_o, want_lse)):
+            args = x[b:b + 1], y[:, b:b + 1], [(0, 1)], q[b:b + 1].double().cpu().numpy(), kv, d ** -0.5, True, H
+            check4(*args) if cache == "4 bit" else check_attention(*args, held[0].dtype)

@@ -360,18 +360,17 @@ __device__ __forceinline__ void start_unit(Rows<D, NT>& s, const Attn4Problem& p
 #pragma unroll
   for (int j = 0; j < NT; ++j) {
     uint32_t (&w)[kPer / 2] = raw[j];
-    // the power of two at or below the row's largest magnitude (1 for a row
-    // of zeros, infinities or NaN)
+    // the power of two at or below the row's largest finite magnitude (1 for a row
+    // without one but 0): beside an infinity the others stay finite, too
     float mx = 0.f;
 #pragma unroll
     for (int i = 0; i < kPer / 2; ++i) {
       const float2 f = unpack_bf16x2(w[i]);
-      mx = fmaxf(mx, fmaxf(fabsf(f.x), fabsf(f.y)));
+      mx = fmaxf(mx, fmaxf(finite_abs(f.x), finite_abs(f.y)));
     }
     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-    const bool plain = mx == 0.f || isinf(mx);
-    const int e = plain ? 0 : min(max(static_cast<int>(__float_as_uint(mx) >> 23) - 127, -126), 126);
+    const int e = mx == 0.f ? 0 : min(max(static_cast<int>(__float_as_uint(mx) >> 23) - 127, -126), 126);
     const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
     // (kept off zero and infinity: the score of a masked key is -inf times it)
     const float up = fminf(fmaxf(__uint_as_float(static_cast<uint32_t>(127 + e) << 23) * p.scale_log2, 1e-37f), 3e38f);

@@ -324,19 +324,18 @@ __device__ __forceinline__ void put_queries(uint32_t* sq, float* factor, const Q
 #pragma unroll
       for (int c = 0; c < 4; ++c) to[2 * c + (x & 1)] = w[c];
     } else {
-      // the power of two at or below the row's largest magnitude (1 for a row
-      // of zeros, infinities or NaN)
+      // the power of two at or below the row's largest finite magnitude (1 for a row
+      // without one but 0): beside an infinity the others stay finite, too
       float mx = 0.f;
 #pragma unroll
       for (int m = 0; m < 4; ++m) {
         const float2 f = unpack_bf16x2(w[m]);
-        mx = fmaxf(mx, fmaxf(fabsf(f.x), fabsf(f.y)));
+        mx = fmaxf(mx, fmaxf(finite_abs(f.x), finite_abs(f.y)));
       }
       constexpr uint32_t kMask = Q::kPieces >= 32 ? 0xffffffffu : (1u << (Q::kPieces & 31)) - 1u;
 #pragma unroll
       for (int sh = 1; sh < Q::kLanes; sh <<= 1) mx = fmaxf(mx, __shfl_xor_sync(kMask, mx, sh));
-      const bool plain = mx == 0.f || isinf(mx);
-      const int e = plain ? 0 : min(max(static_cast<int>(__float_as_uint(mx) >> 23) - 127, -126), 126);
+      const int e = mx == 0.f ? 0 : min(max(static_cast<int>(__float_as_uint(mx) >> 23) - 127, -126), 126);
       const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
 #pragma unroll
       for (int m = 0; m < 4; ++m) {

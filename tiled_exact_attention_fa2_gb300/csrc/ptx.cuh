@@ -523,6 +523,12 @@ __device__ __forceinline__ float f16lo_to_f32(uint32_t v) {
   return f;
 }
 
+// |x| of a finite number, else 0.
+__device__ __forceinline__ float finite_abs(float x) {
+  const float a = fabsf(x);
+  return a <= 3.402823466e38f ? a : 0.f;
+}
+
 __device__ __forceinline__ float2 unpack_bf16x2(uint32_t v) {
   return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
 }
