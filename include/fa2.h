@@ -529,11 +529,16 @@ int fa2_kv4_attn(const void* q, const void* cache, long long page_stride, const 
  * slowed down by the factor, those that turn high_turns times or more are left,
  * and those between are mixed.  trained_positions = 0: all are slowed down (g =
  * 0: positions interpolated; factor = 1: the plain table).  Another base is the
- * caller's.  A value is within (2^-21 + position 2^-51) times the amplitude of
- * the definition.  rot_dim: a multiple of 16, 16 to 128; positions from 0 to
- * 2^31 - 1.  base, factor, amplitude: finite and > 0, trained_positions finite and
- * >= 0, low_turns < high_turns where they count (FA2_ERR_SCALE).  num_positions
- * = 0 is allowed and does nothing.  One launch.
+ * caller's.  A value is within (2^-21 + position e) times the amplitude of the
+ * definition, e = 2^-50 max(1, 1 / base) max(1, 1 / factor) what fp64 leaves of
+ * theta'; with trained_positions > 0, e = 2^-49 times these and max(1, high_turns /
+ * (high_turns - low_turns)).  rot_dim: a multiple of 16, 16 to 128; positions from
+ * 0 to 2^31 - 1.  base, factor, amplitude: finite and > 0 (the amplitude at least
+ * fp32's least normal number), trained_positions finite and >= 0, low_turns <
+ * high_turns where they count, no theta' of 2 pi 2^52 or more (FA2_ERR_SCALE).
+ * num_positions = 0 is allowed and does nothing.  One launch.
+ * Tables that mix their columns in another way (by the column's number between two
+ * borders, or with a factor of its own for each column) are the caller's to make.
  */
 int fa2_rope_table(float* rope_table, long long first_position, int num_positions, int rot_dim, double base, double factor,
                    double trained_positions, double low_turns, double high_turns, double amplitude, void* stream);

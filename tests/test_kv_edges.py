@@ -112,3 +112,46 @@ def test_infinite_queries(form, cache):
         for x, y in ((o, lse), (want_o, want_lse)):
             args = x[b:b + 1], y[:, b:b + 1], [(0, 1)], q[b:b + 1].double().cpu().numpy(), kv, d ** -0.5, True, H
             check4(*args) if cache == "4 bit" else check_attention(*args, held[0].dtype)
+
+
+def test_table_amplitudes_that_fp32_has_no_digits_for():
+    from tiled_exact_attention_fa2_gb300 import _build
+    _build.build()
+    lib = fa2.load_library()
+    call = lambda amp: lib.fa2_rope_table(None, 0, 0, 32, 1e4, 1.0, 0.0, 1.0, 32.0, amp, None)  # noqa: E731
+    for amp in (1e-39, 2.0 ** -127, 1e39, 1e-60):
+        assert call(amp) == 5, amp
+    for amp in (2.0 ** -126, 3.4e38):
+        assert call(amp) == 0, amp
+
+
+def near(column, rot, trained, width):
+    """Borders of 1 +- width times the turns that a column makes, base 10^4."""
+    turns = trained * 10000.0 ** (-2.0 * column / rot) / (2 * math.pi)
+    return dict(low=turns * (1 - width), high=turns * (1 + width))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("first,n,rot,args", [
+    (0, 5, 112, dict(base=1e-12)), (1000, 3000, 128, dict(base=1e-6)), (0, 300, 48, dict(base=3e-8, amplitude=2.0 ** -126)), (7, 1000, 96, dict(base=1e4, factor=1e-3)),
+    ((1 << 31) - 50, 50, 112, dict(base=12.7)), (1 << 20, 99, 64, dict(base=1e4, factor=8.0, trained=8192, **near(10, 64, 8192, 2.0 ** -12))),
+    (1 << 24, 77, 80, dict(base=1e4, factor=0.25, trained=100000, **near(3, 80, 100000, 2.0 ** -5))), (5, 64, 128, dict(base=1e4, amplitude=3e38))])
+def test_table_within_the_stated_bound(first, n, rot, args):
+    """The bound that the header states, for every base and factor: 2^-21 from fp32 (test_rope.py) and, a position, what
+    fp64 leaves of theta'.  Its relative error: the power 1.04 2^-53 and its exponent's correction 2^-53, 1 - g, the
+    quotient by the factor, the sum, the product, the quotient by 2 pi 2^-53 each and 2 pi itself 2^-54.5: 7.4 2^-53 <
+    2^-50, times theta' <= max(1, 1 / base) max(1, 1 / factor).  Mixed columns: g is off by (4.4 high / (high - low) + 3)
+    2^-53 more, where turns <= high: less than 15 2^-53 max(1, high / (high - low)) < 2^-49 of it, together."""
+    import oracle.kv as ref
+
+    call = dict(args)
+    for a, b in (("trained", "trained_positions"), ("low", "low_turns"), ("high", "high_turns")):
+        if a in call:
+            call[b] = call.pop(a)
+    got = fa2.fa2_rope_table(n, rot, first_position=first, **call).cpu().numpy().astype(np.longdouble)
+    e = 2.0 ** -50 * max(1.0, 1 / args["base"]) * max(1.0, 1 / args.get("factor", 1.0))
+    if "trained" in args:
+        e *= 2 * max(1.0, args["high"] / (args["high"] - args["low"]))
+    tol = (2.0 ** -21 + np.arange(first, first + n)[:, None] * e) * args.get("amplitude", 1.0)
+    err = np.abs(got - ref.table(first, n, rot, **args))
+    assert np.all(err <= tol), float((err / tol).max())

@@ -123,7 +123,8 @@ __device__ __forceinline__ void cos_sin(unsigned long long phase, float& c, floa
 
 // A thread takes four columns of every gridDim.x blockDim.y-th position.  The
 // angle p theta_i in turns is an integer product modulo 2^64 of the position and
-// the column's 64-bit share of a turn: off by p 2^-65 turns at most, for any
+// the column's 64-bit share of a turn.  That share comes from fp64 (off by about 2^-55
+// turns where theta is at most 1); the product adds nothing to p times its error, at any
 // position, where fp32 angles lose all digits and fp64 ones would run at a
 // hundredth of the rate.  Every second row is the one before it turned by the step
 // between them (four products in place of some thirty instructions a column).
@@ -290,13 +291,16 @@ int fa2_rope_table(float* rope_table, long long first_position, int num_position
       first_position > 0x80000000LL - num_positions)
     return FA2_ERR_SHAPE;
   auto positive = [](double x) { return std::isfinite(x) && x > 0; };
-  if (!positive(base) || !positive(factor) || !positive(amplitude) || !positive(static_cast<float>(amplitude))) return FA2_ERR_SCALE;
+  if (!positive(base) || !positive(factor) || !positive(amplitude) || !std::isnormal(static_cast<float>(amplitude))) return FA2_ERR_SCALE;
   if (!(std::isfinite(trained_positions) && trained_positions >= 0)) return FA2_ERR_SCALE;
   if (trained_positions > 0 && !(std::isfinite(low_turns) && std::isfinite(high_turns) && low_turns < high_turns)) return FA2_ERR_SCALE;
   TableProblem p{};
   p.half = rot_dim / 2;
   for (int i = 0; i < p.half; ++i) {
-    const double theta = std::pow(base, -2.0 * i / rot_dim);
+    // (the exponent's own rounding, times the logarithm of the base, would be most of the error of a base far below 1)
+    const double exponent = -2.0 * i / rot_dim, rest = std::fma(-exponent, rot_dim, -2.0 * i) / rot_dim;
+    double theta = std::pow(base, exponent);
+    theta += theta * (rest * std::log(base));
     double keep = 0;
     if (trained_positions > 0)
       keep = std::fmin(1.0, std::fmax(0.0, (trained_positions * theta / kTwoPi - low_turns) / (high_turns - low_turns)));
