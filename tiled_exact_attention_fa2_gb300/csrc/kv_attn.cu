@@ -543,6 +543,10 @@ template <int D, int E, int NT>
 __device__ __forceinline__ void find_items(Fixed<D, E, NT>& sm, const AttnProblem& p, int lane) {
   constexpr int kRows = 8 * NT, kKeys = Tile<D, E>::kKeys;
   bool fine = true, mixed = false;
+  // One join waits for the next description, no more: with a part of kAhead slots open, no third
+  // item is described, so a second part is not done before.  (Parts of a wave may be
+  // shorter; a CTA has one item of it.  A part is at least three quarters of the cut.)
+  static_assert(kMinItem<D, E, NT> / 4 * 3 >= kAhead, "parts that are done before a finished unit's join is described");
   const Layout y = layout<kRows, kKeys, kMinItem<D, E, NT>>(p, fine, mixed, lane);
   if (blockIdx.x == 0 && lane == 0 && (!fine || mixed)) atomicCAS(&g_kv_attn_status, kDevOk, kDevBadSeqlens);
   int id = mixed ? INT_MAX : static_cast<int>(blockIdx.x);  // (offsets out of order: nothing is written)
