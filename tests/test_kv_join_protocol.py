@@ -142,10 +142,15 @@ def test_every_cut_unit_is_joined_once(least):
 
 
 def test_model_catches_parts_that_are_too_short():
+    """Units of 6 to 60 slots in two or three parts, whatever their length."""
     found = []
     for seed in range(150):
         r = random.Random(seed)
-        found.append(Run(seed, cut_into_items([r.randint(10, 60) for _ in range(80)], 8, 8), 8).run())
+        items = []
+        for u in range(60):
+            n, parts = r.randint(6, 60), r.randint(2, 3)
+            items += [(u, i, parts, n * i // parts, n * (i + 1) // parts - n * i // parts) for i in range(parts)]
+        found.append(Run(seed, items, 3).run())
     assert any(f and "lost" in f for f in found)
 
 
