@@ -155,3 +155,83 @@ def test_table_within_the_stated_bound(first, n, rot, args):
     tol = (2.0 ** -21 + np.arange(first, first + n)[:, None] * e) * args.get("amplitude", 1.0)
     err = np.abs(got - ref.table(first, n, rot, **args))
     assert np.all(err <= tol), float((err / tol).max())
+
+
+def queue_word(ws):
+    """The queue's counter in a workspace of fa2_kv_attn: behind the two times 1440 counters of parts."""
+    return ws[ws.numel() - -(-2881 * 8 // 256) * 256 + 2880 * 8:][:8].view(torch.int64)
+
+
+@pytest.mark.gpu
+def test_a_workspace_with_half_of_a_calls_number():
+    """A workspace may hold anything: also a word whose upper 32 bits are those of the call's number.  (A captured call
+    keeps its number, and the queue's word is left at it.)"""
+    rng = np.random.default_rng(5)
+    lens = [int(x) for x in rng.integers(1, 400, 120)]
+    caches, table, kv = filled(rng, lens, 4, 16, 32, torch.bfloat16, width=4096)
+    q = torch.from_numpy(rng.standard_normal((120, 4, 32))).to(torch.bfloat16).cuda()
+    ws = torch.zeros(fa2.fa2_kv_attn_workspace_bytes(120, 4, 4, 1, 4096 * 16, 32), dtype=torch.uint8, device="cuda")
+    t, n = i32(table), i32(lens)
+    fa2.fa2_device_status(reset=True)
+    want = fa2.fa2_kv_attn(q, *caches, t, n, workspace=ws)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = fa2.fa2_kv_attn(q, *caches, t, n, workspace=ws)
+    for low in (0, 1, 0x1234):
+        graph.replay()
+        word = queue_word(ws)
+        word.copy_((word ^ (1 << 16)) | low)
+        for x in got:
+            x.fill_(9)
+        graph.replay()
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    assert fa2.fa2_device_status() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("B,Hkv", [(8300, 8), (33000, 4)])  # more than 65383 + 304 items; twice as many
+def test_more_items_than_the_queue_counts(B, Hkv):
+    """Items are then taken in runs: none is left out, a longer request among them is still cut; the same again from a
+    captured call, whatever the workspace holds, and as with the warp form's bound."""
+    d, P = 16, 16
+    rng = np.random.default_rng(B)
+    lens = [0 if i % 1000 == 7 else int(x) for i, x in enumerate(rng.integers(1, 33, B))]
+    assert B * Hkv - Hkv * lens.count(0) > 65383 + 304
+    lens[B // 2] = 20000
+    g = torch.Generator("cuda").manual_seed(1)
+    pages = 3000
+    caches = fa2.fa2_kv_cache(pages, Hkv, P, d)
+    for c in caches:
+        c.copy_(torch.randn(c.shape, generator=g, device="cuda"))
+    table = torch.randint(0, pages, (B, 20000 // P), generator=g, device="cuda", dtype=torch.int32)  # (requests share pages)
+    q = torch.randn((B, Hkv, d), generator=g, device="cuda").to(torch.bfloat16)
+    n = i32(lens)
+    ws = torch.full((fa2.fa2_kv_attn_workspace_bytes(B, Hkv, Hkv, 1, 20000, d),), 0xFF, dtype=torch.uint8, device="cuda")
+    assert ws.numel() > 0
+    fa2.fa2_device_status(reset=True)
+    o, lse = torch.full_like(q, 9.0), torch.full((Hkv, B), 9.0, device="cuda")
+    call = lambda: fa2.fa2_kv_attn(q, *caches, table, n, o=o, lse=lse, workspace=ws)  # noqa: E731
+    call()
+    assert not torch.any(lse == 9)
+    first = o.clone(), lse.clone()
+    some = sorted({0, 1, B // 2, B - 1} | {int(x) for x in rng.integers(0, B, 200)})
+    for b in some:
+        got = fa2.fa2_kv_gather(*caches, table[b:b + 1].contiguous(), i32([0, lens[b]]), lens[b])
+        kv = tuple(x.double().cpu().numpy().transpose(1, 0, 2) for x in got)
+        check_attention(o[b:b + 1], lse[:, b:b + 1], [(0, 1)], q[b:b + 1].double().cpu().numpy(), [kv], d ** -0.5, True, Hkv, torch.bfloat16)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    for fill in (0, 0x5A, None):
+        if fill is not None:
+            ws.fill_(fill)
+        o.fill_(9), lse.fill_(9)
+        graph.replay()
+        assert torch.equal(o, first[0]) and torch.equal(lse, first[1])
+    # Without the long request the warp form may take them: the same to two roundings of bf16 and twice check_attention's
+    # bound, (2^-16 + 2 x) mass with scale sum |q| |k| < 2^4, so x < 2^-14 + 2^-20, and mass < 4: 2^-9.8.
+    n[B // 2] = 32
+    call()
+    short = fa2.fa2_kv_attn(q, *caches, table, n, max_seqlen_k=32)
+    assert torch.all((o.float() - short[0].float()).abs() <= 2.0 ** -7 * o.float().abs() + 2.0 ** -9)
+    assert fa2.fa2_device_status() == 0

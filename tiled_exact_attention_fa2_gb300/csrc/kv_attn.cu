@@ -467,15 +467,13 @@ __device__ __forceinline__ void join_parts(const AttnProblem& p, const Unit& it,
 }
 
 // Counters.  A workspace may hold anything, so a counter counts only where it
-// carries the call's number (in the bits from SHIFT on): a CTA sees to that for its
+// carries the call's number (in its upper 48 bits): a CTA sees to that for its
 // share of them when it begins, or whoever adds before.  The last to add sets it
 // back, so a graph may be replayed with the same number.
-template <int SHIFT>
-__device__ __forceinline__ unsigned long long unused(unsigned long long call) { return call >> SHIFT << SHIFT; }
-template <int SHIFT>
+constexpr int kMaxRuns = 0xffff - kCtas;  // (each CTA asks once more than it is given)
 __device__ __forceinline__ void claim(unsigned long long* counter, unsigned long long call) {
   const unsigned long long old = *static_cast<volatile unsigned long long*>(counter);
-  if ((old ^ call) >> SHIFT != 0) atomicCAS(counter, old, unused<SHIFT>(call));  // (if another was faster, it is done)
+  if ((old ^ call) >> 16 != 0) atomicCAS(counter, old, call);  // (if another was faster, it is done)
 }
 // One more, and the count before (releases what the CTA has written, acquires what
 // those before it have).
@@ -485,28 +483,27 @@ __device__ __forceinline__ unsigned long long add_one(unsigned long long* counte
   return old;
 }
 // The count before, of what add_one returned.
-template <int SHIFT>
 __device__ __forceinline__ unsigned long long counted(unsigned long long* counter, unsigned long long old, unsigned long long call) {
-  while ((old ^ call) >> SHIFT != 0) {  // it was not this call's yet
+  while ((old ^ call) >> 16 != 0) {  // it was not this call's yet
     const unsigned long long seen = *static_cast<volatile unsigned long long*>(counter);
-    if ((seen ^ call) >> SHIFT == 0) {
+    if ((seen ^ call) >> 16 == 0) {
       old = add_one(counter);
     } else {
       unsigned long long got;
       asm volatile("atom.cas.acq_rel.gpu.global.b64 %0, [%1], %2, %3;"
-                   : "=l"(got) : "l"(counter), "l"(seen), "l"(unused<SHIFT>(call) + 1) : "memory");
-      if (got == seen) old = unused<SHIFT>(call);  // (the first)
+                   : "=l"(got) : "l"(counter), "l"(seen), "l"(call + 1) : "memory");
+      if (got == seen) old = call;  // (the first)
     }
   }
-  return old - unused<SHIFT>(call);
+  return old - call;
 }
 // Whether all `count` parts are there with this one (the same for the CTA, whose
 // threads have written theirs).
 __device__ __forceinline__ bool arrive(unsigned long long* counter, unsigned long long call, int count, int* flag) {
   sync_warps();
   if (threadIdx.x == 0) {
-    const bool last = static_cast<int>(counted<16>(counter, add_one(counter), call)) + 1 == count;
-    if (last) atomicExch(counter, unused<16>(call));
+    const bool last = static_cast<int>(counted(counter, add_one(counter), call)) + 1 == count;
+    if (last) atomicExch(counter, call);
     *flag = last;
   }
   sync_warps();
@@ -551,6 +548,9 @@ __device__ __forceinline__ void find_items(Fixed<D, E, NT>& sm, const AttnProble
   if (blockIdx.x == 0 && lane == 0 && (!fine || mixed)) atomicCAS(&g_kv_attn_status, kDevOk, kDevBadSeqlens);
   int id = mixed ? INT_MAX : static_cast<int>(blockIdx.x);  // (offsets out of order: nothing is written)
   bool there = id < y.total;
+  // The queue hands out runs of items, of one each unless they are more than its counter can count.
+  const int left = max(y.total - 2 * kCtas, 0), run = left / kMaxRuns + 1, runs = (left + run - 1) / run;
+  int until = 0;  // where the run that was taken ends
   int described = 0, done = 0, open = 0, ahead = 0;  // descriptions, those that are done; items and slots that are not done
   Unit join{};  // to be joined, of its group `group`
   int group = 0;
@@ -570,13 +570,14 @@ __device__ __forceinline__ void find_items(Fixed<D, E, NT>& sm, const AttnProble
       if (id == INT_MIN) {  // (an item is better taken by a CTA that is free)
         if (lane == 0) {
           // (every CTA asks until it is told that there is no more; the last to hear so sets the queue back)
-          const int n = static_cast<int>(counted<32>(p.queue, add_one(p.queue), p.call)), left = max(y.total - 2 * kCtas, 0);
-          if (n == left + min(kCtas, y.total - kCtas) - 1) atomicExch(p.queue, unused<32>(p.call));
-          id = n < left ? 2 * kCtas + n : INT_MAX;
+          const int n = static_cast<int>(counted(p.queue, add_one(p.queue), p.call));
+          if (n == runs + min(kCtas, y.total - kCtas) - 1) atomicExch(p.queue, p.call);
+          id = n < runs ? 2 * kCtas + n * run : INT_MAX;
         }
         id = __shfl_sync(0xffffffffu, id, 0);
         there = id < y.total;
         if (!there) continue;
+        until = min(id + run, y.total);
       }
       Desc d{};
       const Item it = find_item<kRows, kKeys>(y, p, id, lane);
@@ -587,12 +588,12 @@ __device__ __forceinline__ void find_items(Fixed<D, E, NT>& sm, const AttnProble
       ahead += it.len;
       if (described == 1) {
         // (counters that this CTA claims)
-        for (int i = blockIdx.x + lane * kCtas; i < 2 * kPlaces; i += 32 * kCtas) claim<16>(p.arrived + i, p.call);
-        if (blockIdx.x == 0 && lane == 31) claim<32>(p.queue, p.call);
+        for (int i = blockIdx.x + lane * kCtas; i < 2 * kPlaces; i += 32 * kCtas) claim(p.arrived + i, p.call);
+        if (blockIdx.x == 0 && lane == 31) claim(p.queue, p.call);
         id += kCtas;
         there = id < y.total;
       } else {
-        id = INT_MIN;  // from the queue, when there is room for it
+        id = id + 1 < until ? id + 1 : INT_MIN;  // (the latter: from the queue, when there is room for it)
       }
       continue;
     }
@@ -624,8 +625,8 @@ __device__ __forceinline__ void find_items(Fixed<D, E, NT>& sm, const AttnProble
         const bool one = u.parts <= kJoin;
         const int from = part / kJoin * kJoin, size = one ? u.parts : min(kJoin, u.parts - from);
         unsigned long long* const counter = p.arrived + (one ? u.place : kPlaces + u.place + from);
-        last = static_cast<int>(counted<16>(counter, add_one(counter), p.call)) + 1 == size;
-        if (last) atomicExch(counter, unused<16>(p.call));
+        last = static_cast<int>(counted(counter, add_one(counter), p.call)) + 1 == size;
+        if (last) atomicExch(counter, p.call);
       }
       if (__shfl_sync(0xffffffffu, last, 0)) join = u, group = part / kJoin;
     }
@@ -960,8 +961,9 @@ int launch_attn(const CacheMaps& maps, const AttnProblem& p, cudaStream_t st) {
   }
 }
 
-// A number for a call's counters, from a random one on: no word that a workspace
-// happens to hold has it but by a chance of 2^-48.
+// A number for a call's counters, from a random one on: a word that a workspace
+// happens to hold has it by a chance of 2^-48, one of those that a call may count in
+// by 2^-36.
 unsigned long long first_call() {
   try {
     std::random_device r;

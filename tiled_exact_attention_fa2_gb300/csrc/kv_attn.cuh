@@ -53,8 +53,8 @@ struct AttnProblem {
   float* part;        // [kPlaces][rows][d] unnormalised O
   float2* part_ml;    // [kPlaces][rows] maximum - lift (log2), sum
   unsigned long long* arrived;  // [2][kPlaces]: this call's number in the upper 48 bits, parts that are there in the lower
-  unsigned long long* queue;    // its upper 32 bits, and items that have been taken
-  unsigned long long call;      // that number, in the upper 48 bits
+  unsigned long long* queue;    // the number, and runs of items that have been taken
+  unsigned long long call;      // the number, in the upper 48 bits
   uint32_t g_mul, g_shift;      // r / G = (umulhi(r, g_mul) + r) >> g_shift
   int num_pages, shift, heads;  // pages of 1 << shift tokens
   int B, H, G, total_q, max_q, max_k;
