@@ -235,3 +235,23 @@ def test_more_items_than_the_queue_counts(B, Hkv):
     short = fa2.fa2_kv_attn(q, *caches, table, n, max_seqlen_k=32)
     assert torch.all((o.float() - short[0].float()).abs() <= 2.0 ** -7 * o.float().abs() + 2.0 ** -9)
     assert fa2.fa2_device_status() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", [torch.bfloat16, torch.float8_e4m3fn], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("B,H,Hkv,d,bound", [(100, 8, 2, 64, None), (2, 16, 1, 128, None), (100, 40, 2, 32, None), (3, 8, 2, 64, 40), (30, 8, 2, 128, 40),
+                                             (100, 8, 2, 16, 40), (150, 15, 3, 64, 40), (400, 4, 2, 128, 40)])
+def test_weights_keep_more_bits_than_one_16_bit_number(B, H, Hkv, d, bound, kind):
+    """Few keys of scores near one another and values of either sign: outputs that nearly cancel show how the weights were
+    rounded.  A weight is the sum of two numbers of 16 bits: 2^-16 relative, of either type (one fp16 number, 2^-11, leaves
+    the bound four times over in one output of sixty).  Below fp16's normal numbers a weight is off by 2^-36 of the sum
+    (test_kv.py), 40 of them by less than the 2^-19 that the bound has for the exponential."""
+    rng = np.random.default_rng(B + d)
+    lens = [int(x) for x in rng.integers(3, 41, B)]
+    factors = (1.0, 1.0) if kind == torch.bfloat16 else (2.0 ** -6, 2.0 ** -6)
+    caches, table, kv = filled(rng, lens, Hkv, 16, d, kind, factors, width=1 if bound else 4096, spread=0.5)
+    q = torch.from_numpy(rng.standard_normal((B, H, d)) * 0.25).to(torch.bfloat16).cuda()
+    fa2.fa2_device_status(reset=True)
+    o, lse = fa2.fa2_kv_attn(q, *caches, i32(table), i32(lens), max_seqlen_k=bound, k_scale=factors[0], v_scale=factors[1])
+    check_attention(o, lse, [(b, b + 1) for b in range(B)], q.double().cpu().numpy(), kv, d ** -0.5, True, H, torch.bfloat16)
+    assert fa2.fa2_device_status() == 0

@@ -10,13 +10,18 @@
 // made fp16 in registers; which columns a lane then holds is another order of
 // the contraction (of S, Q has the same) or of O's columns.
 //
-// Precision.  bf16: scores are exact products summed in fp32; P is split into
-// two bf16 numbers, high and low part, 16 significant bits together, for two
-// instructions instead of one: the matrix pipe has the time.  e4m3 is exact in
+// Precision.  P is split into two numbers of the cache's 16-bit type, high and low
+// part, for two instructions instead of one: 16 significant bits of bf16, 22 of
+// fp16.  One fp16 number (11 bits) would make O differ from an fp32 P's by 0.05 to
+// 0.1 % (its rounding to bf16 hides that from nothing but sums that nearly cancel);
+// the second costs what the matrix pipe and the conversions have no time left for: e4m3,
+// 128 columns, one and two parts, us: 2 x 131072 keys, 16 rows a head 50.5 / 50.5, 32 rows
+// 64.5 / 75.9; 64 requests of up to 1024, 4 rows 21.1 / 22.5; 300 of up to 512 41.5 / 43.1.
+// bf16: scores are exact products summed in fp32.  e4m3 is exact in
 // fp16; Q (8 bits) is divided by a power of two per row so that its largest
 // value is in [1, 2), exact in fp16 down to 2^-14 of it (2^-25 absolute below);
-// P is rounded to fp16 (11 bits), held 2^11 up so that weights down to 2^-25 of
-// the largest keep all 11.  The running maximum is raised only when a score
+// P is held 2^11 up so that weights down to 2^-25 of the largest keep all bits of
+// the high part.  The running maximum is raised only when a score
 // passes it by kLag, which saves the tile's maximum and the rescaling of O for
 // nearly every tile.  Maximum, sum and O are fp32; the quotient removes the
 // common factor exactly.  Any finite V gives a finite O: see lift().
@@ -168,6 +173,14 @@ __device__ __forceinline__ uint32_t max_abs(uint32_t a, uint32_t b) {
   else
     asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
+}
+// Two numbers as a pair of fp16 or bf16, and back.
+template <bool F16>
+__device__ __forceinline__ uint32_t pack(float lo, float hi) { return F16 ? pack_f16x2(lo, hi) : pack_bf16x2(lo, hi); }
+template <bool F16>
+__device__ __forceinline__ float2 unpack(uint32_t v) {
+  if constexpr (!F16) return unpack_bf16x2(v);
+  return make_float2(f16lo_to_f32(v), f16lo_to_f32(v >> 16));
 }
 // Two e4m3 numbers (the low 16 bits) as an fp16 pair.
 __device__ __forceinline__ uint32_t e4m3x2_to_f16(uint32_t w) {
@@ -351,9 +364,8 @@ __device__ __forceinline__ void put_queries(uint32_t* sq, float* factor, const Q
   }
 }
 
-// bf16 P is a sum of two numbers.
-template <int E>
-constexpr int kParts = E == 2 ? 2 : 1;
+// P is a sum of two numbers.
+constexpr int kParts = 2;
 
 // Keys of a slot's tile i: its first `end` keys less those of the tiles before,
 // none where its bit of `bad` is set (a page id out of range).
@@ -363,7 +375,7 @@ __device__ __forceinline__ int tile_keys(int end, uint32_t bad, int i) { return 
 // an infinity or NaN: rows that see the same number n of the tile's keys are taken
 // together, V of later keys as zeros.
 template <int D, int E, int NT>
-__device__ __forceinline__ void odd_values(Rows<D, NT>& s, const uint32_t (&pb)[NT][kParts<E>][2], uint32_t v_half, int tile, int t0,
+__device__ __forceinline__ void odd_values(Rows<D, NT>& s, const uint32_t (&pb)[NT][kParts][2], uint32_t v_half, int tile, int t0,
                                            int key0, int keys, int lane) {
   constexpr int kSteps = D / 16, kPer = E == 1 && D >= 32 ? 2 : 1, kGroup = kSteps < 4 ? kSteps : 4;
 #pragma unroll 1
@@ -392,6 +404,8 @@ __device__ __forceinline__ void odd_values(Rows<D, NT>& s, const uint32_t (&pb)[
             if ((v[u] >> 16 & 0x7f80u) == 0x7f80u) v[u] &= 0x0000ffffu;
           }
           mma<false>(add, v, pb[j][1][0], pb[j][1][1]);
+        } else {
+          mma<true>(add, a[t], pb[j][1][0], pb[j][1][1]);
         }
 #pragma unroll
         for (int u = 0; u < 4; ++u)
@@ -498,7 +512,7 @@ __device__ __forceinline__ void step(Rows<D, NT>& s, const uint32_t* sq, const f
         }
       }
   }
-  uint32_t pb[TILES][NT][kParts<E>][2];
+  uint32_t pb[TILES][NT][kParts][2];
 #pragma unroll
   for (int i = 0; i < TILES; ++i)
 #pragma unroll
@@ -510,14 +524,10 @@ __device__ __forceinline__ void step(Rows<D, NT>& s, const uint32_t* sq, const f
       s.l[j][1] += e[1] + e[3];
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        if constexpr (E == 2) {
-          const uint32_t hi = pack_bf16x2(e[2 * k], e[2 * k + 1]);
-          const float2 f = unpack_bf16x2(hi);
-          pb[i][j][0][k] = transpose8x8(hi);
-          pb[i][j][1][k] = transpose8x8(pack_bf16x2(e[2 * k] - f.x, e[2 * k + 1] - f.y));
-        } else {
-          pb[i][j][0][k] = transpose8x8(pack_f16x2(e[2 * k], e[2 * k + 1]));
-        }
+        const uint32_t hi = pack<E == 1>(e[2 * k], e[2 * k + 1]);
+        const float2 f = unpack<E == 1>(hi);
+        pb[i][j][0][k] = transpose8x8(hi);
+        pb[i][j][1][k] = transpose8x8(pack<E == 1>(e[2 * k] - f.x, e[2 * k + 1] - f.y));
       }
     }
   // O in groups of up to four blocks of columns.  An infinity or NaN in V takes
@@ -551,7 +561,7 @@ __device__ __forceinline__ void step(Rows<D, NT>& s, const uint32_t* sq, const f
 #pragma unroll
         for (int j = 0; j < NT; ++j)
 #pragma unroll
-          for (int k = 0; k < kParts<E>; ++k) mma<E == 1>(s.o[j][t0 + t], a[t], pb[i][j][k][0], pb[i][j][k][1]);
+          for (int k = 0; k < kParts; ++k) mma<E == 1>(s.o[j][t0 + t], a[t], pb[i][j][k][0], pb[i][j][k][1]);
     }
   }
 }
