@@ -26,9 +26,10 @@
 //
 // Measured (128 columns): 48 requests of up to 8191 keys, 8 K/V heads, bf16 149 us
 // (6.8 TB/s, a copy's rate); 64 of up to 1024 36 us (4.8 TB/s); 2 of 131072 keys, 4 K/V
-// heads, 4 queries each, e4m3 49 us (5.1 TB/s: the join of 19 parts of 16 rows takes
+// heads, 4 queries each, e4m3 50.5 us (5 TB/s: the join of 19 parts of 16 rows takes
 // some 7 us); 1 of 1000 keys, 8 heads, bf16 7.4 us (latency).  With 32 rows the products
-// bound: 2 of 131072 keys, 8 queries each, 4 K/V heads, e4m3 70 us.
+// bound: 2 of up to 131072 keys, 8 queries each, 4 K/V heads, e4m3 76 us (bf16 alike, 7 of up to
+// 3527 keys, 8 heads, 40 rows: 43.6 us, e4m3 43.8).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -127,9 +128,11 @@ __device__ __forceinline__ Layout layout(const AttnProblem& p, bool& fine, bool&
   y.tail = false;
   int places;
   // Of few units the least cut of kTries that gives a wave at most (total / (kCtas - all)
-  // does), if it is not far above a share (64 units of up to 20000 keys, 1.7 shares: 69 us
-  // as the queue's items, 67 as a wave); else parts of shares; or (it does not happen, kPlaces is
-  // enough) no cut at all.
+  // does), if it is not far above a share; else parts of shares; or (it does not happen,
+  // kPlaces is enough) no cut at all.  Measured (128 columns, bf16; us, the queue's items and a
+  // wave): 64 units of up to 20000 keys, 1.1 shares 64.9 and 60.4, 1.3 42.6 and 35.0; 72 units
+  // of up to 60000, 1.9 shares 88.6 and 89.6 or (one more uneven) 120.3 and 119.7.  Nearer than
+  // the rule goes, 1.7 shares, a wave is still ahead (64 units of up to 60000, 84.4 and 71.5).
   constexpr int kTries = 5;
   int attempt = all <= kFewUnits && total > 0 ? 0 : kTries;
 #pragma unroll 1
@@ -909,7 +912,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // keys 6.1 and 4.7, 1000: 8.6 and 7.4, 4000: 9.8 and 9.6, 8000: 12.1 and 13.1; 4 of
 // up to 2000: 10.7 and 9.4; 8 of up to 1024: 11.9 and 9.2; 16 of up to 512: 9.2 and
 // 7.4, 2048: 25.9 and 20.4, 4096: 40.3 and 35.4, but one long request among short ones
-// would wait for its one CTA.
+// would wait for its one CTA.  (Not by type and columns: they were not measured.)
 inline int cluster_ctas(int B, int H_kv, long long max_rows, int max_keys) {
   const int rows = 8 * tiles_of(max_rows);
   const long long units = static_cast<long long>(B) * H_kv * ((max_rows + rows - 1) / rows);
@@ -925,9 +928,16 @@ inline int cluster_ctas(int B, int H_kv, long long max_rows, int max_keys) {
 // 20 requests of up to 120 keys 9.6 and 9.0 / 7.3 / 6.6, 512: 13.0 and 26.6 / 16.0 / 11.6,
 // 1000: 21.5 and - / 27.5 / 19.9, 2000: 28.2 and - / - / 33.3; 40 of 120: 12.7 and 9.3 / 8.1 /
 // 9.7, 512: 19.8 and 26.9 / 19.5 / 22.0, 1000: 27.2 and - / 30.9 / 31.2; 64 of 1000: 36.8 and
-// - / 36.2 / 39.2 (e4m3 27.3 and - / 22.7 / 25.4); 100 of 120: 22.0 and 11.7 / 14.5 / 16.9,
+// - / 36.2 / 39.2; 100 of 120: 22.0 and 11.7 / 14.5 / 16.9,
 // 512: 33.9 and 31.9 / 33.5 / 31.8, 1000: 49.6 and - / 59.6 / 52.5; 300 of 1000: 127 and - /
 // 135 / 129, with 16 rows a unit 152 and - / 145 / 147, 32 rows 246 and - / 205 / 218.
+// e4m3: 20 of 120 9.9 and 7.1 / 6.5 / 6.0, 512: 11.5 and 16.0 / 10.7 / 9.0; 40 of 120 14.2 and
+// 6.6 / 6.4 / 9.1, 512: 16.3 and 15.8 / 11.9 / 13.4; 64 of 1000 28.1 and - / 23.3 / 24.8; 100 of
+// 120 25.2 and 7.9 / 10.6 / 14.3, 512: 30.4 and 21.4 / 22.7 / 23.8; 300 of 1000 with 16 rows 138
+// and - / 120 / 125.  64 columns: 64 of 1000 24.4 and - / 19.8 / 21.6 (e4m3 21.2 and - / 18.0 /
+// 19.7), 40 of 512, 4 rows 13.4 and 14.3 / 10.1 / 11.7; 32 columns: 100 of 512, 4 rows 21.2 and
+// 14.8 / 16.3 / 16.6.  The rule does not go by type, and so takes the slower for 300 of 1000 in
+// e4m3, 8 rows or fewer (93.5 and - / 73.0 / 82.6) and, by 3 %, 32 (236 and - / 244 / 264).
 inline int warps_each(int B, int H_kv, long long max_rows, int max_keys) {
   const long long units = static_cast<long long>(B) * H_kv;
   if (max_rows > 32 || units > 1 << 30 || cluster_ctas(B, H_kv, max_rows, max_keys)) return 0;

@@ -12,11 +12,11 @@
 //
 // Precision.  P is split into two numbers of the cache's 16-bit type, high and low
 // part, for two instructions instead of one: 16 significant bits of bf16, 22 of
-// fp16.  One fp16 number (11 bits) would make O differ from an fp32 P's by 0.05 to
-// 0.1 % (its rounding to bf16 hides that from nothing but sums that nearly cancel);
-// the second costs what the matrix pipe and the conversions have no time left for: e4m3,
-// 128 columns, one and two parts, us: 2 x 131072 keys, 16 rows a head 50.5 / 50.5, 32 rows
-// 64.5 / 75.9; 64 requests of up to 1024, 4 rows 21.1 / 22.5; 300 of up to 512 41.5 / 43.1.
+// fp16.  With one fp16 number (11 bits) outputs in bf16 would differ from an fp32 P's by
+// 4 to 8 in 10^4 of their norm, and sums that nearly cancel by more than bf16's
+// rounding.  The second number's time (e4m3, 128 columns, one / two, us): 2 x
+// 131072 keys, 16 rows a head 50.5 / 50.5, 32 rows 64.5 / 75.9; 64 requests of up to 1024,
+// 4 rows 21.1 / 22.5; 300 of up to 512 41.5 / 43.1.
 // bf16: scores are exact products summed in fp32.  e4m3 is exact in
 // fp16; Q (8 bits) is divided by a power of two per row so that its largest
 // value is in [1, 2), exact in fp16 down to 2^-14 of it (2^-25 absolute below);

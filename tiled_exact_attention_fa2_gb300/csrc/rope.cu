@@ -187,7 +187,9 @@ int launch_rope_rows(RopeProblem p, int d, cudaStream_t st) {
 // 3.1 / 2.3 / 2.1 / 2.8, 16000 57.6 / 51.3 / 49.8 / 50.3; 16000 x 5 heads 7.9 / 7.3 / 8.2
 // / 9.9; 400 x 40 heads x 64 2.0 / 1.9 / 2.2 / 3.0; 16000 x 40 heads x 16 7.4 / 8.6 /
 // 14.3 / 14.9; 13914 x 24 heads x 32 8.0 / 9.3 / 9.6; 92910 x 1 head of q and of k x 128
-// 18.0 / 19.6 / 23.9.
+// 18.0 / 19.6 / 23.9.  Those of 16 and 32 columns are packed rows, whose heads lie side by
+// side; the rule does not look at that, and where they do not it takes the slowest: 6 x
+// 16384 tokens x 40 heads x 16 as [B, H, N, d] 78.6 / 64.3 / 55.3.
 template <bool INTER>
 int launch_rope(const RopeProblem& p, int d, cudaStream_t st) {
   const long long elements = static_cast<long long>(p.tokens) * (p.heads[0] + p.heads[1]) * d;
