@@ -629,6 +629,8 @@ int fa2_kv_gather(const void* k_cache, const void* v_cache, const long long* cac
  * i + Lk - Lq; a query that sees no key gets o = 0 and lse = -inf.  Rows outside
  * every request are not written.  What the pages hold past a request's length, or
  * of keys that a row does not see, has no influence on it, not even a NaN.
+ * Finite values give a finite o, up to bf16's largest; those below 2^-118 times
+ * the request's keys lose bits (products below fp32's normal numbers).
  * max_seqlen_k >= 1 bounds the lengths (table_width * page_size or 2^30 where it
  * is larger).
  * A request whose lengths are out of range (negative, more than max_seqlen_k

@@ -261,7 +261,8 @@ struct Rows {
 
 // A score may pass the maximum by 2^kLag.  e4m3: weights are held 2^11 up (fp16 ones
 // reach 2^15).  bf16: they are held down by 2^kLag and the number of keys, so that
-// their sum is at most 1 and O stays within the largest value of V, whatever that is
+// their sum is at most 1 and O stays within the largest value of V, whatever that is,
+// at the price of bits of values below 2^-118 times the number of keys
 // (7 requests of up to 3527 keys, 40 rows a head, a lag of 2^4 / 2^8: 44.4 / 43.6 us).
 // That number's logarithm lies in shared memory: 32-row kernels have no register for it.
 template <int E>
